@@ -8,11 +8,11 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libcarve.so")
-SOURCES = [os.path.join(PKG, "csrc", "carve_lib.hip")]
+SOURCES = [os.path.join(PKG, "csrc", n) for n in ("carve_lib.hip", "attn_lib.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # packed fp32 instructions stay off for every kernel in this library
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # MFMA accumulators in ordinary VGPRs: the kernels post-process every
@@ -35,13 +35,27 @@ SANITIZE_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitiz
 
 
 def build_library(verbose: bool = True, sanitize: bool = False) -> str:
+    """Compiles the sources side by side, one object each, and links them."""
     out = SANITIZE_LIB if sanitize else LIB
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(SANITIZE_FLAGS if sanitize else []), *SOURCES, "-o", tmp]
+    extra = SANITIZE_FLAGS if sanitize else []
+    objects = [f"{out}.{os.path.basename(src)}.o" for src in SOURCES]
+    cmds = [[HIPCC, *FLAGS, *extra, "-c", src, "-o", obj] for src, obj in zip(SOURCES, objects)]
+    link = [HIPCC, *FLAGS, *extra, "-shared", *objects, "-o", out + ".tmp"]
     if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
+        for cmd in (*cmds, link):
+            print(" ".join(cmd), flush=True)
+    running = [subprocess.Popen(cmd) for cmd in cmds]
+    codes = [p.wait() for p in running]
+    try:
+        for cmd, code in zip(cmds, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.run(link, check=True)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
+    os.replace(out + ".tmp", out)
     return out
 
 

@@ -5,9 +5,9 @@
 
 #include <atomic>
 #include <cstdio>
-#include <cstring>
 
 #include "carve.h"
+#include "host.h"
 #include "kernels/kernels.h"
 #include "kernels/bwd.h"
 #include "kernels/bwd_chunk.h"
@@ -15,9 +15,13 @@
 
 namespace {
 
-thread_local char g_hip_msg[256] = "no HIP error recorded";
+using carve_host::elem_bytes;
+using carve_host::kMaxDevices;
+using carve_host::misaligned;
+using carve_host::overlaps;
+using carve_host::set_lds;
 
-size_t elem_bytes(int dtype) { return dtype == CARVE_F32 ? 4 : 2; }
+thread_local char g_hip_msg[256] = "no HIP error recorded";
 
 bool valid_width(int d) { return d == 64 || d == 128; }
 bool valid_chunk(int L) { return L == 16 || L == 32 || L == 64 || L == 128; }
@@ -41,14 +45,6 @@ int check_config(const carve_config* c) {
   if ((int64_t)64 * c->H * (c->dk > c->dv ? c->dk : c->dv) * elem_bytes(c->dtype) > 0xffffffffLL)
     return CARVE_EUNSUPPORTED;
   return CARVE_OK;
-}
-
-bool misaligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
 }
 
 // block length used by the chunk-serial kernel: divides L, fits LDS
@@ -105,30 +101,6 @@ BwdBytes bwd_bytes(const carve_config* c) {
   const int64_t img = (own + 255) & ~(int64_t)255;
   const int64_t o = img + parallel_workspace_bytes(c);
   return {img, o, o + B * T * H * c->dv * (int64_t)sizeof(carve::bf16)};
-}
-
-// Raises kernel Kern's dynamic-LDS limit to `bytes`. The attribute only ever
-// needs raising, so the largest value set so far is kept per kernel (one
-// instantiation of this function per kernel) and device, and the driver is
-// called only to go beyond it: later calls (and launches inside a graph
-// capture) make no attribute call at all.
-constexpr int kMaxDevices = 64;
-template <auto Kern>
-hipError_t set_lds(int bytes) {
-  static std::atomic<int> set_bytes[kMaxDevices];
-  auto raise = [&] {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(Kern),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return raise();
-  int cur = set_bytes[dev].load(std::memory_order_acquire);
-  if (cur >= bytes) return hipSuccess;
-  const hipError_t e = raise();
-  if (e != hipSuccess) return e;
-  while (cur < bytes && !set_bytes[dev].compare_exchange_weak(cur, bytes, std::memory_order_acq_rel)) {
-  }
-  return hipSuccess;
 }
 
 template <typename E, int D, int BL, bool LG, bool NRM>
@@ -378,6 +350,11 @@ hipError_t launch_step(const carve::StepArgs& a, hipStream_t s) {
 
 }  // namespace
 
+int carve_host::hip_failed(hipError_t e) {
+  std::snprintf(g_hip_msg, sizeof(g_hip_msg), "%s", hipGetErrorString(e));
+  return CARVE_EHIP;
+}
+
 extern "C" int carve_recurrent_ref_shapes(const carve_config* cfg, carve_shapes* out) {
   const int st = check_config(cfg);
   if (st != CARVE_OK) return st;
@@ -444,10 +421,7 @@ int fwd_launch(const carve_config* cfg, const void* q, const void* k, const void
   a.ckpt = nullptr; a.ckpt_bh = 0; a.ckpt_shift = 0;
 
   const hipError_t e = dispatch_fwd_flags(cfg, a, reinterpret_cast<hipStream_t>(stream));
-  if (e != hipSuccess) {
-    std::snprintf(g_hip_msg, sizeof(g_hip_msg), "%s", hipGetErrorString(e));
-    return CARVE_EHIP;
-  }
+  if (e != hipSuccess) return carve_host::hip_failed(e);
   return CARVE_OK;
 }
 
@@ -511,10 +485,7 @@ extern "C" int carve_chunk_fwd_noalloc(const carve_config* cfg,
   void* ws = nullptr;
   if (sh.workspace_bytes > 0) {
     const hipError_t e = noalloc_scratch_ptr(&ws);
-    if (e != hipSuccess) {
-      std::snprintf(g_hip_msg, sizeof(g_hip_msg), "%s", hipGetErrorString(e));
-      return CARVE_EHIP;
-    }
+    if (e != hipSuccess) return carve_host::hip_failed(e);
   }
   return fwd_launch(cfg, q, k, v, g, bx, w, ub_down, ub_up, state_in, mean_in, o, state_out, mean_out, ws, stream);
 }
@@ -646,10 +617,7 @@ extern "C" int carve_chunk_bwd(const carve_config* cfg,
     e = cfg->dtype == CARVE_BF16
             ? (lg ? dispatch_bwd_width<carve::bf16, true>(cfg, a, s) : dispatch_bwd_width<carve::bf16, false>(cfg, a, s))
             : (lg ? dispatch_bwd_width<float, true>(cfg, a, s) : dispatch_bwd_width<float, false>(cfg, a, s));
-  if (e != hipSuccess) {
-    std::snprintf(g_hip_msg, sizeof(g_hip_msg), "%s", hipGetErrorString(e));
-    return CARVE_EHIP;
-  }
+  if (e != hipSuccess) return carve_host::hip_failed(e);
   return CARVE_OK;
 }
 
@@ -701,10 +669,7 @@ extern "C" int carve_recurrent_step(const carve_config* cfg, int32_t pos,
     e = cfg->dk == 64 ? launch_step<carve::bf16, 64>(a, s) : launch_step<carve::bf16, 128>(a, s);
   else
     e = cfg->dk == 64 ? launch_step<float, 64>(a, s) : launch_step<float, 128>(a, s);
-  if (e != hipSuccess) {
-    std::snprintf(g_hip_msg, sizeof(g_hip_msg), "%s", hipGetErrorString(e));
-    return CARVE_EHIP;
-  }
+  if (e != hipSuccess) return carve_host::hip_failed(e);
   return CARVE_OK;
 }
 
@@ -712,9 +677,9 @@ extern "C" const char* carve_error_string(int code) {
   switch (code) {
     case CARVE_OK: return "ok";
     case CARVE_EINVAL: return "invalid argument (NULL required pointer, negative size, unknown flag or overlapping output)";
-    case CARVE_EUNSUPPORTED: return "unsupported configuration (dk/dv in {64,128} with dk == dv, L in {16,32,64,128}, rank <= 64, sizes within 32-bit indexing)";
-    case CARVE_EALIGN: return "a tensor pointer is not 16-byte aligned";
-    case CARVE_EWORKSPACE: return "workspace smaller than carve_recurrent_ref_shapes() requires (for carve_chunk_fwd_noalloc: the problem needs more workspace than its fixed 64 MiB scratch)";
+    case CARVE_EUNSUPPORTED: return "unsupported configuration (dk/dv in {64,128} with dk == dv, L in {16,32,64,128}, rank <= 64, sizes within 32-bit indexing; attention layer: d in {64,128}, rot a multiple of 16 up to d, page_size a power of two, 0 < scale <= 16)";
+    case CARVE_EALIGN: return "a tensor pointer or stride is not 16-byte aligned";
+    case CARVE_EWORKSPACE: return "workspace smaller than the entry point's size function requires (for carve_chunk_fwd_noalloc: the problem needs more workspace than its fixed 64 MiB scratch)";
     case CARVE_EHIP: return g_hip_msg;
     default: return "unknown status code";
   }

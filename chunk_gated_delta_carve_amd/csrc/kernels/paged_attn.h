@@ -1,0 +1,705 @@
+// Attention of new tokens over a paged cache.
+//
+// Sequence s has kv tokens, the last n of them new. New token i stands at
+// p = kv - n + i and sees the keys j in (p - window, p] (all j <= p without a
+// window). Query head h reads key/value head h / G, G = Hq / Hk, so the rows of
+// one key/value head are the (token, head in group) pairs r = i G + g, and a
+// tile of rows shares every key and value it loads.
+//
+//   o_r = sum_j e^{c (x_rj - m)} v_j / l,  l = sum_j e^{c (x_rj - m)},  x_rj = q_r . k_j
+//
+// in one pass over the keys: m is a running reference near the row maximum (in
+// fp32, as l and o are), and the exponentials are powers of two with
+// c = scale log2 e. Products run transposed, X^T = K Q^T and O^T = V^T P^T: a
+// lane then owns one row (a column of the C tile), its maximum needs one or two
+// cross-lane steps, rescaling is lane-local, and P^T leaves the first product
+// in the very registers the second one wants as its B operand. Its only loss is
+// P rounded to the input type (bf16: half a step is 2^-9 of each weight; l sums
+// the unrounded ones).
+//
+// Masked keys never reach a row: their scores are replaced before use, pages
+// outside the cache and keys no row of the tile may see are loaded as zeros,
+// and a row whose result is not finite is computed again over its visible keys
+// alone (careful_row), since 0 x inf inside a product that other rows need
+// would have put a NaN there.
+//
+// Long contexts are split over `splits` workgroups per tile, each leaving
+// (o, m, l) in fp32; paged_combine_kernel joins them in a fixed order. Every
+// tile works out from its own key range how many of them it needs, so no length
+// is read on the host and a captured graph follows the lengths on the device.
+#pragma once
+#include "common.h"
+#include "rope.h"
+
+namespace carve {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+struct PagedArgs {
+  const void *q, *kc, *vc;
+  const int *cu, *kv_lens, *table;
+  void* o;
+  float* lse;                                       // [N][Hq] or NULL
+  float *po, *pml;                                  // partials: [splits][N Hq][D], [splits][N Hq][2]
+  int64_t q_row, o_row, table_row;
+  int64_t kc_page, kc_tok, kc_head, vc_page, vc_tok, vc_head;
+  int N, S, Hq, Hk, G, width, pages, page_shift, window, splits, tiles;
+  float scale, c;                                   // c = scale log2 e
+};
+
+constexpr float kNoMax = -1e37f;                    // below every score that counts; c kNoMax stays finite (c < 24)
+
+// The tile `t` of BM rows: its sequence, its rows and the keys they see.
+struct AttnTile {
+  int n0;                                           // the sequence's first token
+  int row0, rows;                                   // first row in the sequence, rows in the tile (0: nothing to do)
+  int s, pos0;                                      // sequence, position of its first new token
+  int lo, hi;                                       // keys some row may see
+};
+
+// Tiles are numbered without knowing the lengths: sequence s starts at tile
+// floor(cu[s] G / BM) + s, which leaves room for its ceil(n G / BM) tiles.
+__device__ __forceinline__ AttnTile tile_of_rows(const PagedArgs& a, int s, int n0, int cnt, int row0, int BM) {
+  AttnTile x;
+  x.s = s; x.n0 = n0; x.row0 = row0;
+  const int all = cnt * a.G;
+  x.rows = all - row0 < BM ? all - row0 : BM;
+  const int kv = a.kv_lens[s];
+  x.pos0 = (kv > 0 ? kv : 0) - cnt;
+  const int64_t cap = (int64_t)a.width << a.page_shift;
+  const int64_t first = (int64_t)x.pos0 + row0 / a.G, last = (int64_t)x.pos0 + (row0 + x.rows - 1) / a.G;
+  const int64_t hi = last + 1 < cap ? last + 1 : cap;
+  const int64_t lo = a.window > 0 && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
+  x.hi = hi > 0 ? (int)hi : 0;
+  x.lo = lo < x.hi ? (int)lo : x.hi;
+  return x;
+}
+
+__device__ __forceinline__ AttnTile find_tile(const PagedArgs& a, int t, int BM) {
+  AttnTile none;
+  none.rows = 0;
+  if (!a.cu) {
+    const int per = (a.G + BM - 1) / BM, s = t / per;
+    if (s >= a.S || s >= a.N) return none;
+    return tile_of_rows(a, s, s, 1, (t - s * per) * BM, BM);
+  }
+  int lo = 0, len = a.S;                            // as find_sequence, over the tiles' starts
+  while (len > 0) {
+    const int step = (len + 63) >> 6, at = (lane_id() + 1) * step;
+    const bool past = at <= len && (int64_t)a.cu[lo + at] * a.G / BM + lo + at <= t;
+    const int k = __popcll(__ballot(past));
+    lo += k * step;
+    len = step - 1 < len - k * step ? step - 1 : len - k * step;
+  }
+  if (lo >= a.S) return none;
+  const int n0 = a.cu[lo];
+  int n1 = a.cu[lo + 1];
+  n1 = n1 < a.N ? n1 : a.N;
+  if (n0 < 0 || n1 <= n0) return none;
+  const int64_t row0 = (t - ((int64_t)n0 * a.G / BM + lo)) * BM;
+  if (row0 < 0 || row0 >= (int64_t)(n1 - n0) * a.G) return none;
+  return tile_of_rows(a, lo, n0, n1 - n0, (int)row0, BM);
+}
+
+// The keys [lo, hi) in blocks of BN (aligned), dealt to at most `splits`
+// workgroups, at least `least` blocks each.
+struct Share { int b0, per, count; };
+__device__ __forceinline__ Share share_of(int lo, int hi, int BN, int splits, int least) {
+  Share x;
+  x.b0 = lo / BN;
+  const int nb = hi > lo ? (hi + BN - 1) / BN - x.b0 : 0;
+  x.per = (nb + splits - 1) / splits;
+  x.per = x.per > least ? x.per : least;
+  x.count = (nb + x.per - 1) / x.per;
+  return x;
+}
+
+__device__ __forceinline__ int page_of(const PagedArgs& a, int s, int j) {   // page number or -1
+  const int slot = j >> a.page_shift;
+  if (j < 0 || slot >= a.width) return -1;
+  const int id = a.table[s * a.table_row + slot];
+  return id >= 0 && id < a.pages ? id : -1;
+}
+
+// Where a row's results go: the output itself when the tile has one share.
+template <typename E, int D>
+struct RowOut {
+  const PagedArgs& a;
+  int sp;
+  bool whole;
+  int h;
+  __device__ __forceinline__ int64_t index(const AttnTile& x, int r) const {     // n Hq + query head
+    const int row = x.row0 + r;
+    return (int64_t)(x.n0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  }
+  __device__ __forceinline__ E* out(int64_t at) const {
+    return static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D;
+  }
+  __device__ __forceinline__ float* part(int64_t at) const {
+    return a.po + ((int64_t)sp * a.N * a.Hq + at) * D;
+  }
+  __device__ __forceinline__ void stats(int64_t at, float m, float l) const {    // one lane per row
+    if (whole) {
+      if (a.lse) a.lse[at] = l == 0.f ? -__builtin_inff() : (m * a.c + fast_log2(l)) * 0.6931471805599453f;
+    } else {
+      float* p = a.pml + ((int64_t)sp * a.N * a.Hq + at) * 2;
+      p[0] = m; p[1] = l;
+    }
+  }
+};
+
+// One row over keys [k0, k1) by a whole wave, key by key and without products
+// that other rows share: lanes score 64 keys at once, then add their values.
+template <typename E, int D>
+__device__ __noinline__ void careful_row(const PagedArgs& a, const AttnTile& x, int h, int r, int k0, int k1, int sp,
+                                         bool whole) {
+  constexpr int V = Piece<E>::V, PER = D / 64;
+  const RowOut<E, D> ro{a, sp, whole, h};
+  const int64_t at = ro.index(x, r);
+  const int p = x.pos0 + (x.row0 + r) / a.G, lane = lane_id();
+  const E* q = static_cast<const E*>(a.q) + at / a.Hq * a.q_row + at % a.Hq * D;
+  const E* kc = static_cast<const E*>(a.kc) + h * a.kc_head;
+  const E* vc = static_cast<const E*>(a.vc) + h * a.vc_head;
+  const int first = a.window > 0 && p - a.window + 1 > k0 ? p - a.window + 1 : k0, end = p + 1 < k1 ? p + 1 : k1;
+  float m = kNoMax, l = 0.f, o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  for (int j0 = first; j0 < end; j0 += 64) {
+    const int j = j0 + lane, id = j < end ? page_of(a, x.s, j) : -1;
+    const int64_t off = j & ((1 << a.page_shift) - 1);
+    float s = -__builtin_inff();
+    if (id >= 0) {
+      const E* k = kc + id * a.kc_page + off * a.kc_tok;
+      s = 0.f;
+      for (int i = 0; i < D; i += V) {
+        float kx[V], qx[V];
+        Piece<E>::open(*reinterpret_cast<const u32x4*>(k + i), kx);
+        Piece<E>::open(*reinterpret_cast<const u32x4*>(q + i), qx);
+#pragma unroll
+        for (int u = 0; u < V; ++u) s += kx[u] * qx[u];
+      }
+    }
+    if (__ballot(s != s)) {                         // a visible score is NaN: so is the row
+      l = __builtin_nanf("");
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = l;
+      break;
+    }
+    float top = s;
+#pragma unroll
+    for (int w = 1; w < 64; w <<= 1) top = fmaxf(top, __shfl_xor(top, w));
+    const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
+    const float e = fast_exp2((s - mn) * a.c);      // +inf - +inf: NaN, as the formula has it
+    m = mn;
+    l = l * al + wave_sum(e);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] *= al;
+    for (int u = 0; u < 64; ++u) {
+      const int uid = __shfl(id, u);
+      if (uid < 0) continue;
+      const float w = __shfl(e, u);
+      const E* v = vc + uid * a.vc_page + ((j0 + u) & ((1 << a.page_shift) - 1)) * a.vc_tok + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] += w * to_f32(v[i]);
+    }
+  }
+  if (whole) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ro.out(at)[lane * PER + i] = from_f32<E>(o[i] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ro.part(at)[lane * PER + i] = o[i];
+  }
+  if (lane == 0) ro.stats(at, m, l);
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// ---------------------------------------------------------------------------
+// Few rows: 16 rows per workgroup, whose four waves take alternate blocks of 32
+// keys and are joined at the end. Keys go from memory straight into operand
+// registers (a 16-byte piece of a key's row is one operand), values through a
+// wave's own LDS to be transposed (ds_read_b64_tr_b16 hands a lane four keys
+// of one channel), so there is no barrier in the loop. Bound by reading the
+// cache: per 32 keys of 256 bytes a wave spends 16 + 16 matrix instructions of
+// 16 cycles, a tenth of the time its share of HBM needs to deliver them.
+template <typename E, int D>
+struct RowsLayout {
+  static constexpr int BM = 16, KT = 32, BN = 128, LEAST = 1;                    // BN: keys per round of four waves
+  static constexpr int NP = D * (int)sizeof(E) / 64;                             // pieces per lane and key
+  static constexpr int VLD = D * (int)sizeof(E) + (sizeof(E) == 2 ? 32 : 16);    // bytes per value row: spread banks
+  static constexpr int OLD = D + 4;                                              // floats per row of a wave's result
+  static constexpr int v_bytes = 4 * KT * VLD, o_bytes = 4 * BM * OLD * 4;
+  static constexpr int bytes = v_bytes > o_bytes ? v_bytes : o_bytes;
+};
+
+template <typename E>
+__device__ __forceinline__ f32x4 mma_piece(u32x4 k, u32x4 q, f32x4 acc) {
+  if constexpr (sizeof(E) == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), acc, 0,
+                                                   0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[i]), __uint_as_float(q[i]), acc, 0, 0, 0);
+    return acc;
+  }
+}
+
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+__device__ __forceinline__ s16x4 read_tr(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
+  using LY = RowsLayout<E, D>;
+  constexpr int NP = LY::NP, KT = LY::KT;
+  __shared__ __align__(16) char lds[LY::bytes];
+  __shared__ float ms[4][16], ls[4][16];
+  __shared__ int bad[16];
+  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest % a.splits;
+  const AttnTile x = find_tile(a, rest / a.splits, LY::BM);
+  if (x.rows <= 0) return;
+  const Share sh = share_of(x.lo, x.hi, LY::BN, a.splits, LY::LEAST);
+  if (sp > 0 && sp >= sh.count) return;
+  const bool whole = sh.count <= 1;
+  const int k0 = (sh.b0 + sp * sh.per) * LY::BN < x.lo ? x.lo : (sh.b0 + sp * sh.per) * LY::BN;
+  const int64_t k1_ = (int64_t)(sh.b0 + (sp + 1) * sh.per) * LY::BN;
+  const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
+  const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
+
+  // this lane's row and its queries, in the pieces the keys come in
+  const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
+  const int p = x.pos0 + row / a.G;
+  const int p_min = x.pos0 + x.row0 / a.G, p_max = x.pos0 + (x.row0 + x.rows - 1) / a.G;
+  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
+  u32x4 q[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) q[i] = reinterpret_cast<const u32x4*>(qp)[4 * i + g];
+
+  const char* kb = reinterpret_cast<const char*>(static_cast<const E*>(a.kc) + h * a.kc_head) + 16 * g;
+  const char* vb = reinterpret_cast<const char*>(static_cast<const E*>(a.vc) + h * a.vc_head) + 16 * g;
+  const int pmask = (1 << a.page_shift) - 1;
+  char* vl = lds + wave * KT * LY::VLD;
+
+  f32x4 o[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i] = zero4();
+  float m = kNoMax, l = 0.f;
+
+  // a lane looks up the pages of its two keys (c and 16 + c of the block)
+  auto lookup = [&](int j0, int (&id)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j = j0 + 16 * b + c;
+      id[b] = j >= k0 && j < k1 ? page_of(a, x.s, j) : -1;
+    }
+  };
+  u32x4 kr[2][NP], vr[2][NP];
+  unsigned long long okn = 0;                       // which of the 32 keys exist (bit = key)
+  auto fetch = [&](int j0, const int (&id)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int64_t pg = id[b] < 0 ? 0 : id[b], off = (j0 + 16 * b + c) & pmask;
+      const char* kp = kb + (pg * a.kc_page + off * a.kc_tok) * (int64_t)sizeof(E);
+      const char* vp = vb + (pg * a.vc_page + off * a.vc_tok) * (int64_t)sizeof(E);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kr[b][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) vr[b][i] = *reinterpret_cast<const u32x4*>(vp + 64 * i);
+    }
+    okn = (__ballot(id[0] >= 0) & 0xffffu) | ((__ballot(id[1] >= 0) & 0xffffu) << 16);
+  };
+  constexpr int STEP = 4 * KT;
+  int j0 = (k0 / LY::BN) * LY::BN + wave * KT;
+  int id[2];
+  if (j0 < k1) {
+    lookup(j0, id);
+    fetch(j0, id);
+    lookup(j0 + STEP, id);
+  }
+  for (; j0 < k1; j0 += STEP) {
+    const unsigned ok = (unsigned)okn;
+    f32x4 s[2] = {zero4(), zero4()};
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s[b] = mma_piece<E>(kr[b][i], q[i], s[b]);
+    // values to LDS; rows that do not exist as zeros
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bool z = ok != 0xffffffffu && !((ok >> (16 * b + c)) & 1u);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (z) vr[b][i] = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(vl + (16 * b + c) * LY::VLD + 64 * i + 16 * g) = vr[b][i];
+      }
+    }
+    if (j0 + STEP < k1) {
+      fetch(j0 + STEP, id);
+      lookup(j0 + 2 * STEP, id);
+    }
+    // lane: row c, keys 16 b + 4 g + i
+    if (ok != 0xffffffffu || j0 + KT - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 16 * b + 4 * g + i, j = j0 + kk;
+          const bool see = ((ok >> kk) & 1u) && j <= p && (a.window <= 0 || j > p - a.window);
+          s[b][i] = see ? s[b][i] : -__builtin_inff();
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__ballot(top > m)) {
+      const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i] *= al;
+    }
+    const float mc = m * a.c;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[b][i] = fast_exp2(s[b][i] * a.c - mc);
+        l += s[b][i];
+      }
+    if constexpr (sizeof(E) == 2) {
+      const bf16x8 pb = Mma<bf16>::pack(s);
+      const char* src = vl + (4 * g + (lane & 15) / 4) * LY::VLD + (lane & 3) * 8;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        const s16x4 v0 = read_tr(src + 32 * d), v1 = read_tr(src + 32 * d + 16 * LY::VLD);
+        const bf16x4 b0 = __builtin_bit_cast(bf16x4, v0), b1 = __builtin_bit_cast(bf16x4, v1);
+        o[d] = Mma<bf16>::mma(bf16x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]}, pb, o[d]);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const float v = *reinterpret_cast<const float*>(vl + (16 * b + 4 * g + i) * LY::VLD + (16 * d + c) * 4);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, s[b][i], o[d], 0, 0, 0);
+          }
+    }
+  }
+
+  // join the four waves
+  l = sum_groups(l);
+  if (threadIdx.x < 16) bad[threadIdx.x] = 0;
+  if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }
+  __syncthreads();
+  float* ol = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+    *reinterpret_cast<f32x4*>(ol + (wave * 16 + c) * LY::OLD + 16 * d + 4 * g) = o[d];
+  __syncthreads();
+  const int r = threadIdx.x >> 4, t = threadIdx.x & 15;
+  const RowOut<E, D> ro{a, sp, whole, h};
+  if (r < x.rows) {
+    float M = ms[0][r], L = 0.f, acc[D / 16];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) M = fmaxf(M, ms[w][r]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = fast_exp2((ms[w][r] - M) * a.c);
+      L += ls[w][r] * f;
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(ol + (w * 16 + r) * LY::OLD + t * (D / 16) + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[i + u] += v[u] * f;
+      }
+    }
+    const int64_t at = ro.index(x, r);
+    bool nf = not_finite(L);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
+    if (nf) bad[r] = 1;
+    if (whole) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      E* out = ro.out(at) + t * (D / 16);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) out[i] = from_f32<E>(acc[i] * inv);
+    } else {
+      f32x4* out = reinterpret_cast<f32x4*>(ro.part(at) + t * (D / 16));
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4) out[i / 4] = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    }
+    if (t == 0) ro.stats(at, M, L);
+  }
+  __syncthreads();
+  for (int i = wave; i < x.rows; i += 4)
+    if (bad[i]) careful_row<E, D>(a, x, h, i, k0, k1, sp, whole);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (bf16): 32 rows per wave, keys and values shared by the workgroup
+// through LDS in blocks of 64, loaded into registers one block ahead and
+// written to the buffer that the last block left.
+template <int D, int NW>
+struct TileLayout {
+  static constexpr int BM = 32 * NW, BN = 64, NT = 64 * NW, LEAST = 4;
+  static constexpr int KLD = 2 * D + 16, VLD = 2 * D + 32;   // bytes per row: row starts walk over the banks
+  static constexpr int buf = BN * (KLD + VLD), bytes = 2 * buf;
+  static constexpr int CPR = D / 8;                          // 16-byte chunks per row
+  static constexpr int ST = BN * CPR / NT;                   // chunks per thread and tensor
+  static constexpr int RS = NT / CPR;                        // rows between a thread's chunks
+};
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
+  using E = bf16;
+  using LY = TileLayout<D, NW>;
+  extern __shared__ __align__(16) char lds[];
+  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest % a.splits;
+  // the last tiles of a sequence see the most keys: start with them
+  const AttnTile x = find_tile(a, a.tiles - 1 - rest / a.splits, LY::BM);
+  if (x.rows <= 0) return;
+  const Share sh = share_of(x.lo, x.hi, LY::BN, a.splits, LY::LEAST);
+  if (sp > 0 && sp >= sh.count) return;
+  const bool whole = sh.count <= 1;
+  const int lane = lane_id(), wave = wave_id(), c = lane & 31, hf = lane >> 5;
+  const int first_b = sh.b0 + sp * sh.per;
+  int last_b = first_b + sh.per;
+  { const int all = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN : sh.b0; last_b = last_b < all ? last_b : all; }
+
+  // the wave's rows; rows past the tile's end repeat the last one and are not stored
+  const int wr0 = wave * 32 < x.rows ? wave * 32 : x.rows - 1;
+  const int wr1 = wave * 32 + 31 < x.rows ? wave * 32 + 31 : x.rows - 1;
+  const int row = x.row0 + (wave * 32 + c < x.rows ? wave * 32 + c : x.rows - 1);
+  const int p = x.pos0 + row / a.G;
+  const int p_min = x.pos0 + (x.row0 + wr0) / a.G, p_max = x.pos0 + (x.row0 + wr1) / a.G;
+  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
+  bf16x8 q[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
+
+  const int pmask = (1 << a.page_shift) - 1;
+  const int sr = threadIdx.x / LY::CPR, sc = threadIdx.x % LY::CPR;
+  const E* kb = static_cast<const E*>(a.kc) + h * a.kc_head + sc * 8;
+  const E* vb = static_cast<const E*>(a.vc) + h * a.vc_head + sc * 8;
+
+  // lane l of every wave looks up key l of a block
+  auto lookup = [&](int b) {
+    const int j = b * LY::BN + lane;
+    return b < last_b && j >= x.lo && j < x.hi ? page_of(a, x.s, j) : -1;
+  };
+  u32x4 kr[LY::ST], vr[LY::ST];
+  auto fetch = [&](int b, int id) {
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) {
+      const int r = sr + LY::RS * i, rid = __shfl(id, r);
+      const int64_t pg = rid < 0 ? 0 : rid, off = (b * LY::BN + r) & pmask;
+      kr[i] = *reinterpret_cast<const u32x4*>(kb + pg * a.kc_page + off * a.kc_tok);
+      vr[i] = *reinterpret_cast<const u32x4*>(vb + pg * a.vc_page + off * a.vc_tok);
+    }
+  };
+  auto store = [&](int buf, unsigned long long ok) {
+    char* kl = lds + buf * LY::buf;
+    char* vl = kl + LY::BN * LY::KLD;
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) {
+      const int r = sr + LY::RS * i;
+      if (ok != ~0ull && !((ok >> r) & 1ull)) kr[i] = vr[i] = u32x4{0, 0, 0, 0};
+      *reinterpret_cast<u32x4*>(kl + r * LY::KLD + sc * 16) = kr[i];
+      *reinterpret_cast<u32x4*>(vl + r * LY::VLD + sc * 16) = vr[i];
+    }
+  };
+
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int u = 0; u < 16; ++u) o[i][u] = 0.f;
+  float m = kNoMax, l = 0.f;
+
+  unsigned long long ok = 0;
+  int idn = -1;                                     // pages of the block after the one in registers
+  if (first_b < last_b) {
+    const int id0 = lookup(first_b);
+    ok = __ballot(id0 >= 0);
+    fetch(first_b, id0);
+    idn = lookup(first_b + 1);
+    store(0, ok);
+  }
+  for (int b = first_b; b < last_b; ++b) {
+    const int buf = (b - first_b) & 1;
+    __syncthreads();                                // block b is in LDS; nobody reads the other buffer any more
+    const unsigned long long okn = __ballot(idn >= 0);
+    if (b + 1 < last_b) {
+      fetch(b + 1, idn);
+      idn = lookup(b + 2);
+    }
+    const int j0 = b * LY::BN;
+    if (j0 <= p_max && (a.window <= 0 || j0 + LY::BN - 1 > p_min - a.window)) {
+      const char* kl = lds + buf * LY::buf;
+      const char* vl = kl + LY::BN * LY::KLD;
+      f32x16 s[2];
+#pragma unroll
+      for (int kb2 = 0; kb2 < 2; ++kb2) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s[kb2][u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const bf16x8 k = *reinterpret_cast<const bf16x8*>(kl + (32 * kb2 + c) * LY::KLD + 32 * i + 16 * hf);
+          s[kb2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[kb2], 0, 0, 0);
+        }
+      }
+      // lane: row c, keys 32 kb2 + 8 (u / 4) + 4 hf + u % 4
+      if (ok != ~0ull || j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+        const unsigned long long mine = ok >> (4 * hf);
+        const int far = p - j0 - 4 * hf, near = a.window > 0 ? far - a.window : -1000000;   // visible: near < key <= far
+#pragma unroll
+        for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const int kk = 32 * kb2 + 8 * (u / 4) + u % 4;
+            const bool see = ((mine >> kk) & 1ull) && kk <= far && kk > near;
+            s[kb2][u] = see ? s[kb2][u] : -__builtin_inff();
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) top = fmaxf(top, s[kb2][u]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__ballot(top > m)) {
+        const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
+        m = mn;
+        l *= al;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o[i][u] *= al;
+      }
+      const float mc = m * a.c;
+      bf16x8 pb[4];
+#pragma unroll
+      for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const float e = fast_exp2(s[kb2][u] * a.c - mc);
+          l += e;
+          pb[2 * kb2 + u / 8][u % 8] = (bf16)e;
+        }
+      const char* src = vl + (4 * hf + (lane & 15) / 4) * LY::VLD + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          const s16x4 v0 = read_tr(src + 16 * ks * LY::VLD + 64 * d);
+          const s16x4 v1 = read_tr(src + (16 * ks + 8) * LY::VLD + 64 * d);
+          const bf16x4 b0 = __builtin_bit_cast(bf16x4, v0), b1 = __builtin_bit_cast(bf16x4, v1);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              bf16x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]}, pb[ks], o[d], 0, 0, 0);
+        }
+    }
+    if (b + 1 < last_b) store(buf ^ 1, okn);
+    ok = okn;
+  }
+
+  l += __shfl_xor(l, 32);
+  const RowOut<E, D> ro{a, sp, whole, h};
+  const int r = wave * 32 + c;
+  bool nf = false;
+  if (r < x.rows) {
+    const int64_t at = ro.index(x, r);
+    nf = not_finite(l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int u = 0; u < 16; ++u) nf = nf || not_finite(o[i][u]);
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      E* out = ro.out(at) + 4 * hf;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int u = 0; u < 16; u += 4)
+          *reinterpret_cast<bf16x4*>(out + 32 * i + 2 * u) =
+              bf16x4{(bf16)(o[i][u] * inv), (bf16)(o[i][u + 1] * inv), (bf16)(o[i][u + 2] * inv),
+                     (bf16)(o[i][u + 3] * inv)};
+    } else {
+      float* out = ro.part(at) + 4 * hf;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int u = 0; u < 16; u += 4)
+          *reinterpret_cast<f32x4*>(out + 32 * i + 2 * u) = f32x4{o[i][u], o[i][u + 1], o[i][u + 2], o[i][u + 3]};
+    }
+    if (hf == 0) ro.stats(at, m, l);
+  }
+  unsigned long long again = __ballot(nf);
+  again = (again | again >> 32) & 0xffffffffull;
+  const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
+  const int64_t k1_ = (int64_t)last_b * LY::BN;
+  const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
+  while (again) {
+    const int i = __ffsll((unsigned long long)again) - 1;
+    again &= again - 1;
+    careful_row<E, D>(a, x, h, wave * 32 + i, k0, k1, sp, whole);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins a tile's shares: one wave per (token, query head).
+template <typename E, int D, int BM, int BN, int LEAST>
+__global__ __launch_bounds__(256) void paged_combine_kernel(PagedArgs a) {
+  constexpr int PER = D / 64;
+  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
+  if (at >= (int64_t)a.N * a.Hq) return;
+  const int n = (int)(at / a.Hq), hq = (int)(at % a.Hq);
+  int s = n, i = 0, cnt = 1, n0 = n;
+  if (a.cu) {
+    s = find_sequence(a.cu, a.S, n);
+    if (s >= a.S) return;
+    n0 = a.cu[s];
+    int n1 = a.cu[s + 1];
+    n1 = n1 < a.N ? n1 : a.N;
+    i = n - n0; cnt = n1 - n0;
+    if (n0 < 0 || i < 0 || i >= cnt) return;
+  } else if (s >= a.S) return;
+  const int row = i * a.G + hq % a.G;
+  const AttnTile x = tile_of_rows(a, s, n0, cnt, row / BM * BM, BM);
+  const Share sh = share_of(x.lo, x.hi, BN, a.splits, LEAST);
+  if (sh.count <= 1) return;
+  const int lane = lane_id();
+  const int64_t stride = (int64_t)a.N * a.Hq;
+  float M = kNoMax;
+  for (int sp = 0; sp < sh.count; ++sp) M = fmaxf(M, a.pml[(sp * stride + at) * 2]);
+  float L = 0.f, o[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) o[u] = 0.f;
+  for (int sp = 0; sp < sh.count; ++sp) {
+    const float* ml = a.pml + (sp * stride + at) * 2;
+    const float f = fast_exp2((ml[0] - M) * a.c);
+    L += ml[1] * f;
+    const float* po = a.po + (sp * stride + at) * D + lane * PER;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) o[u] += po[u] * f;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  E* out = static_cast<E*>(a.o) + n * a.o_row + hq * D + lane * PER;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) out[u] = from_f32<E>(o[u] * inv);
+  if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+}
+
+}  // namespace carve

@@ -53,8 +53,8 @@ typedef enum {
   CARVE_EINVAL = 1,        /* NULL required pointer, negative size, unknown flag bit */
   CARVE_EUNSUPPORTED = 2,  /* d_k/d_v not in {64,128}, L not in {16,32,64,128}, d_k != d_v,
                               rank > 64, or a size past the kernels' 32-bit index range */
-  CARVE_EALIGN = 3,        /* a pointer is not 16-byte aligned */
-  CARVE_EWORKSPACE = 4,    /* workspace smaller than carve_recurrent_ref_shapes() asks */
+  CARVE_EALIGN = 3,        /* a pointer (or, where there are strides, a stride) is not 16-byte aligned */
+  CARVE_EWORKSPACE = 4,    /* workspace smaller than the entry point's size function asks */
   CARVE_EHIP = 5           /* a HIP launch failed; carve_error_string(CARVE_EHIP) has the text */
 } carve_status;
 
@@ -247,6 +247,123 @@ int carve_recurrent_step(const carve_config* cfg, int32_t pos,
                          const void* ub_down, const void* ub_up,
                          float* state, float* mean_prev, float* chunk_acc,
                          void* o, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention layer beside the mixer. The paper's hybrid model puts
+ * sliding-window attention layers between CARVE layers; these entry points are
+ * that layer's operators: the norm and rotation of queries and keys with their
+ * gradients, a paged cache of keys and values, and attention of new tokens over
+ * it. A prompt chunk and a single token are one call each, as chunk_fwd with a
+ * carried state and recurrent_step are for the mixer.
+ *
+ * The conventions above hold, except that these tensors may have strides: the
+ * d channels of a head are contiguous, a token's heads follow each other, and
+ * the `*_row` fields give the elements from one token to the next (so q and k
+ * can be parts of one projection's output). Every stride is a multiple of 16
+ * bytes. d is 64 or 128. */
+
+/* Bits of carve_rope_config.flags and carve_paged_config.flags.
+ *   CARVE_ROPE_INTERLEAVED  a rotated pair is channels (2i, 2i + 1); without it
+ *                           (i, i + rot / 2)
+ *   CARVE_ROPE_NORM         divide each row by its root mean square (and multiply
+ *                           by the weights, where given) before the rotation
+ *   CARVE_PAGED_STEP        every sequence has exactly one new token (N == S) and
+ *                           `cu` is not read */
+enum { CARVE_ROPE_INTERLEAVED = 1, CARVE_ROPE_NORM = 2, CARVE_PAGED_STEP = 4 };
+
+typedef struct {
+  int64_t N;                /* tokens */
+  int64_t q_row, k_row;     /* q, k: elements from one token to the next */
+  int64_t qo_row, ko_row;   /* q_out, k_out; in the backward d_q_out, d_k_out */
+  int64_t dq_row, dk_row;   /* dq, dk (backward only) */
+  int32_t T;                /* without positions, token n stands at n mod T */
+  int32_t Hq, Hk, d;
+  int32_t rot;              /* rotated channels: a multiple of 16 up to d, 0 for none */
+  int32_t table_len;        /* rows of cos and sin */
+  int32_t dtype, flags;
+  float eps;                /* under the root, > 0 with CARVE_ROPE_NORM */
+} carve_rope_config;
+
+/* Norm and rotation of queries and keys in one pass. For each head x of each
+ * token at position p:  y = R(p) (x / sqrt(mean(x^2) + eps) * weight), summed in
+ * fp32 and rounded once.
+ *   q [N,Hq,d], k [N,Hk,d] dtype, rows q_row and k_row apart
+ *   q_weight, k_weight [d] dtype or NULL (ones); only with CARVE_ROPE_NORM
+ *   cos, sin [table_len, rot/2] fp32: the angles' cosines and sines per position
+ *   positions [N] int32 or NULL. A position outside [0, table_len) gives NaN in
+ *               the rotated channels.
+ *   q_out, k_out  dtype; each may be its input itself (same rows) */
+int carve_qk_norm_rope_fwd(const carve_rope_config* cfg, const void* q, const void* k, const void* q_weight,
+                           const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                           void* q_out, void* k_out, void* stream);
+
+/* Bytes of workspace carve_qk_norm_rope_bwd needs (0 without weights; `weights`
+ * says whether either weight is given). */
+int carve_qk_norm_rope_workspace(const carve_rope_config* cfg, int32_t weights, int64_t* bytes);
+
+/* Gradients of carve_qk_norm_rope_fwd's inputs. q, k and what follows them as
+ * given to the forward pass; d_q_out, d_k_out the gradients of its outputs.
+ *   dq, dk      dtype; each may be its d_*_out or its input itself (same rows)
+ *   dq_weight, dk_weight [d] fp32, required with the weight, summed over tokens
+ *               and heads in a fixed order (no atomics) */
+int carve_qk_norm_rope_bwd(const carve_rope_config* cfg, const void* q, const void* k, const void* q_weight,
+                           const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                           const void* d_q_out, const void* d_k_out, void* dq, void* dk, float* dq_weight,
+                           float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A paged cache and the sequences of one call.
+ * Token t of sequence s is entry t mod page_size of page table[s][t / page_size]
+ * of k_cache and v_cache; page, token and head strides are free (so one tensor
+ * can hold both caches, heads may come before tokens, ...).
+ * The N new tokens are packed: sequence s has the tokens cu[s] .. cu[s+1] - 1,
+ * the last of its kv_lens[s] tokens (the length counts the new ones, a negative
+ * one is 0). cu does not decrease and starts at 0; tokens from cu[S] on belong to
+ * no sequence and their outputs are left as they were. Lengths and pages are read
+ * on the device, so a captured graph follows them. */
+typedef struct {
+  int32_t N, S;                      /* new tokens, sequences */
+  int32_t Hq, Hk, d;                 /* Hq = G Hk; query head h reads head h / G (append: Hq = 0 without q) */
+  int32_t page_size, pages, width;   /* page_size a power of two; table [S, width], width * page_size <= 2^30 */
+  int32_t rot, table_len;            /* append: as in carve_rope_config */
+  int32_t window;                    /* attention: keys a token sees, itself included; 0 for all before it */
+  int32_t dtype, flags;
+  float eps;                         /* append, with CARVE_ROPE_NORM */
+  float scale;                       /* attention: 0 < scale <= 16 */
+  int64_t q_row, k_row, v_row;       /* elements from one new token to the next */
+  int64_t o_row;                     /* of attention's o and of append's q_out */
+  int64_t table_row;                 /* entries from one sequence's table row to the next's */
+  int64_t kc_page, kc_tok, kc_head;  /* strides of k_cache in elements */
+  int64_t vc_page, vc_tok, vc_head;  /* strides of v_cache */
+} carve_paged_config;
+
+/* Stores the new tokens' keys and values in the cache; the keys (and q, where
+ * given) are normed and rotated on the way as by carve_qk_norm_rope_fwd at the
+ * tokens' positions kv_lens[s] - n_s + i.
+ *   k, v [N,Hk,d], q [N,Hq,d] or NULL (Hq = 0); q_out may be q itself
+ * A token whose position is negative or lies past the table, or whose page
+ * number is outside [0, pages), is not stored. No page may be shared by two
+ * sequences that store to it. */
+int carve_paged_append(const carve_paged_config* cfg, const void* k, const void* v, const void* q,
+                       const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                       const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* k_cache, void* v_cache,
+                       void* q_out, void* stream);
+
+/* Bytes of workspace carve_paged_attention needs for this configuration. */
+int carve_paged_workspace(const carve_paged_config* cfg, int64_t* bytes);
+
+/* Attention of the new tokens over the cache (which holds them already): a token
+ * at position p sees the keys j <= p with j > p - window.
+ *   o = softmax(scale q k^T) v,   lse = log sum exp(scale q k^T)
+ *   q [N,Hq,d], o [N,Hq,d] dtype (o overlaps no input); lse [N,Hq] fp32 or NULL
+ * Softmax statistics and sums are fp32; in bf16 the weights are rounded to bf16
+ * for the product with v. A token that sees no key (a negative position) has o = 0
+ * and lse = -inf. Keys whose page number is outside [0, pages) or past the table
+ * are not seen. What is not seen does not matter, infinities and NaN included.
+ * The workspace may be shared by calls that do not overlap in time. Results are
+ * deterministic (no atomics). */
+int carve_paged_attention(const carve_paged_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* o, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. For CARVE_EHIP it returns the HIP error text
  * of the most recent failure on the calling thread. */
