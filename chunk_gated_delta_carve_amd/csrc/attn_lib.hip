@@ -151,14 +151,17 @@ size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_
 // fp32 and, in bf16, batches whose sequences average at most kRowsPerSeq rows
 // (tokens x grouped heads).
 constexpr int kRowsPerSeq = 32;
-constexpr int kMaxSplits = 128;
+constexpr int kTileSplits = 128;
+constexpr int kCUs = 256;
 struct Plan {
   bool tile;
-  int BM, BN, least;
-  int64_t tiles;
-  int splits;
+  int64_t tiles, most;       // row kernel: blocks of keys at most, over all items
+  int splits, shares;
+  int64_t rows;              // partial results
   int64_t bytes;
 };
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_of(const carve_paged_config* c) {
   Plan p{};
@@ -166,46 +169,55 @@ Plan plan_of(const carve_paged_config* c) {
   const int64_t G = c->Hq / c->Hk;
   const bool step = (c->flags & CARVE_PAGED_STEP) != 0;
   p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)kRowsPerSeq * c->S;
-  p.BM = p.tile ? 128 : 16;
-  p.BN = p.tile ? 64 : 128;
-  p.least = p.tile ? 4 : 1;
-  p.tiles = step ? c->S * ((G + p.BM - 1) / p.BM) : (int64_t)c->N * G / p.BM + c->S;
-  const int64_t want = p.tile ? 512 : 2048;       // workgroups
+  const int BM = p.tile ? 128 : 16, BN = p.tile ? 64 : 128;
+  p.tiles = step ? c->S * up(G, BM) : (int64_t)c->N * G / BM + c->S;
   int64_t keys = (int64_t)c->width * c->page_size;
-  if (c->window > 0 && keys > (int64_t)c->window + p.BM + p.BN) keys = (int64_t)c->window + p.BM + p.BN;
-  const int64_t most = (keys + (int64_t)p.BN * p.least - 1) / ((int64_t)p.BN * p.least);
-  int64_t s = want / (p.tiles * c->Hk);
-  s = s < most ? s : most;
-  s = s < kMaxSplits ? s : kMaxSplits;
-  p.splits = s < 1 ? 1 : (int)s;
-  p.bytes = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq * (c->d + 2) * 4 : 0;
+  if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
+  if (p.tile) {
+    const int64_t most = up(keys, (int64_t)BN * 4);
+    int64_t s = 512 / (p.tiles * c->Hk);
+    s = s < most ? s : most;
+    s = s < kTileSplits ? s : kTileSplits;
+    p.splits = s < 1 ? 1 : (int)s;
+    p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
+  } else {
+    // a workgroup per block of keys at most
+    const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1);
+    const bool f32 = c->dtype == CARVE_F32;
+    const int64_t want = kCUs * (c->d == 128 ? (f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU)
+                                             : (f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU));
+    p.most = blocks;
+    p.shares = (int)(blocks < want ? blocks : want);
+    p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
+  }
+  p.bytes = p.rows * (c->d + 2) * 4;
   return p;
 }
 
-template <typename E, int D, typename K, typename C>
-hipError_t launch_attention(const carve::PagedArgs& a, K kern, C combine, int threads, int lds, hipStream_t s) {
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(threads), lds, s, a);
-  hipError_t e = hipGetLastError();
+template <int D>
+hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
+  using LY = carve::TileLayout<D, 4>;
+  constexpr auto kern = carve::paged_tile_kernel<D, 4>;
+  hipError_t e = set_lds<kern>(LY::bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(LY::NT), LY::bytes, s, a);
+  e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(combine, dim3((unsigned)(((int64_t)a.N * a.Hq + 3) / 4)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((carve::paged_tile_combine_kernel<LY::BM, LY::BN, LY::LEAST, D>),
+                     dim3((unsigned)((int64_t)a.N * a.Hq)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename E, int D>
 hipError_t dispatch_attention(const carve::PagedArgs& a, bool tile, hipStream_t s) {
-  if constexpr (sizeof(E) == 2) {
-    if (tile) {
-      using LY = carve::TileLayout<D, 4>;
-      constexpr auto kern = carve::paged_tile_kernel<D, 4>;
-      const hipError_t e = set_lds<kern>(LY::bytes);
-      if (e != hipSuccess) return e;
-      return launch_attention<E, D>(a, kern, carve::paged_combine_kernel<E, D, LY::BM, LY::BN, LY::LEAST>, LY::NT,
-                                    LY::bytes, s);
-    }
-  }
-  using LY = carve::RowsLayout<E, D>;
-  return launch_attention<E, D>(a, carve::paged_rows_kernel<E, D>,
-                                carve::paged_combine_kernel<E, D, LY::BM, LY::BN, LY::LEAST>, 256, 0, s);
+  if constexpr (sizeof(E) == 2)
+    if (tile) return launch_tiles<D>(a, s);
+  hipLaunchKernelGGL((carve::paged_rows_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.shares == 1) return e;
+  hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D>), dim3((unsigned)((int64_t)a.N * a.Hq)), dim3(256), 0, s,
+                     a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -409,7 +421,7 @@ int check_attention(const carve_paged_config* c) {
   if (!(c->scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c->Hq > 0 && (c->Hk == 0 || c->Hq % c->Hk)) return CARVE_EINVAL;
   const Plan p = plan_of(c);
-  if (p.tiles * p.splits * c->Hk > kMaxInt) return CARVE_EUNSUPPORTED;
+  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxInt) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
 }  // namespace
@@ -465,14 +477,14 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
   a.cu = step ? nullptr : cu; a.kv_lens = kv_lens; a.table = table;
   a.o = o; a.lse = lse;
   a.po = static_cast<float*>(workspace);
-  a.pml = plan.bytes ? a.po + (int64_t)plan.splits * c.N * c.Hq * c.d : nullptr;
+  a.pml = plan.bytes ? a.po + plan.rows * c.d : nullptr;
   a.q_row = c.q_row; a.o_row = c.o_row; a.table_row = c.table_row;
   a.kc_page = c.kc_page; a.kc_tok = c.kc_tok; a.kc_head = c.kc_head;
   a.vc_page = c.vc_page; a.vc_tok = c.vc_tok; a.vc_head = c.vc_head;
   a.N = c.N; a.S = c.S; a.Hq = c.Hq; a.Hk = c.Hk; a.G = c.Hq / c.Hk;
   a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
   a.window = c.window < (1 << 30) ? c.window : 1 << 30;
-  a.splits = plan.splits; a.tiles = (int)plan.tiles;
+  a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
   a.scale = c.scale; a.c = c.scale * carve::kLog2e;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
     return dispatch_attention<decltype(t), decltype(d)::value>(a, plan.tile, reinterpret_cast<hipStream_t>(stream));

@@ -41,10 +41,12 @@ struct PagedArgs {
   const int *cu, *kv_lens, *table;
   void* o;
   float* lse;                                       // [N][Hq] or NULL
-  float *po, *pml;                                  // partials: [splits][N Hq][D], [splits][N Hq][2]
+  float *po, *pml;                                  // partial results (o, and m with l)
   int64_t q_row, o_row, table_row;
   int64_t kc_page, kc_tok, kc_head, vc_page, vc_tok, vc_head;
-  int N, S, Hq, Hk, G, width, pages, page_shift, window, splits, tiles;
+  int N, S, Hq, Hk, G, width, pages, page_shift, window;
+  int tiles, splits;                                // tile kernel: tiles, workgroups per tile at most
+  int shares;                                       // row kernel: workgroups that the work is dealt to
   float scale, c;                                   // c = scale log2 e
 };
 
@@ -60,13 +62,17 @@ struct AttnTile {
 
 // Tiles are numbered without knowing the lengths: sequence s starts at tile
 // floor(cu[s] G / BM) + s, which leaves room for its ceil(n G / BM) tiles.
-__device__ __forceinline__ AttnTile tile_of_rows(const PagedArgs& a, int s, int n0, int cnt, int row0, int BM) {
+__device__ __forceinline__ int first_position(const PagedArgs& a, int s, int cnt) {
+  const int kv = a.kv_lens[s];
+  return (kv > 0 ? kv : 0) - cnt;
+}
+
+__device__ __forceinline__ AttnTile tile_of_rows(const PagedArgs& a, int s, int n0, int cnt, int pos0, int row0,
+                                                 int BM) {
   AttnTile x;
-  x.s = s; x.n0 = n0; x.row0 = row0;
+  x.s = s; x.n0 = n0; x.row0 = row0; x.pos0 = pos0;
   const int all = cnt * a.G;
   x.rows = all - row0 < BM ? all - row0 : BM;
-  const int kv = a.kv_lens[s];
-  x.pos0 = (kv > 0 ? kv : 0) - cnt;
   const int64_t cap = (int64_t)a.width << a.page_shift;
   const int64_t first = (int64_t)x.pos0 + row0 / a.G, last = (int64_t)x.pos0 + (row0 + x.rows - 1) / a.G;
   const int64_t hi = last + 1 < cap ? last + 1 : cap;
@@ -82,7 +88,7 @@ __device__ __forceinline__ AttnTile find_tile(const PagedArgs& a, int t, int BM)
   if (!a.cu) {
     const int per = (a.G + BM - 1) / BM, s = t / per;
     if (s >= a.S || s >= a.N) return none;
-    return tile_of_rows(a, s, s, 1, (t - s * per) * BM, BM);
+    return tile_of_rows(a, s, s, 1, first_position(a, s, 1), (t - s * per) * BM, BM);
   }
   int lo = 0, len = a.S;                            // as find_sequence, over the tiles' starts
   while (len > 0) {
@@ -99,19 +105,36 @@ __device__ __forceinline__ AttnTile find_tile(const PagedArgs& a, int t, int BM)
   if (n0 < 0 || n1 <= n0) return none;
   const int64_t row0 = (t - ((int64_t)n0 * a.G / BM + lo)) * BM;
   if (row0 < 0 || row0 >= (int64_t)(n1 - n0) * a.G) return none;
-  return tile_of_rows(a, lo, n0, n1 - n0, (int)row0, BM);
+  return tile_of_rows(a, lo, n0, n1 - n0, first_position(a, lo, n1 - n0), (int)row0, BM);
 }
 
-// The keys [lo, hi) in blocks of BN (aligned), dealt to at most `splits`
-// workgroups, at least `least` blocks each.
+// Blocks of BN keys per workgroup when a tile's keys are dealt to several: the
+// longest sequence of the call fills all `splits` of them, at least `least`
+// blocks each, and shorter ones need fewer, so that every workgroup has about
+// the same to do. The whole wave takes part.
+__device__ __forceinline__ int share_blocks(const PagedArgs& a, int BM, int BN, int least) {
+  if (a.splits == 1) return 0x40000000;
+  int top = 0;
+  for (int s = lane_id(); s < a.S; s += 64) top = top > a.kv_lens[s] ? top : a.kv_lens[s];
+#pragma unroll
+  for (int w = 1; w < 64; w <<= 1) { const int y = __shfl_xor(top, w); top = top > y ? top : y; }
+  const int64_t cap = (int64_t)a.width << a.page_shift;
+  int64_t keys = top < cap ? top : cap;
+  // a window's tile starts inside a block
+  if (a.window > 0 && keys > (int64_t)a.window + BM + BN) keys = (int64_t)a.window + BM + BN;
+  const int64_t nb = (keys + BN - 1) / BN;
+  const int per = (int)((nb + a.splits - 1) / a.splits);
+  return __builtin_amdgcn_readfirstlane(per > least ? per : least);
+}
+
+// The keys [lo, hi) in blocks of BN (aligned), `per` of them to a workgroup.
 struct Share { int b0, per, count; };
-__device__ __forceinline__ Share share_of(int lo, int hi, int BN, int splits, int least) {
+__device__ __forceinline__ Share share_of(int lo, int hi, int BN, int per) {
   Share x;
   x.b0 = lo / BN;
+  x.per = per;
   const int nb = hi > lo ? (hi + BN - 1) / BN - x.b0 : 0;
-  x.per = (nb + splits - 1) / splits;
-  x.per = x.per > least ? x.per : least;
-  x.count = (nb + x.per - 1) / x.per;
+  x.count = (nb + per - 1) / per;
   return x;
 }
 
@@ -122,28 +145,28 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int s, int j) {   // 
   return id >= 0 && id < a.pages ? id : -1;
 }
 
-// Where a row's results go: the output itself when the tile has one share.
+// Where a row's results go: the output itself when one workgroup sees all of
+// the row's keys, otherwise its place among the partial results.
 template <typename E, int D>
 struct RowOut {
   const PagedArgs& a;
-  int sp;
-  bool whole;
   int h;
+  bool whole;
+  int64_t part0, part_row;                          // partial index of row r: part0 + (part_row ? r : index(r))
   __device__ __forceinline__ int64_t index(const AttnTile& x, int r) const {     // n Hq + query head
     const int row = x.row0 + r;
     return (int64_t)(x.n0 + row / a.G) * a.Hq + h * a.G + row % a.G;
   }
+  __device__ __forceinline__ int64_t slot(int64_t at, int r) const { return part0 + (part_row ? r : at); }
   __device__ __forceinline__ E* out(int64_t at) const {
     return static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D;
   }
-  __device__ __forceinline__ float* part(int64_t at) const {
-    return a.po + ((int64_t)sp * a.N * a.Hq + at) * D;
-  }
-  __device__ __forceinline__ void stats(int64_t at, float m, float l) const {    // one lane per row
+  __device__ __forceinline__ float* part(int64_t at, int r) const { return a.po + slot(at, r) * D; }
+  __device__ __forceinline__ void stats(int64_t at, int r, float m, float l) const {    // one lane per row
     if (whole) {
       if (a.lse) a.lse[at] = l == 0.f ? -__builtin_inff() : (m * a.c + fast_log2(l)) * 0.6931471805599453f;
     } else {
-      float* p = a.pml + ((int64_t)sp * a.N * a.Hq + at) * 2;
+      float* p = a.pml + slot(at, r) * 2;
       p[0] = m; p[1] = l;
     }
   }
@@ -152,10 +175,10 @@ struct RowOut {
 // One row over keys [k0, k1) by a whole wave, key by key and without products
 // that other rows share: lanes score 64 keys at once, then add their values.
 template <typename E, int D>
-__device__ __noinline__ void careful_row(const PagedArgs& a, const AttnTile& x, int h, int r, int k0, int k1, int sp,
-                                         bool whole) {
+__device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTile& x, int r, int k0, int k1) {
   constexpr int V = Piece<E>::V, PER = D / 64;
-  const RowOut<E, D> ro{a, sp, whole, h};
+  const PagedArgs& a = ro.a;
+  const int h = ro.h;
   const int64_t at = ro.index(x, r);
   const int p = x.pos0 + (x.row0 + r) / a.G, lane = lane_id();
   const E* q = static_cast<const E*>(a.q) + at / a.Hq * a.q_row + at % a.Hq * D;
@@ -204,30 +227,39 @@ __device__ __noinline__ void careful_row(const PagedArgs& a, const AttnTile& x, 
       for (int i = 0; i < PER; ++i) o[i] += w * to_f32(v[i]);
     }
   }
-  if (whole) {
+  if (ro.whole) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int i = 0; i < PER; ++i) ro.out(at)[lane * PER + i] = from_f32<E>(o[i] * inv);
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) ro.part(at)[lane * PER + i] = o[i];
+    for (int i = 0; i < PER; ++i) ro.part(at, r)[lane * PER + i] = o[i];
   }
-  if (lane == 0) ro.stats(at, m, l);
+  if (lane == 0) ro.stats(at, r, m, l);
 }
 
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
 
 // ---------------------------------------------------------------------------
-// Few rows: 16 rows per workgroup, whose four waves take alternate blocks of 32
-// keys and are joined at the end. Keys go from memory straight into operand
-// registers (a 16-byte piece of a key's row is one operand), values through a
-// wave's own LDS to be transposed (ds_read_b64_tr_b16 hands a lane four keys
-// of one channel), so there is no barrier in the loop. Bound by reading the
-// cache: per 32 keys of 256 bytes a wave spends 16 + 16 matrix instructions of
-// 16 cycles, a tenth of the time its share of HBM needs to deliver them.
+// Few rows: 16 rows at a time, four waves taking alternate blocks of 32 keys and
+// joined at the end. Keys go from memory straight into operand registers (a
+// 16-byte piece of a key's row is one operand), values through a wave's own LDS
+// to be transposed (ds_read_b64_tr_b16 hands a lane four keys of one channel),
+// so there is no barrier in the loop. Bound by reading the cache: per 32 keys of
+// 256 bytes a wave spends 16 + 16 matrix instructions of 16 cycles, a tenth of
+// the time its share of HBM needs to deliver them.
+//
+// Lengths differ, so the work is dealt evenly: the items (sequence, tile of 16
+// rows, key/value head), each as many blocks of BN keys as its sequence's rows
+// see, are laid end to end, and every workgroup takes an equal stretch of blocks.
+// An item that ends up in several workgroups leaves partial results: a workgroup
+// has at most two, the item its stretch starts inside of and the one it ends in.
 template <typename E, int D>
 struct RowsLayout {
-  static constexpr int BM = 16, KT = 32, BN = 128, LEAST = 1;                    // BN: keys per round of four waves
+  static constexpr int BM = 16, KT = 32, BN = 128;                               // BN: keys per round of four waves
+  // Workgroups per CU that registers allow without spills in the loop; so many
+  // are launched, one stretch of the work each.
+  static constexpr int PER_CU = D == 128 ? 2 : sizeof(E) == 4 ? 3 : 4;
   static constexpr int NP = D * (int)sizeof(E) / 64;                             // pieces per lane and key
   static constexpr int VLD = D * (int)sizeof(E) + (sizeof(E) == 2 ? 32 : 16);    // bytes per value row: spread banks
   static constexpr int OLD = D + 4;                                              // floats per row of a wave's result
@@ -253,23 +285,100 @@ __device__ __forceinline__ s16x4 read_tr(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
 }
 
+// A sequence's part of the work: `items` times `nb` blocks, from key block b0.
+struct RowsWork {
+  int n0, cnt, pos0, items, b0, nb;
+  __device__ __forceinline__ int blocks() const { return items * nb; }
+};
+__device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM, int BN) {
+  RowsWork w;
+  w.n0 = s; w.cnt = 1;
+  if (a.cu) {
+    w.n0 = a.cu[s];
+    const int n1 = a.cu[s + 1];
+    w.cnt = w.n0 < 0 ? 0 : (n1 < a.N ? n1 : a.N) - w.n0;
+  }
+  if (w.cnt <= 0) { w.pos0 = w.items = w.nb = w.b0 = w.cnt = 0; return w; }
+  w.pos0 = first_position(a, s, w.cnt);
+  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, 0, 0x7fffffff);
+  w.items = (w.cnt * a.G + BM - 1) / BM * a.Hk;
+  w.b0 = x.lo / BN;
+  w.nb = x.hi > x.lo ? (x.hi + BN - 1) / BN - w.b0 : 1;    // rows without keys are an item too
+  return w;
+}
+
+// Prefix sums of the sequences' blocks, a lane per run of sequences; with one
+// sequence a lane, `own` keeps what the lane worked out. Counts stay below 2^31
+// (checked on the host for the longest lengths that fit the table).
+struct RowsPlan {
+  int run, before;                                  // sequences per lane, blocks before this lane's run
+  RowsWork own;
+  int total, shares;                                // blocks, workgroups in use
+  int base, more;                                   // blocks per workgroup, one more for the first `more`
+  __device__ __forceinline__ int start(int w) const { return w * base + (w < more ? w : more); }
+  __device__ __forceinline__ int share(int b) const {      // the workgroup that holds block b
+    const int big = more * (base + 1);
+    return b < big ? b / (base + 1) : more + (b - big) / base;
+  }
+  __device__ __forceinline__ RowsWork work(const PagedArgs& a, int s, int BM, int BN) const {
+    if (run > 1) return rows_work(a, s, BM, BN);
+    auto at = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
+    return RowsWork{at(own.n0), at(own.cnt), at(own.pos0), at(own.items), at(own.b0), at(own.nb)};
+  }
+};
+__device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN) {
+  RowsPlan p;
+  p.run = (a.S + 63) >> 6;
+  p.own = RowsWork{};
+  int sum = 0;
+  for (int i = 0; i < p.run; ++i) {
+    const int s = lane_id() * p.run + i;
+    if (s < a.S) { p.own = rows_work(a, s, BM, BN); sum += p.own.blocks(); }
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(incl, d);
+    if (lane_id() >= d) incl += y;
+  }
+  p.before = incl - sum;
+  p.total = __builtin_amdgcn_readlane(incl, 63);
+  p.shares = p.total < a.shares ? p.total : a.shares;
+  p.base = p.total / (p.shares > 0 ? p.shares : 1);
+  p.more = p.total - p.base * p.shares;
+  return p;
+}
+
 template <typename E, int D>
-__global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
   constexpr int NP = LY::NP, KT = LY::KT;
   __shared__ __align__(16) char lds[LY::bytes];
   __shared__ float ms[4][16], ls[4][16];
   __shared__ int bad[16];
-  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest % a.splits;
-  const AttnTile x = find_tile(a, rest / a.splits, LY::BM);
-  if (x.rows <= 0) return;
-  const Share sh = share_of(x.lo, x.hi, LY::BN, a.splits, LY::LEAST);
-  if (sp > 0 && sp >= sh.count) return;
-  const bool whole = sh.count <= 1;
-  const int k0 = (sh.b0 + sp * sh.per) * LY::BN < x.lo ? x.lo : (sh.b0 + sp * sh.per) * LY::BN;
-  const int64_t k1_ = (int64_t)(sh.b0 + (sp + 1) * sh.per) * LY::BN;
-  const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
+  const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
+  if ((int)blockIdx.x >= plan.shares) return;
+  int at_block = plan.start(blockIdx.x);
+  const int end_block = plan.start(blockIdx.x + 1);
+  // the sequence that holds at_block
+  const int in = 63 - __clzll(__ballot(plan.before <= at_block));
+  int s = in * plan.run;
+  int seq_block = __builtin_amdgcn_readlane(plan.before, in);
+  RowsWork w = plan.work(a, s, LY::BM, LY::BN);
+  while (at_block < end_block) {
+  while (at_block >= seq_block + w.blocks()) {
+    seq_block += w.blocks();
+    w = plan.work(a, ++s, LY::BM, LY::BN);
+  }
+  const int item = (at_block - seq_block) / w.nb, blk = at_block - seq_block - item * w.nb;
+  const int take = w.nb - blk < end_block - at_block ? w.nb - blk : end_block - at_block;
+  at_block += take;
+  const int h = item % a.Hk;
+  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
+  const int64_t k0_ = (int64_t)(w.b0 + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
+  const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
+  const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
 
   // this lane's row and its queries, in the pieces the keys come in
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
@@ -290,20 +399,26 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
   for (int i = 0; i < D / 16; ++i) o[i] = zero4();
   float m = kNoMax, l = 0.f;
 
-  // a lane looks up the pages of its two keys (c and 16 + c of the block)
+  // A lane looks up the pages of its two keys (c and 16 + c of the block). The
+  // entries are used a block later: loads return in order, so looking at them any
+  // sooner would wait for the keys and values under way.
+  const int* trow = a.table + s * a.table_row;
   auto lookup = [&](int j0, int (&id)[2]) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int j = j0 + 16 * b + c;
-      id[b] = j >= k0 && j < k1 ? page_of(a, x.s, j) : -1;
+      id[b] = trow[(j < k1 ? j : k1 - 1) >> a.page_shift];
     }
   };
   u32x4 kr[2][NP], vr[2][NP];
   unsigned long long okn = 0;                       // which of the 32 keys exist (bit = key)
   auto fetch = [&](int j0, const int (&id)[2]) {
+    bool ok[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int64_t pg = id[b] < 0 ? 0 : id[b], off = (j0 + 16 * b + c) & pmask;
+      const int j = j0 + 16 * b + c;
+      ok[b] = j >= k0 && j < k1 && (unsigned)id[b] < (unsigned)a.pages;
+      const int64_t pg = ok[b] ? id[b] : 0, off = j & pmask;
       const char* kp = kb + (pg * a.kc_page + off * a.kc_tok) * (int64_t)sizeof(E);
       const char* vp = vb + (pg * a.vc_page + off * a.vc_tok) * (int64_t)sizeof(E);
 #pragma unroll
@@ -311,15 +426,16 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) vr[b][i] = *reinterpret_cast<const u32x4*>(vp + 64 * i);
     }
-    okn = (__ballot(id[0] >= 0) & 0xffffu) | ((__ballot(id[1] >= 0) & 0xffffu) << 16);
+    okn = (__ballot(ok[0]) & 0xffffu) | ((__ballot(ok[1]) & 0xffffu) << 16);
   };
   constexpr int STEP = 4 * KT;
   int j0 = (k0 / LY::BN) * LY::BN + wave * KT;
   int id[2];
   if (j0 < k1) {
-    lookup(j0, id);
-    fetch(j0, id);
+    int id0[2];
+    lookup(j0, id0);
     lookup(j0 + STEP, id);
+    fetch(j0, id0);
   }
   for (; j0 < k1; j0 += STEP) {
     const unsigned ok = (unsigned)okn;
@@ -339,8 +455,10 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
       }
     }
     if (j0 + STEP < k1) {
+      int id2[2];
+      lookup(j0 + 2 * STEP, id2);
       fetch(j0 + STEP, id);
-      lookup(j0 + 2 * STEP, id);
+      id[0] = id2[0]; id[1] = id2[1];
     }
     // lane: row c, keys 16 b + 4 g + i
     if (ok != 0xffffffffu || j0 + KT - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
@@ -397,7 +515,7 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
     }
   }
 
-  // join the four waves
+  // join the four waves (the last item's readers are past the barrier that ended it)
   l = sum_groups(l);
   if (threadIdx.x < 16) bad[threadIdx.x] = 0;
   if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }
@@ -408,7 +526,6 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
     *reinterpret_cast<f32x4*>(ol + (wave * 16 + c) * LY::OLD + 16 * d + 4 * g) = o[d];
   __syncthreads();
   const int r = threadIdx.x >> 4, t = threadIdx.x & 15;
-  const RowOut<E, D> ro{a, sp, whole, h};
   if (r < x.rows) {
     float M = ms[0][r], L = 0.f, acc[D / 16];
 #pragma unroll
@@ -431,21 +548,23 @@ __global__ __launch_bounds__(256) void paged_rows_kernel(PagedArgs a) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
-    if (whole) {
+    if (ro.whole) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
       E* out = ro.out(at) + t * (D / 16);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) out[i] = from_f32<E>(acc[i] * inv);
     } else {
-      f32x4* out = reinterpret_cast<f32x4*>(ro.part(at) + t * (D / 16));
+      f32x4* out = reinterpret_cast<f32x4*>(ro.part(at, r) + t * (D / 16));
 #pragma unroll
       for (int i = 0; i < D / 16; i += 4) out[i / 4] = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
     }
-    if (t == 0) ro.stats(at, M, L);
+    if (t == 0) ro.stats(at, r, M, L);
   }
   __syncthreads();
   for (int i = wave; i < x.rows; i += 4)
-    if (bad[i]) careful_row<E, D>(a, x, h, i, k0, k1, sp, whole);
+    if (bad[i]) careful_row<E, D>(ro, x, i, k0, k1);
+  __syncthreads();                                  // the next item writes the same LDS
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -467,11 +586,11 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   using E = bf16;
   using LY = TileLayout<D, NW>;
   extern __shared__ __align__(16) char lds[];
-  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest % a.splits;
+  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest / a.tiles;
   // the last tiles of a sequence see the most keys: start with them
-  const AttnTile x = find_tile(a, a.tiles - 1 - rest / a.splits, LY::BM);
+  const AttnTile x = find_tile(a, a.tiles - 1 - rest % a.tiles, LY::BM);
   if (x.rows <= 0) return;
-  const Share sh = share_of(x.lo, x.hi, LY::BN, a.splits, LY::LEAST);
+  const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
   if (sp > 0 && sp >= sh.count) return;
   const bool whole = sh.count <= 1;
   const int lane = lane_id(), wave = wave_id(), c = lane & 31, hf = lane >> 5;
@@ -495,17 +614,23 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   const E* kb = static_cast<const E*>(a.kc) + h * a.kc_head + sc * 8;
   const E* vb = static_cast<const E*>(a.vc) + h * a.vc_head + sc * 8;
 
-  // lane l of every wave looks up key l of a block
+  // lane l of every wave looks up key l of a block; as above, the entry is not
+  // looked at before the next block's turn
+  const int* trow = a.table + x.s * a.table_row;
   auto lookup = [&](int b) {
     const int j = b * LY::BN + lane;
-    return b < last_b && j >= x.lo && j < x.hi ? page_of(a, x.s, j) : -1;
+    return trow[(j < x.hi ? j : x.hi - 1) >> a.page_shift];
+  };
+  auto valid = [&](int b, int id) {
+    const int j = b * LY::BN + lane;
+    return b < last_b && j >= x.lo && j < x.hi && (unsigned)id < (unsigned)a.pages;
   };
   u32x4 kr[LY::ST], vr[LY::ST];
   auto fetch = [&](int b, int id) {
 #pragma unroll
     for (int i = 0; i < LY::ST; ++i) {
-      const int r = sr + LY::RS * i, rid = __shfl(id, r);
-      const int64_t pg = rid < 0 ? 0 : rid, off = (b * LY::BN + r) & pmask;
+      const int r = sr + LY::RS * i;
+      const int64_t pg = __shfl(id, r), off = (b * LY::BN + r) & pmask;
       kr[i] = *reinterpret_cast<const u32x4*>(kb + pg * a.kc_page + off * a.kc_tok);
       vr[i] = *reinterpret_cast<const u32x4*>(vb + pg * a.vc_page + off * a.vc_tok);
     }
@@ -533,18 +658,21 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   int idn = -1;                                     // pages of the block after the one in registers
   if (first_b < last_b) {
     const int id0 = lookup(first_b);
-    ok = __ballot(id0 >= 0);
-    fetch(first_b, id0);
     idn = lookup(first_b + 1);
+    const bool v0 = valid(first_b, id0);
+    ok = __ballot(v0);
+    fetch(first_b, v0 ? id0 : 0);
     store(0, ok);
   }
   for (int b = first_b; b < last_b; ++b) {
     const int buf = (b - first_b) & 1;
     __syncthreads();                                // block b is in LDS; nobody reads the other buffer any more
-    const unsigned long long okn = __ballot(idn >= 0);
+    const bool vn = valid(b + 1, idn);
+    const unsigned long long okn = __ballot(vn);
     if (b + 1 < last_b) {
-      fetch(b + 1, idn);
-      idn = lookup(b + 2);
+      const int id2 = lookup(b + 2);
+      fetch(b + 1, vn ? idn : 0);
+      idn = id2;
     }
     const int j0 = b * LY::BN;
     if (j0 <= p_max && (a.window <= 0 || j0 + LY::BN - 1 > p_min - a.window)) {
@@ -616,7 +744,7 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   }
 
   l += __shfl_xor(l, 32);
-  const RowOut<E, D> ro{a, sp, whole, h};
+  const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
   const int r = wave * 32 + c;
   bool nf = false;
   if (r < x.rows) {
@@ -637,14 +765,14 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
               bf16x4{(bf16)(o[i][u] * inv), (bf16)(o[i][u + 1] * inv), (bf16)(o[i][u + 2] * inv),
                      (bf16)(o[i][u + 3] * inv)};
     } else {
-      float* out = ro.part(at) + 4 * hf;
+      float* out = ro.part(at, r) + 4 * hf;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int u = 0; u < 16; u += 4)
           *reinterpret_cast<f32x4*>(out + 32 * i + 2 * u) = f32x4{o[i][u], o[i][u + 1], o[i][u + 2], o[i][u + 3]};
     }
-    if (hf == 0) ro.stats(at, m, l);
+    if (hf == 0) ro.stats(at, r, m, l);
   }
   unsigned long long again = __ballot(nf);
   again = (again | again >> 32) & 0xffffffffull;
@@ -654,18 +782,65 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   while (again) {
     const int i = __ffsll((unsigned long long)again) - 1;
     again &= again - 1;
-    careful_row<E, D>(a, x, h, wave * 32 + i, k0, k1, sp, whole);
+    careful_row<E, D>(ro, x, wave * 32 + i, k0, k1);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Joins a tile's shares: one wave per (token, query head).
-template <typename E, int D, int BM, int BN, int LEAST>
-__global__ __launch_bounds__(256) void paged_combine_kernel(PagedArgs a) {
-  constexpr int PER = D / 64;
-  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
-  if (at >= (int64_t)a.N * a.Hq) return;
-  const int n = (int)(at / a.Hq), hq = (int)(at % a.Hq);
+// Joins the partial results of one (token, query head) per workgroup. Every wave
+// forms the joint statistics (a lane per share) and takes every fourth share's
+// output with eight loads in flight; the four sums meet in LDS. The order is
+// fixed by the lengths alone.
+template <typename E, int D>
+__device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t first, int64_t next, int64_t stride, int count) {
+  // partial index of share i: first for i = 0, next + (i - 1) stride from there on
+  constexpr int PER = D / 64, U = 8;
+  __shared__ float sum[4][D];
+  const int lane = lane_id(), wave = wave_id();
+  auto slot = [&](int i) { return i == 0 ? first : next + (i - 1) * stride; };
+  float M = kNoMax, L = 0.f;
+  for (int i = lane; i < count; i += 64) M = fmaxf(M, a.pml[slot(i) * 2]);
+#pragma unroll
+  for (int w = 1; w < 64; w <<= 1) M = fmaxf(M, __shfl_xor(M, w));
+  for (int i = lane; i < count; i += 64) L += a.pml[slot(i) * 2 + 1] * fast_exp2((a.pml[slot(i) * 2] - M) * a.c);
+  L = wave_sum(L);
+  float o[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) o[k] = 0.f;
+  for (int i0 = wave; i0 < count; i0 += 4 * U) {
+    float v[U][PER], f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t p = slot(i0 + 4 * u < count ? i0 + 4 * u : count - 1);
+      f[u] = a.pml[p * 2];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) v[u][k] = a.po[p * D + lane * PER + k];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + 4 * u < count) {
+        const float e = fast_exp2((f[u] - M) * a.c);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) o[k] += v[u][k] * e;
+      }
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) sum[wave][lane * PER + k] = o[k];
+  __syncthreads();
+  const int64_t at = blockIdx.x;
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x;
+    const float t = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
+    E* out = static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D + d;
+    *out = from_f32<E>(L == 0.f ? 0.f : t / L);
+  }
+  if (threadIdx.x == 0 && a.lse)
+    a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+}
+
+template <int BM, int BN, int LEAST, int D>
+__global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
+  const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
   int s = n, i = 0, cnt = 1, n0 = n;
   if (a.cu) {
     s = find_sequence(a.cu, a.S, n);
@@ -677,29 +852,32 @@ __global__ __launch_bounds__(256) void paged_combine_kernel(PagedArgs a) {
     if (n0 < 0 || i < 0 || i >= cnt) return;
   } else if (s >= a.S) return;
   const int row = i * a.G + hq % a.G;
-  const AttnTile x = tile_of_rows(a, s, n0, cnt, row / BM * BM, BM);
-  const Share sh = share_of(x.lo, x.hi, BN, a.splits, LEAST);
-  if (sh.count <= 1) return;
-  const int lane = lane_id();
+  const AttnTile x = tile_of_rows(a, s, n0, cnt, first_position(a, s, cnt), row / BM * BM, BM);
+  const int count = share_of(x.lo, x.hi, BN, share_blocks(a, BM, BN, LEAST)).count;
+  if (count <= 1) return;
   const int64_t stride = (int64_t)a.N * a.Hq;
-  float M = kNoMax;
-  for (int sp = 0; sp < sh.count; ++sp) M = fmaxf(M, a.pml[(sp * stride + at) * 2]);
-  float L = 0.f, o[PER];
-#pragma unroll
-  for (int u = 0; u < PER; ++u) o[u] = 0.f;
-  for (int sp = 0; sp < sh.count; ++sp) {
-    const float* ml = a.pml + (sp * stride + at) * 2;
-    const float f = fast_exp2((ml[0] - M) * a.c);
-    L += ml[1] * f;
-    const float* po = a.po + (sp * stride + at) * D + lane * PER;
-#pragma unroll
-    for (int u = 0; u < PER; ++u) o[u] += po[u] * f;
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  E* out = static_cast<E*>(a.o) + n * a.o_row + hq * D + lane * PER;
-#pragma unroll
-  for (int u = 0; u < PER; ++u) out[u] = from_f32<E>(o[u] * inv);
-  if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+  join_shares<bf16, D>(a, blockIdx.x, blockIdx.x + stride, stride, count);
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__(256) void paged_rows_combine_kernel(PagedArgs a) {
+  using LY = RowsLayout<E, D>;
+  const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+  const int s = a.cu ? find_sequence(a.cu, a.S, n) : n;
+  const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
+  if (s >= a.S) return;
+  const RowsWork w = plan.work(a, s, LY::BM, LY::BN);
+  const int i = n - w.n0;
+  if (i < 0 || i >= w.cnt) return;
+  const int run0 = s / plan.run;
+  int b = __builtin_amdgcn_readlane(plan.before, run0);     // the item's first block
+  for (int u = run0 * plan.run; u < s; ++u) b += rows_work(a, u, LY::BM, LY::BN).blocks();
+  const int row = i * a.G + hq % a.G;
+  b += (row / LY::BM * a.Hk + hq / a.G) * w.nb;
+  const int64_t w0 = plan.share(b), w1 = plan.share(b + w.nb - 1);
+  if (w0 == w1) return;
+  const int64_t r = row % LY::BM;
+  join_shares<E, D>(a, (2 * w0 + 1) * LY::BM + r, 2 * (w0 + 1) * LY::BM + r, 2 * LY::BM, (int)(w1 - w0) + 1);
 }
 
 }  // namespace carve

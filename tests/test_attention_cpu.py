@@ -309,13 +309,17 @@ def test_attention_arguments_refused(L):
     assert attention(L, paged_cfg(Hq=0)) == _lib.CARVE_OK
 
 
-def test_paged_workspace_does_not_depend_on_the_batch_alone(L):
-    """Splitting fills the GPU when there are few rows: many sequences need no partial results."""
+def test_paged_workspace_is_bounded(L):
+    """Partial results belong to workgroups, not to sequences: a larger batch or a longer table asks for no more
+    than fills the GPU, and a call that one workgroup does asks for none."""
     need = ctypes.c_int64()
-    step = _lib.CARVE_PAGED_STEP
     size = {}
-    for S in (1, 4096):
-        c = paged_cfg(N=S, S=S, width=512, flags=step)
+    for S, width in ((1, 1), (1, 512), (64, 512), (4096, 512), (64, 65536)):
+        c = paged_cfg(N=S, S=S, width=width, flags=_lib.CARVE_PAGED_STEP, Hq=1, Hk=1)
         assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_OK
-        size[S] = need.value
-    assert size[1] > 0 and size[4096] == 0
+        size[S, width] = need.value
+    assert 0 < size[1, 512] <= size[64, 512] == size[4096, 512] == size[64, 65536]
+    assert size[64, 512] <= 32 * MB
+    # more blocks of keys than 32 bits count
+    c = paged_cfg(N=1 << 20, S=1 << 20, width=1 << 26, flags=_lib.CARVE_PAGED_STEP)
+    assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_EUNSUPPORTED
