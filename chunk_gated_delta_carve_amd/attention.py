@@ -45,101 +45,111 @@ def _flat(t, name, shape, dtype, device):
     """A dense tensor's address (None for None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _like(t, name, dtype, device)
+    if t.dtype is not dtype or t.device != device:
+        _like(t, name, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name, lead, H, d, dtype, device):
+def _rows(t, name, shape, dtype, device):
     """Elements from one token of t [*lead, H, d] to the next."""
-    shape, stride = t.shape, t.stride()
-    if tuple(shape) != (*lead, H, d):
-        raise ValueError(f"{name}: expected shape {(*lead, H, d)}, got {tuple(shape)}")
-    _like(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.device != device:
+        _like(t, name, dtype, device)
+    stride = t.stride()
+    H, d = shape[-2], shape[-1]
     if t.numel() == 0:
         return H * d
     if stride[-1] != 1 or (H > 1 and stride[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    row, size = None, 1                  # the token dimensions must step evenly
-    for n, s in zip(reversed(lead), reversed(stride[:-2])):
+    row, size = H * d, 0                 # the token dimensions must step evenly
+    for i in range(len(shape) - 3, -1, -1):
+        n = shape[i]
         if n == 1:
             continue
-        if row is None:
-            row = s
-        elif s != row * size:
+        if not size:
+            row, size = stride[i], 1
+        elif stride[i] != row * size:
             raise ValueError(f"{name}: tokens must be evenly spaced")
         size *= n
-    return H * d if row is None else row
+    return row
 
 
-class _Call:
-    """Stream and device of one call: temporaries belong to the stream that the kernels run on, and the
-    tensors' device is current for the launch."""
+def _dense(like):
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
+class _On:
+    """The given stream and the tensors' device made current: temporaries belong to the stream that the kernels
+    run on."""
 
     def __init__(self, device, stream):
-        self.device, self.given = device, stream
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(device))
+        if handle is not None and handle != torch._C._cuda_getCurrentRawStream(device.index):
+            self.stack.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)))
 
     def __enter__(self):
-        dev = self.device
-        self.stack = None
-        if torch.cuda.current_device() != dev.index:
-            self.stack = contextlib.ExitStack()
-            self.stack.enter_context(torch.cuda.device(dev))
-        if self.given is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            self.stream = self.given.cuda_stream if isinstance(self.given, torch.cuda.Stream) else int(self.given)
-            if self.stream != torch.cuda.current_stream(dev).cuda_stream:
-                self.stack = self.stack or contextlib.ExitStack()
-                self.stack.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=dev)))
         return self
 
     def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
-        return False
+        return self.stack.__exit__(*exc)
+
+
+_HERE = contextlib.nullcontext()         # nothing to change: the usual case, on the device and stream that are current
+
+
+def _on(device, stream):
+    return _HERE if stream is None and device.index == torch._C._cuda_getDevice() else _On(device, stream)
 
 
 def _first(t, name, what):
-    if t.device.type != "cuda":
+    device, dtype = t.device, t.dtype
+    if device.type != "cuda":
         raise ValueError(f"{what} runs on the GPU only; move the inputs to a cuda device")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {t.dtype}")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
     if t.dim() < 3:
         raise ValueError(f"{name}: expected [..., heads, d], got {tuple(t.shape)}")
-    return t.dtype, t.device
+    return dtype, device
 
 
 def _angles(cos, sin, device):
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    if cos is None:
+    if cos is None and sin is None:
         return None, None, 0, 0
-    if cos.dim() != 2:
-        raise ValueError(f"cos: expected [positions, rot / 2], got {tuple(cos.shape)}")
-    return (_flat(cos, "cos", cos.shape, torch.float32, device), _flat(sin, "sin", cos.shape, torch.float32, device),
-            2 * cos.shape[1], cos.shape[0])
+    if cos is None or sin is None:
+        raise ValueError("cos and sin come together")
+    shape = cos.shape
+    if len(shape) != 2:
+        raise ValueError(f"cos: expected [positions, rot / 2], got {tuple(shape)}")
+    return (_flat(cos, "cos", shape, torch.float32, device), _flat(sin, "sin", shape, torch.float32, device),
+            2 * shape[1], shape[0])
+
+
+def _flags(norm, interleaved, q_weight, k_weight):
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to the norm")
+    return (_lib.CARVE_ROPE_NORM if norm else 0) | (_lib.CARVE_ROPE_INTERLEAVED if interleaved else 0)
 
 
 def _rope_call(what, q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
     dt, dev = _first(q, "q", what)
-    lead, Hq, d = tuple(q.shape[:-2]), q.shape[-2], q.shape[-1]
-    Hk = k.shape[-2] if k.dim() >= 2 else -1
-    c = _lib.CarveRopeConfig()
-    c.q_row, c.k_row = _rows(q, "q", lead, Hq, d, dt, dev), _rows(k, "k", lead, Hk, d, dt, dev)
-    c.N, c.T, c.Hq, c.Hk, c.d = math.prod(lead), max(lead[-1], 1), Hq, Hk, d
-    pc, ps, c.rot, c.table_len = _angles(cos, sin, dev)
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights belong to the norm")
-    c.dtype = _DTYPES[dt]
-    c.flags = (_lib.CARVE_ROPE_NORM if norm else 0) | (_lib.CARVE_ROPE_INTERLEAVED if interleaved else 0)
-    c.eps = eps
+    sq, sk = q.shape, k.shape
+    lead, d = sq[:-2], sq[-1]
+    if sk[:-2] != lead or sk[-1] != d:
+        raise ValueError(f"k: expected shape {(*lead, 'heads', d)}, got {tuple(sk)}")
+    pc, ps, rot, table_len = _angles(cos, sin, dev)
+    c = _lib.CarveRopeConfig(math.prod(lead), _rows(q, "q", sq, dt, dev), _rows(k, "k", sk, dt, dev), 0, 0, 0, 0,
+                             lead[-1] or 1, sq[-2], sk[-2], d, rot, table_len, _DTYPES[dt],
+                             _flags(norm, interleaved, q_weight, k_weight), eps)
     args = (q.data_ptr(), k.data_ptr(), _flat(q_weight, "q_weight", (d,), dt, dev),
             _flat(k_weight, "k_weight", (d,), dt, dev), pc, ps, _flat(positions, "positions", lead, _I32, dev))
-    return c, args, lead, Hq, Hk, d, dt, dev
+    return c, args, sq, sk, dt, dev
 
 
 def qk_norm_rope_fwd(q, k, cos=None, sin=None, positions=None, q_weight=None, k_weight=None, norm=True, eps=1e-6,
@@ -150,16 +160,16 @@ def qk_norm_rope_fwd(q, k, cos=None, sin=None, positions=None, q_weight=None, k_
     rotation); positions int32 over the token dimensions (None: the index in the last of them). A position
     outside the table gives NaN. norm=False leaves the norm out. q_out, k_out may be q and k themselves.
     Returns (q_out, k_out)."""
-    c, args, lead, Hq, Hk, d, dt, dev = _rope_call("qk_norm_rope_fwd", q, k, cos, sin, positions, q_weight, k_weight,
-                                                   norm, eps, interleaved)
-    with _Call(dev, stream) as call:
-        if q_out is None:
-            q_out = torch.empty((*lead, Hq, d), dtype=dt, device=dev)
-        if k_out is None:
-            k_out = torch.empty((*lead, Hk, d), dtype=dt, device=dev)
-        c.qo_row, c.ko_row = (_rows(q_out, "q_out", lead, Hq, d, dt, dev), _rows(k_out, "k_out", lead, Hk, d, dt, dev))
-        _lib.check(_lib.lib().carve_qk_norm_rope_fwd(ctypes.byref(c), *args, q_out.data_ptr(), k_out.data_ptr(),
-                                                     call.stream))
+    c, args, sq, sk, dt, dev = _rope_call("qk_norm_rope_fwd", q, k, cos, sin, positions, q_weight, k_weight, norm,
+                                          eps, interleaved)
+    with _on(dev, stream):
+        q_out = _dense(q) if q_out is None else q_out
+        k_out = _dense(k) if k_out is None else k_out
+        c.qo_row, c.ko_row = _rows(q_out, "q_out", sq, dt, dev), _rows(k_out, "k_out", sk, dt, dev)
+        code = _lib.lib().carve_qk_norm_rope_fwd(c, *args, q_out.data_ptr(), k_out.data_ptr(),
+                                                 torch._C._cuda_getCurrentRawStream(dev.index))
+    if code:
+        _lib.check(code)
     return q_out, k_out
 
 
@@ -168,26 +178,25 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, cos=None, sin=None, positions=None,
     """Gradients of qk_norm_rope_fwd's q, k and weights from those of its outputs; the other arguments as given to
     the forward pass. dq may be d_q_out or q itself, dk likewise. Returns a dict with dq, dk (input dtype) and
     dq_weight, dk_weight (fp32, None without the weight)."""
-    c, args, lead, Hq, Hk, d, dt, dev = _rope_call("qk_norm_rope_bwd", q, k, cos, sin, positions, q_weight, k_weight,
-                                                   norm, eps, interleaved)
-    c.qo_row, c.ko_row = (_rows(d_q_out, "d_q_out", lead, Hq, d, dt, dev),
-                          _rows(d_k_out, "d_k_out", lead, Hk, d, dt, dev))
-    with _Call(dev, stream) as call:
-        if dq is None:
-            dq = torch.empty((*lead, Hq, d), dtype=dt, device=dev)
-        if dk is None:
-            dk = torch.empty((*lead, Hk, d), dtype=dt, device=dev)
-        c.dq_row, c.dk_row = _rows(dq, "dq", lead, Hq, d, dt, dev), _rows(dk, "dk", lead, Hk, d, dt, dev)
-        dqw = torch.empty(d, dtype=torch.float32, device=dev) if q_weight is not None else None
-        dkw = torch.empty(d, dtype=torch.float32, device=dev) if k_weight is not None else None
+    c, args, sq, sk, dt, dev = _rope_call("qk_norm_rope_bwd", q, k, cos, sin, positions, q_weight, k_weight, norm,
+                                          eps, interleaved)
+    c.qo_row, c.ko_row = _rows(d_q_out, "d_q_out", sq, dt, dev), _rows(d_k_out, "d_k_out", sk, dt, dev)
+    L = _lib.lib()
+    with _on(dev, stream):
+        dq = _dense(q) if dq is None else dq
+        dk = _dense(k) if dk is None else dk
+        c.dq_row, c.dk_row = _rows(dq, "dq", sq, dt, dev), _rows(dk, "dk", sk, dt, dev)
+        dqw = torch.empty(sq[-1], dtype=torch.float32, device=dev) if q_weight is not None else None
+        dkw = torch.empty(sq[-1], dtype=torch.float32, device=dev) if k_weight is not None else None
         need = ctypes.c_int64()
-        _lib.check(_lib.lib().carve_qk_norm_rope_workspace(ctypes.byref(c), int(dqw is not None or dkw is not None),
-                                                           ctypes.byref(need)))
+        _lib.check(L.carve_qk_norm_rope_workspace(c, int(dqw is not None or dkw is not None), need))
         workspace, ws = _workspace(workspace, need.value, dev)
-        _lib.check(_lib.lib().carve_qk_norm_rope_bwd(
-            ctypes.byref(c), *args, d_q_out.data_ptr(), d_k_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+        code = L.carve_qk_norm_rope_bwd(
+            c, *args, d_q_out.data_ptr(), d_k_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
             None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), ws, need.value,
-            call.stream))
+            torch._C._cuda_getCurrentRawStream(dev.index))
+    if code:
+        _lib.check(code)
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
@@ -204,34 +213,34 @@ def _workspace(given, need, dev):
     return given, given.data_ptr()
 
 
-def _paged_call(N, Hq, Hk, d, k_cache, v_cache, block_table, kv_lens, cu_seqlens, dt, dev):
+def _caches(k_cache, v_cache, Hk, d, dt, dev):
+    shape = k_cache.shape
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dim() != 4 or t.shape[2] != Hk or t.shape[3] != d:
             raise ValueError(f"{name}: expected [pages, page_size, {Hk}, {d}], got {tuple(t.shape)}")
-        _like(t, name, dt, dev)
+        if t.dtype is not dt or t.device != dev:
+            _like(t, name, dt, dev)
         if t.stride(3) != 1:
             raise ValueError(f"{name}: the channels of a head must be contiguous")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"v_cache: expected shape {tuple(k_cache.shape)}, got {tuple(v_cache.shape)}")
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache: expected shape {tuple(shape)}, got {tuple(v_cache.shape)}")
+    return shape, k_cache.stride(), v_cache.stride()
+
+
+def _sequences(block_table, kv_lens, cu_seqlens, N, dev):
+    """(S, table width, elements between its rows, flags, addresses of cu_seqlens, kv_lens and the table)."""
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected [sequences, pages each], got {tuple(block_table.shape)}")
-    _like(block_table, "block_table", _I32, dev)
     S, width = block_table.shape
-    if width > 1 and block_table.stride(1) != 1:
+    row, step = block_table.stride()
+    if block_table.dtype is not _I32 or block_table.device != dev:
+        _like(block_table, "block_table", _I32, dev)
+    if width > 1 and step != 1:
         raise ValueError("block_table: a sequence's entries must be contiguous")
-    c = _lib.CarvePagedConfig()
-    c.N, c.S, c.Hq, c.Hk, c.d = N, S, Hq, Hk, d
-    c.pages, c.page_size = k_cache.shape[0], k_cache.shape[1]
-    c.width, c.table_row = width, block_table.stride(0) if S > 1 else width
-    c.kc_page, c.kc_tok, c.kc_head = k_cache.stride()[:3]
-    c.vc_page, c.vc_tok, c.vc_head = v_cache.stride()[:3]
-    c.dtype = _DTYPES[dt]
-    c.scale = 1.0
-    if cu_seqlens is None:
-        if N != S:
-            raise ValueError(f"without cu_seqlens every sequence has one new token: {N} tokens, {S} sequences")
-        c.flags = _lib.CARVE_PAGED_STEP
-    return (c, _flat(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev), _flat(kv_lens, "kv_lens", (S,), _I32, dev),
+    if cu_seqlens is None and N != S:
+        raise ValueError(f"without cu_seqlens every sequence has one new token: {N} tokens, {S} sequences")
+    return (S, width, row if S > 1 else width, _lib.CARVE_PAGED_STEP if cu_seqlens is None else 0,
+            _flat(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev), _flat(kv_lens, "kv_lens", (S,), _I32, dev),
             block_table.data_ptr())
 
 
@@ -245,27 +254,35 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     page number is not in [0, pages), is not stored; tokens behind cu_seqlens[S] are left alone. Returns q_out
     (None without q)."""
     dt, dev = _first(k, "k", "paged_append")
-    N, Hk, d = k.shape[0], k.shape[-2], k.shape[-1]
-    Hq = 0 if q is None else q.shape[-2]
-    c, cu, lens, table = _paged_call(N, Hq, Hk, d, k_cache, v_cache, block_table, kv_lens, cu_seqlens, dt, dev)
-    c.k_row, c.v_row = _rows(k, "k", (N,), Hk, d, dt, dev), _rows(v, "v", (N,), Hk, d, dt, dev)
-    pc, ps, c.rot, c.table_len = _angles(cos, sin, dev)
-    if not norm and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights belong to the norm")
-    if q is None and (q_weight is not None or q_out is not None):
-        raise ValueError("q_weight and q_out belong to q")
-    c.flags |= (_lib.CARVE_ROPE_NORM if norm else 0) | (_lib.CARVE_ROPE_INTERLEAVED if interleaved else 0)
-    c.eps = eps
+    sk = k.shape
+    if len(sk) != 3:
+        raise ValueError(f"k: expected [tokens, heads, d], got {tuple(sk)}")
+    N, Hk, d = sk
+    cache, ks, vs = _caches(k_cache, v_cache, Hk, d, dt, dev)
+    S, width, table_row, step, cu, lens, table = _sequences(block_table, kv_lens, cu_seqlens, N, dev)
+    pc, ps, rot, table_len = _angles(cos, sin, dev)
+    flags = step | _flags(norm, interleaved, q_weight, k_weight)
     wq, wk = _flat(q_weight, "q_weight", (d,), dt, dev), _flat(k_weight, "k_weight", (d,), dt, dev)
-    with _Call(dev, stream) as call:
+    Hq = q_row = o_row = 0
+    pq = po = None
+    with _on(dev, stream):
         if q is not None:
-            c.q_row = _rows(q, "q", (N,), Hq, d, dt, dev)
-            if q_out is None:
-                q_out = torch.empty((N, Hq, d), dtype=dt, device=dev)
-            c.o_row = _rows(q_out, "q_out", (N,), Hq, d, dt, dev)
-        _lib.check(_lib.lib().carve_paged_append(
-            ctypes.byref(c), k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(), wq, wk, pc, ps, cu, lens,
-            table, k_cache.data_ptr(), v_cache.data_ptr(), None if q is None else q_out.data_ptr(), call.stream))
+            sq = q.shape
+            if len(sq) != 3 or sq[0] != N or sq[2] != d:
+                raise ValueError(f"q: expected shape {(N, 'heads', d)}, got {tuple(sq)}")
+            Hq, q_row, pq = sq[1], _rows(q, "q", sq, dt, dev), q.data_ptr()
+            q_out = _dense(q) if q_out is None else q_out
+            o_row, po = _rows(q_out, "q_out", sq, dt, dev), q_out.data_ptr()
+        elif q_weight is not None or q_out is not None:
+            raise ValueError("q_weight and q_out belong to q")
+        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, rot, table_len, 0, _DTYPES[dt], flags,
+                                  eps, 1.0, q_row, _rows(k, "k", sk, dt, dev), _rows(v, "v", sk, dt, dev), o_row,
+                                  table_row, *ks[:3], *vs[:3])
+        code = _lib.lib().carve_paged_append(c, k.data_ptr(), v.data_ptr(), pq, wq, wk, pc, ps, cu, lens, table,
+                                             k_cache.data_ptr(), v_cache.data_ptr(), po,
+                                             torch._C._cuda_getCurrentRawStream(dev.index))
+    if code:
+        _lib.check(code)
     return q_out
 
 
@@ -278,24 +295,33 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     workspace: device scratch to use (paged_workspace_bytes of it); allocated when None. Returns o [N, Hq, d], and
     lse [N, Hq] fp32 when return_lse."""
     dt, dev = _first(q, "q", "paged_attention")
-    N, Hq, d = q.shape[0], q.shape[-2], q.shape[-1]
+    sq = q.shape
+    if len(sq) != 3:
+        raise ValueError(f"q: expected [tokens, heads, d], got {tuple(sq)}")
+    N, Hq, d = sq
     Hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    c, cu, lens, table = _paged_call(N, Hq, Hk, d, k_cache, v_cache, block_table, kv_lens, cu_seqlens, dt, dev)
-    c.q_row = _rows(q, "q", (N,), Hq, d, dt, dev)
-    c.scale = d ** -0.5 if scale is None else scale
-    c.window = window
+    cache, ks, vs = _caches(k_cache, v_cache, Hk, d, dt, dev)
+    S, width, table_row, step, cu, lens, table = _sequences(block_table, kv_lens, cu_seqlens, N, dev)
     L = _lib.lib()
-    with _Call(dev, stream) as call:
-        if out is None:
-            out = torch.empty((N, Hq, d), dtype=dt, device=dev)
-        c.o_row = _rows(out, "out", (N,), Hq, d, dt, dev)
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    lse = pl = None
+    with _on(dev, stream):
+        out = _dense(q) if out is None else out
+        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, 0, 0, window, _DTYPES[dt], step, 0.0,
+                                  d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0,
+                                  _rows(out, "out", sq, dt, dev), table_row, *ks[:3], *vs[:3])
+        if return_lse:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+            pl = lse.data_ptr()
         need = ctypes.c_int64()
-        _lib.check(L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)))
+        code = L.carve_paged_workspace(c, need)
+        if code:
+            _lib.check(code)
         workspace, ws = _workspace(workspace, need.value, dev)
-        _lib.check(L.carve_paged_attention(
-            ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu, lens, table, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), ws, need.value, call.stream))
+        code = L.carve_paged_attention(c, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu, lens, table,
+                                       out.data_ptr(), pl, ws, need.value,
+                                       torch._C._cuda_getCurrentRawStream(dev.index))
+    if code:
+        _lib.check(code)
     return (out, lse) if return_lse else out
 
 
@@ -309,5 +335,5 @@ def paged_workspace_bytes(N, S, Hq, Hk, d, page_size, width, dtype=torch.bfloat1
     c.table_row = width
     c.kc_page = c.kc_tok = c.kc_head = c.vc_page = c.vc_tok = c.vc_head = d
     need = ctypes.c_int64()
-    _lib.check(_lib.lib().carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)))
+    _lib.check(_lib.lib().carve_paged_workspace(c, need))
     return need.value
