@@ -50,6 +50,11 @@ struct PagedArgs {
   float scale, c;                                   // c = scale log2 e
 };
 
+// The reference m of a row follows its maximum only when that has grown by more
+// than 2^kSlack: the weights then stay below 2^kSlack (harmless in fp32 and in
+// bf16, whose relative step is the same everywhere) and most blocks spare the
+// rescaling of o.
+constexpr float kSlack = 8.f;
 constexpr float kNoMax = -1e37f;                    // below every score that counts; c kNoMax stays finite (c < 24)
 
 // The tile `t` of BM rows: its sequence, its rows and the keys they see.
@@ -478,7 +483,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    if (__ballot(top > m)) {
+    if (__ballot((top - m) * a.c > kSlack)) {
       const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
       m = mn;
       l *= al;
@@ -611,8 +616,14 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
 
   const int pmask = (1 << a.page_shift) - 1;
   const int sr = threadIdx.x / LY::CPR, sc = threadIdx.x % LY::CPR;
-  const E* kb = static_cast<const E*>(a.kc) + h * a.kc_head + sc * 8;
-  const E* vb = static_cast<const E*>(a.vc) + h * a.vc_head + sc * 8;
+  const E* kb = static_cast<const E*>(a.kc) + h * a.kc_head;
+  const E* vb = static_cast<const E*>(a.vc) + h * a.vc_head;
+  // The rows that one load of a wave covers (4, or 8 at d = 64) lie in one page of
+  // at least 8 tokens: page and offset are scalars then, and a lane adds a constant.
+  constexpr int WR = 64 / LY::CPR;
+  const bool wide = a.page_shift >= 3;
+  const unsigned kv_off = (unsigned)((lane / LY::CPR) * a.kc_tok + sc * 8) * 2u;
+  const unsigned vv_off = (unsigned)((lane / LY::CPR) * a.vc_tok + sc * 8) * 2u;
 
   // lane l of every wave looks up key l of a block; as above, the entry is not
   // looked at before the next block's turn
@@ -627,12 +638,22 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
   };
   u32x4 kr[LY::ST], vr[LY::ST];
   auto fetch = [&](int b, int id) {
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < LY::ST; ++i) {
-      const int r = sr + LY::RS * i;
-      const int64_t pg = __shfl(id, r), off = (b * LY::BN + r) & pmask;
-      kr[i] = *reinterpret_cast<const u32x4*>(kb + pg * a.kc_page + off * a.kc_tok);
-      vr[i] = *reinterpret_cast<const u32x4*>(vb + pg * a.vc_page + off * a.vc_tok);
+      for (int i = 0; i < LY::ST; ++i) {
+        const int r0 = wave * WR + LY::RS * i;      // the wave's first row: its page is that of all of them
+        const int64_t pg = __builtin_amdgcn_readlane(id, r0), off = (b * LY::BN + r0) & pmask;
+        kr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(kb + pg * a.kc_page + off * a.kc_tok) + kv_off);
+        vr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(vb + pg * a.vc_page + off * a.vc_tok) + vv_off);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LY::ST; ++i) {
+        const int r = sr + LY::RS * i;
+        const int64_t pg = __shfl(id, r), off = (b * LY::BN + r) & pmask;
+        kr[i] = *reinterpret_cast<const u32x4*>(kb + pg * a.kc_page + off * a.kc_tok + sc * 8);
+        vr[i] = *reinterpret_cast<const u32x4*>(vb + pg * a.vc_page + off * a.vc_tok + sc * 8);
+      }
     }
   };
   auto store = [&](int buf, unsigned long long ok) {
@@ -661,7 +682,7 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
     idn = lookup(first_b + 1);
     const bool v0 = valid(first_b, id0);
     ok = __ballot(v0);
-    fetch(first_b, v0 ? id0 : 0);
+    fetch(first_b, (unsigned)id0 < (unsigned)a.pages ? id0 : 0);
     store(0, ok);
   }
   for (int b = first_b; b < last_b; ++b) {
@@ -671,7 +692,7 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
     const unsigned long long okn = __ballot(vn);
     if (b + 1 < last_b) {
       const int id2 = lookup(b + 2);
-      fetch(b + 1, vn ? idn : 0);
+      fetch(b + 1, (unsigned)idn < (unsigned)a.pages ? idn : 0);
       idn = id2;
     }
     const int j0 = b * LY::BN;
@@ -708,7 +729,7 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
 #pragma unroll
         for (int u = 0; u < 16; ++u) top = fmaxf(top, s[kb2][u]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      if (__ballot(top > m)) {
+      if (__ballot((top - m) * a.c > kSlack)) {
         const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
         m = mn;
         l *= al;
