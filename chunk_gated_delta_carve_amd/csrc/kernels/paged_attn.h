@@ -573,132 +573,257 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
 }
 
 // ---------------------------------------------------------------------------
-// Many rows (bf16): 32 rows per wave, keys and values shared by the workgroup
-// through LDS in blocks of 64, loaded into registers one block ahead and
-// written to the buffer that the last block left.
-template <int D, int NW>
+// Many rows (bf16): 32 rows per wave, over blocks of 64 keys that the workgroup
+// shares through LDS. What the two kernels for it have in common: a workgroup's
+// tile and blocks, a wave's rows and queries, the way of a block from the cache to
+// LDS, and the end.
+template <int D, int NW_>
 struct TileLayout {
-  static constexpr int BM = 32 * NW, BN = 64, NT = 64 * NW, LEAST = 4;
+  static constexpr int NW = NW_, BM = 32 * NW, BN = 64, NT = 64 * NW, LEAST = 4;
   static constexpr int KLD = 2 * D + 16, VLD = 2 * D + 32;   // bytes per row: row starts walk over the banks
-  static constexpr int buf = BN * (KLD + VLD), bytes = 2 * buf;
+  static constexpr int k_bytes = BN * KLD, v_bytes = BN * VLD, bytes = 2 * (k_bytes + v_bytes);
   static constexpr int CPR = D / 8;                          // 16-byte chunks per row
   static constexpr int ST = BN * CPR / NT;                   // chunks per thread and tensor
   static constexpr int RS = NT / CPR;                        // rows between a thread's chunks
+  static constexpr int WR = 64 / CPR;                        // rows of one load of a wave
 };
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
-  using E = bf16;
+template <int D, int NW, bool WIDE>
+struct TileWork {
   using LY = TileLayout<D, NW>;
-  extern __shared__ __align__(16) char lds[];
-  const int h = blockIdx.x % a.Hk, rest = blockIdx.x / a.Hk, sp = rest / a.tiles;
-  // the last tiles of a sequence see the most keys: start with them
-  const AttnTile x = find_tile(a, a.tiles - 1 - rest % a.tiles, LY::BM);
-  if (x.rows <= 0) return;
-  const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
-  if (sp > 0 && sp >= sh.count) return;
-  const bool whole = sh.count <= 1;
-  const int lane = lane_id(), wave = wave_id(), c = lane & 31, hf = lane >> 5;
-  const int first_b = sh.b0 + sp * sh.per;
-  int last_b = first_b + sh.per;
-  { const int all = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN : sh.b0; last_b = last_b < all ? last_b : all; }
-
-  // the wave's rows; rows past the tile's end repeat the last one and are not stored
-  const int wr0 = wave * 32 < x.rows ? wave * 32 : x.rows - 1;
-  const int wr1 = wave * 32 + 31 < x.rows ? wave * 32 + 31 : x.rows - 1;
-  const int row = x.row0 + (wave * 32 + c < x.rows ? wave * 32 + c : x.rows - 1);
-  const int p = x.pos0 + row / a.G;
-  const int p_min = x.pos0 + (x.row0 + wr0) / a.G, p_max = x.pos0 + (x.row0 + wr1) / a.G;
-  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
+  using E = bf16;
+  const PagedArgs& a;
+  AttnTile x;
+  int h, sp, first_b, T;                            // key/value head, share, first block, blocks
+  bool whole;
+  int lane, wave, c, hf;                            // the wave's column and half of the lane
+  int p, p_min, p_max;                              // position of the lane's row, of the wave's first and last
   bf16x8 q[D / 16];
+  const char *kb, *vb;
+  const int* trow;
+  int pmask, sr, sc;
+  unsigned k_page, k_tok, v_page, v_tok, k_off, v_off;   // strides in bytes, below 2^32
+
+  __device__ __forceinline__ TileWork(const PagedArgs& a_) : a(a_) {
+    h = blockIdx.x % a.Hk;
+    const int rest = blockIdx.x / a.Hk;
+    sp = rest / a.tiles;
+    // the last tiles of a sequence see the most keys: start with them
+    x = find_tile(a, a.tiles - 1 - rest % a.tiles, LY::BM);
+    T = 0;
+    if (x.rows <= 0) return;
+    const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
+    if (sp > 0 && sp >= sh.count) { x.rows = 0; return; }
+    whole = sh.count <= 1;
+    first_b = sh.b0 + sp * sh.per;
+    const int all = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN : sh.b0;
+    const int last_b = sh.per < all - first_b ? first_b + sh.per : all;
+    T = last_b > first_b ? last_b - first_b : 0;
+    lane = lane_id(); wave = wave_id(); c = lane & 31; hf = lane >> 5;
+    // rows past the tile's end repeat the last one and are not stored
+    const int wr0 = wave * 32 < x.rows ? wave * 32 : x.rows - 1;
+    const int wr1 = wave * 32 + 31 < x.rows ? wave * 32 + 31 : x.rows - 1;
+    const int row = x.row0 + (wave * 32 + c < x.rows ? wave * 32 + c : x.rows - 1);
+    p = x.pos0 + row / a.G;
+    p_min = x.pos0 + (x.row0 + wr0) / a.G;
+    p_max = x.pos0 + (x.row0 + wr1) / a.G;
+    const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
-
-  const int pmask = (1 << a.page_shift) - 1;
-  const int sr = threadIdx.x / LY::CPR, sc = threadIdx.x % LY::CPR;
-  const E* kb = static_cast<const E*>(a.kc) + h * a.kc_head;
-  const E* vb = static_cast<const E*>(a.vc) + h * a.vc_head;
-  // The rows that one load of a wave covers (4, or 8 at d = 64) lie in one page of
-  // at least 8 tokens: page and offset are scalars then, and a lane adds a constant.
-  constexpr int WR = 64 / LY::CPR;
-  const bool wide = a.page_shift >= 3;
-  const unsigned kv_off = (unsigned)((lane / LY::CPR) * a.kc_tok + sc * 8) * 2u;
-  const unsigned vv_off = (unsigned)((lane / LY::CPR) * a.vc_tok + sc * 8) * 2u;
-
-  // lane l of every wave looks up key l of a block; as above, the entry is not
-  // looked at before the next block's turn
-  const int* trow = a.table + x.s * a.table_row;
-  auto lookup = [&](int b) {
-    const int j = b * LY::BN + lane;
+    for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
+    kb = reinterpret_cast<const char*>(static_cast<const E*>(a.kc) + h * a.kc_head);
+    vb = reinterpret_cast<const char*>(static_cast<const E*>(a.vc) + h * a.vc_head);
+    trow = a.table + x.s * a.table_row;
+    pmask = (1 << a.page_shift) - 1;
+    sr = threadIdx.x / LY::CPR;
+    sc = threadIdx.x % LY::CPR;
+    k_page = (unsigned)a.kc_page * 2u; k_tok = (unsigned)a.kc_tok * 2u;
+    v_page = (unsigned)a.vc_page * 2u; v_tok = (unsigned)a.vc_tok * 2u;
+    k_off = (lane / LY::CPR) * k_tok + sc * 16;
+    v_off = (lane / LY::CPR) * v_tok + sc * 16;
+  }
+  // The queries are here before the loop: without this the waits for them stand in it.
+  __device__ __forceinline__ void have_queries() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
+  }
+  // Lane l of every wave looks up key l of block first_b + t (a block past the end
+  // falls on the last key's page). The entry is not looked at before the next
+  // block's turn: loads return in order, so that would wait for the keys and values
+  // under way.
+  __device__ __forceinline__ int lookup(int t) const {
+    const int j = (first_b + t) * LY::BN + lane;
     return trow[(j < x.hi ? j : x.hi - 1) >> a.page_shift];
-  };
-  auto valid = [&](int b, int id) {
-    const int j = b * LY::BN + lane;
-    return b < last_b && j >= x.lo && j < x.hi && (unsigned)id < (unsigned)a.pages;
-  };
-  u32x4 kr[LY::ST], vr[LY::ST];
-  auto fetch = [&](int b, int id) {
-    if (wide) {
-#pragma unroll
-      for (int i = 0; i < LY::ST; ++i) {
-        const int r0 = wave * WR + LY::RS * i;      // the wave's first row: its page is that of all of them
-        const int64_t pg = __builtin_amdgcn_readlane(id, r0), off = (b * LY::BN + r0) & pmask;
-        kr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(kb + pg * a.kc_page + off * a.kc_tok) + kv_off);
-        vr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(vb + pg * a.vc_page + off * a.vc_tok) + vv_off);
-      }
+  }
+  __device__ __forceinline__ unsigned long long valid(int t, int id) const {   // the block's keys that exist, a bit each
+    const int j = (first_b + t) * LY::BN + lane;
+    return __ballot((j >= x.lo) & (j < x.hi) & ((unsigned)id < (unsigned)a.pages));
+  }
+  // Byte offset of the lane's key of block t, on page `id` (page 0 where there is none).
+  __device__ __forceinline__ uint64_t place(int t, int id, unsigned page_bytes, unsigned tok_bytes) const {
+    const unsigned pg = (unsigned)id < (unsigned)a.pages ? id : 0;
+    const unsigned off = ((first_b + t) * LY::BN + lane) & pmask;
+    return (uint64_t)pg * page_bytes + (uint64_t)off * tok_bytes;
+  }
+  // The thread's chunk i of a block. The rows that one load of a wave covers (4, or
+  // 8 at d = 64) lie in one page of at least 8 tokens (WIDE): their first row's
+  // address is a scalar then, and a lane adds a constant.
+  __device__ __forceinline__ u32x4 load(const char* base, uint64_t at, unsigned lane_off, int i) const {
+    if constexpr (WIDE) {
+      const int r0 = wave * LY::WR + LY::RS * i;
+      const unsigned lo = __builtin_amdgcn_readlane((int)at, r0), hi = __builtin_amdgcn_readlane((int)(at >> 32), r0);
+      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + lane_off);
     } else {
+      const int rr = sr + LY::RS * i;
+      const unsigned lo = __shfl((int)at, rr), hi = __shfl((int)(at >> 32), rr);
+      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + sc * 16);
+    }
+  }
+  __device__ __forceinline__ u32x4 load_k(uint64_t at, int i) const { return load(kb, at, k_off, i); }
+  __device__ __forceinline__ u32x4 load_v(uint64_t at, int i) const { return load(vb, at, v_off, i); }
+  // Zeros in the place of values whose key does not exist: a weight of 0 would not
+  // drop what an unused cache entry holds if that is not finite.
+  __device__ __forceinline__ void clear(unsigned long long ok, u32x4 (&vr)[LY::ST]) const {
+    if (ok != ~0ull) {
 #pragma unroll
       for (int i = 0; i < LY::ST; ++i) {
-        const int r = sr + LY::RS * i;
-        const int64_t pg = __shfl(id, r), off = (b * LY::BN + r) & pmask;
-        kr[i] = *reinterpret_cast<const u32x4*>(kb + pg * a.kc_page + off * a.kc_tok + sc * 8);
-        vr[i] = *reinterpret_cast<const u32x4*>(vb + pg * a.vc_page + off * a.vc_tok + sc * 8);
+        const unsigned keep = (ok >> (sr + LY::RS * i)) & 1ull ? ~0u : 0u;
+        vr[i] &= u32x4{keep, keep, keep, keep};
       }
     }
-  };
-  auto store = [&](int buf, unsigned long long ok) {
-    char* kl = lds + buf * LY::buf;
-    char* vl = kl + LY::BN * LY::KLD;
+  }
+  // Scores of block t that a row does not see. Lane: row c, keys 32 kb2 + 8 (u / 4) + 4 hf + u % 4.
+  __device__ __forceinline__ void mask(int t, unsigned long long ok, f32x16 (&s)[2]) const {
+    const int j0 = (first_b + t) * LY::BN;
+    if (ok != ~0ull || j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+      const unsigned long long mine = ok >> (4 * hf);
+      const int far = p - j0 - 4 * hf, near = a.window > 0 ? far - a.window : -1000000;   // visible: near < key <= far
 #pragma unroll
-    for (int i = 0; i < LY::ST; ++i) {
-      const int r = sr + LY::RS * i;
-      if (ok != ~0ull && !((ok >> r) & 1ull)) kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-      *reinterpret_cast<u32x4*>(kl + r * LY::KLD + sc * 16) = kr[i];
-      *reinterpret_cast<u32x4*>(vl + r * LY::VLD + sc * 16) = vr[i];
+      for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int kk = 32 * kb2 + 8 * (u / 4) + u % 4;
+          const bool see = ((mine >> kk) & 1ull) && kk <= far && kk > near;
+          s[kb2][u] = see ? s[kb2][u] : -__builtin_inff();
+        }
     }
-  };
+  }
+  // Moves the row's reference up to `top` where that has grown far enough.
+  __device__ __forceinline__ void rescale(float top, float& m, float& l, f32x16 (&o)[D / 32]) const {
+    if (__ballot((top - m) * a.c > kSlack)) {
+      const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[i][u] *= al;
+    }
+  }
+  __device__ __forceinline__ void finish(const f32x16 (&o)[D / 32], float m, float l) const {
+    l += __shfl_xor(l, 32);
+    const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
+    const int r = wave * 32 + c;
+    bool nf = false;
+    if (r < x.rows) {
+      const int64_t at = ro.index(x, r);
+      nf = not_finite(l);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) nf = nf || not_finite(o[i][u]);
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        E* out = ro.out(at) + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            *reinterpret_cast<bf16x4*>(out + 32 * i + 2 * u) =
+                bf16x4{(bf16)(o[i][u] * inv), (bf16)(o[i][u + 1] * inv), (bf16)(o[i][u + 2] * inv),
+                       (bf16)(o[i][u + 3] * inv)};
+      } else {
+        float* out = ro.part(at, r) + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            *reinterpret_cast<f32x4*>(out + 32 * i + 2 * u) = f32x4{o[i][u], o[i][u + 1], o[i][u + 2], o[i][u + 3]};
+      }
+      if (hf == 0) ro.stats(at, r, m, l);
+    }
+    unsigned long long again = __ballot(nf);
+    again = (again | again >> 32) & 0xffffffffull;
+    const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
+    const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
+    const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
+    while (again) {
+      const int i = __ffsll((unsigned long long)again) - 1;
+      again &= again - 1;
+      careful_row<E, D>(ro, x, wave * 32 + i, k0, k1);
+    }
+  }
+};
 
+// d = 64: four waves, each block in turn (products, softmax, products), three
+// workgroups per CU that fill each other's waits. Vector work outweighs the
+// products here (130 vector instructions of a softmax block against 16 products),
+// and three waves per SIMD issue it faster than two that interleave: the kernel
+// below took 133 us on the windowed prompts (51 GFLOP), this one 107 us.
+template <int D, bool WIDE>
+__global__ __launch_bounds__(256, 2) void paged_tile_kernel(PagedArgs a) {
+  using W = TileWork<D, 4, WIDE>;
+  using LY = typename W::LY;
+  extern __shared__ __align__(16) char lds[];
+  W w(a);
+  if (w.x.rows <= 0) return;
+  const int T = w.T;
   f32x16 o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int u = 0; u < 16; ++u) o[i][u] = 0.f;
   float m = kNoMax, l = 0.f;
-
+  constexpr int buf_bytes = LY::k_bytes + LY::v_bytes;
+  u32x4 kr[LY::ST], vr[LY::ST];
+  auto fetch = [&](int t, int id) {
+    const uint64_t k_at = w.place(t, id, w.k_page, w.k_tok), v_at = w.place(t, id, w.v_page, w.v_tok);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) {
+      kr[i] = w.load_k(k_at, i);
+      vr[i] = w.load_v(v_at, i);
+    }
+  };
+  auto store = [&](int buf, unsigned long long ok) {
+    char* kl = lds + buf * buf_bytes + w.sr * LY::KLD + w.sc * 16;
+    char* vl = lds + buf * buf_bytes + LY::k_bytes + w.sr * LY::VLD + w.sc * 16;
+    w.clear(ok, vr);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) {
+      *reinterpret_cast<u32x4*>(kl + LY::RS * i * LY::KLD) = kr[i];
+      *reinterpret_cast<u32x4*>(vl + LY::RS * i * LY::VLD) = vr[i];
+    }
+  };
   unsigned long long ok = 0;
-  int idn = -1;                                     // pages of the block after the one in registers
-  if (first_b < last_b) {
-    const int id0 = lookup(first_b);
-    idn = lookup(first_b + 1);
-    const bool v0 = valid(first_b, id0);
-    ok = __ballot(v0);
-    fetch(first_b, (unsigned)id0 < (unsigned)a.pages ? id0 : 0);
+  int idn = 0;                                      // table entry of the block after the one in registers
+  if (T > 0) {
+    const int id0 = w.lookup(0);
+    idn = w.lookup(1);
+    ok = w.valid(0, id0);
+    fetch(0, id0);
     store(0, ok);
   }
-  for (int b = first_b; b < last_b; ++b) {
-    const int buf = (b - first_b) & 1;
-    __syncthreads();                                // block b is in LDS; nobody reads the other buffer any more
-    const bool vn = valid(b + 1, idn);
-    const unsigned long long okn = __ballot(vn);
-    if (b + 1 < last_b) {
-      const int id2 = lookup(b + 2);
-      fetch(b + 1, (unsigned)idn < (unsigned)a.pages ? idn : 0);
-      idn = id2;
-    }
-    const int j0 = b * LY::BN;
-    if (j0 <= p_max && (a.window <= 0 || j0 + LY::BN - 1 > p_min - a.window)) {
-      const char* kl = lds + buf * LY::buf;
-      const char* vl = kl + LY::BN * LY::KLD;
+  w.have_queries();
+  for (int t = 0; t < T; ++t) {
+    const int buf = t & 1;
+    __syncthreads();                                // block t is in LDS; nobody reads the other buffer any more
+    const unsigned long long okn = w.valid(t + 1, idn);
+    const int id2 = w.lookup(t + 2);
+    fetch(t + 1, idn);
+    idn = id2;
+    const int j0 = (w.first_b + t) * LY::BN;
+    if (j0 <= w.p_max && (a.window <= 0 || j0 + LY::BN - 1 > w.p_min - a.window)) {
+      const char* kl = lds + buf * buf_bytes;
+      const char* vl = kl + LY::k_bytes;
       f32x16 s[2];
 #pragma unroll
       for (int kb2 = 0; kb2 < 2; ++kb2) {
@@ -706,38 +831,18 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
         for (int u = 0; u < 16; ++u) s[kb2][u] = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const bf16x8 k = *reinterpret_cast<const bf16x8*>(kl + (32 * kb2 + c) * LY::KLD + 32 * i + 16 * hf);
-          s[kb2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[kb2], 0, 0, 0);
+          const bf16x8 k = *reinterpret_cast<const bf16x8*>(kl + (32 * kb2 + w.c) * LY::KLD + 32 * i + 16 * w.hf);
+          s[kb2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, w.q[i], s[kb2], 0, 0, 0);
         }
       }
-      // lane: row c, keys 32 kb2 + 8 (u / 4) + 4 hf + u % 4
-      if (ok != ~0ull || j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
-        const unsigned long long mine = ok >> (4 * hf);
-        const int far = p - j0 - 4 * hf, near = a.window > 0 ? far - a.window : -1000000;   // visible: near < key <= far
-#pragma unroll
-        for (int kb2 = 0; kb2 < 2; ++kb2)
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const int kk = 32 * kb2 + 8 * (u / 4) + u % 4;
-            const bool see = ((mine >> kk) & 1ull) && kk <= far && kk > near;
-            s[kb2][u] = see ? s[kb2][u] : -__builtin_inff();
-          }
-      }
+      w.mask(t, ok, s);
       float top = s[0][0];
 #pragma unroll
       for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
         for (int u = 0; u < 16; ++u) top = fmaxf(top, s[kb2][u]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      if (__ballot((top - m) * a.c > kSlack)) {
-        const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
-        m = mn;
-        l *= al;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int u = 0; u < 16; ++u) o[i][u] *= al;
-      }
+      w.rescale(top, m, l, o);
       const float mc = m * a.c;
       bf16x8 pb[4];
 #pragma unroll
@@ -748,7 +853,7 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
           l += e;
           pb[2 * kb2 + u / 8][u % 8] = (bf16)e;
         }
-      const char* src = vl + (4 * hf + (lane & 15) / 4) * LY::VLD + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+      const char* src = vl + (4 * w.hf + (w.lane & 15) / 4) * LY::VLD + ((w.lane >> 4) & 1) * 32 + (w.lane & 3) * 8;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
@@ -760,51 +865,208 @@ __global__ __launch_bounds__(64 * NW, 2) void paged_tile_kernel(PagedArgs a) {
               bf16x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]}, pb[ks], o[d], 0, 0, 0);
         }
     }
-    if (b + 1 < last_b) store(buf ^ 1, okn);
+    store(buf ^ 1, okn);
     ok = okn;
   }
+  w.finish(o, m, l);
+}
 
-  l += __shfl_xor(l, 32);
-  const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
-  const int r = wave * 32 + c;
-  bool nf = false;
-  if (r < x.rows) {
-    const int64_t at = ro.index(x, r);
-    nf = not_finite(l);
+// d = 128: eight waves, two blocks under way in each. A wave issues an
+// instruction every five cycles or so and a 32x32x16 product occupies the matrix
+// unit for 32, so the vector work has to stand between the products of the same
+// wave: in step t the products X(t+1) are dealt among the exponentials of block t,
+// then the products O += P(t) V(t) among the maxima of X(t+1), and the operands
+// come from LDS a few products ahead. Measured per step of 8 waves: 2200 cycles
+// for the products (2048 without any gap), 1000 for the pair (below) and 900 of
+// wait for the slower half of the waves.
+//
+// Blocks are loaded into registers two steps ahead and written to LDS one ahead:
+// "pair p" is keys p + 1 and values p. Step t, between two barriers, writes pair
+// t + 1 (keys t + 2 over keys t, read in step t - 1; values t + 1 over values
+// t - 1, likewise) while it reads keys t + 1 and values t.
+// 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 544 us, 885 TFLOP/s, where
+// the kernel above takes 620 us.
+template <int D, bool WIDE>
+__global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
+  using W = TileWork<D, 8, WIDE>;
+  using LY = typename W::LY;
+  extern __shared__ __align__(16) char lds[];
+  W w(a);
+  if (w.x.rows <= 0) return;
+  const int T = w.T;
+  f32x16 o[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+  for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int u = 0; u < 16; ++u) nf = nf || not_finite(o[i][u]);
-    if (whole) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      E* out = ro.out(at) + 4 * hf;
+    for (int u = 0; u < 16; ++u) o[i][u] = 0.f;
+  float m = kNoMax, l = 0.f, top = 0.f;             // top: the row's maximum in the next block
+
+  u32x4 kr[LY::ST], vr[LY::ST];
+  int pair = 0;                                     // the pair in registers: keys pair + 1, values pair
+  int id1 = 0, id2 = 0;                             // table entries of blocks pair + 1 and pair + 2
+  unsigned long long ok_now = 0, ok_last = 0;       // keys of blocks pair and pair - 1
+  char* vlds = lds + 2 * LY::k_bytes;
+  char* k_dst = lds + w.sr * LY::KLD + w.sc * 16;
+  char* v_dst = vlds + w.sr * LY::VLD + w.sc * 16;
+  // Pair to LDS, the one after it under way. Nothing here depends on how many
+  // blocks are left (blocks past the end are not used), so the counts of loads in
+  // flight are known and each wait is for its own.
+  auto next_pair = [&]() {
+    w.clear(ok_now, vr);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < LY::ST; ++i)
+      *reinterpret_cast<u32x4*>(k_dst + ((pair + 1) & 1) * LY::k_bytes + LY::RS * i * LY::KLD) = kr[i];
 #pragma unroll
-        for (int u = 0; u < 16; u += 4)
-          *reinterpret_cast<bf16x4*>(out + 32 * i + 2 * u) =
-              bf16x4{(bf16)(o[i][u] * inv), (bf16)(o[i][u + 1] * inv), (bf16)(o[i][u + 2] * inv),
-                     (bf16)(o[i][u + 3] * inv)};
-    } else {
-      float* out = ro.part(at, r) + 4 * hf;
+    for (int i = 0; i < LY::ST; ++i)
+      *reinterpret_cast<u32x4*>(v_dst + (pair & 1) * LY::v_bytes + LY::RS * i * LY::VLD) = vr[i];
+    ok_last = ok_now;
+    ok_now = w.valid(pair + 1, id1);
+    ++pair;
+    const uint64_t k_at = w.place(pair + 1, id2, w.k_page, w.k_tok), v_at = w.place(pair, id1, w.v_page, w.v_tok);
+    id1 = id2;
+    id2 = w.lookup(pair + 2);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
 #pragma unroll
-        for (int u = 0; u < 16; u += 4)
-          *reinterpret_cast<f32x4*>(out + 32 * i + 2 * u) = f32x4{o[i][u], o[i][u + 1], o[i][u + 2], o[i][u + 3]};
+    for (int i = 0; i < LY::ST; ++i) vr[i] = w.load_v(v_at, i);
+  };
+  if (T > 0) {
+    const int id0 = w.lookup(0);
+    id1 = w.lookup(1);
+    id2 = w.lookup(2);
+    ok_now = w.valid(0, id0);
+    uint64_t k_at = w.place(0, id0, w.k_page, w.k_tok);
+    const uint64_t v_at = w.place(0, id0, w.v_page, w.v_tok);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) *reinterpret_cast<u32x4*>(k_dst + LY::RS * i * LY::KLD) = kr[i];
+    k_at = w.place(1, id1, w.k_page, w.k_tok);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) vr[i] = w.load_v(v_at, i);
+  }
+  w.have_queries();
+
+  // the blocks [w0, w1) of the workgroup's that some row of the wave sees
+  int w0 = 0, w1 = w.p_max < 0 ? 0 : (w.p_max >> 6) + 1 - w.first_b;
+  w1 = w1 < T ? w1 : T;
+  if (a.window > 0 && w.p_min - a.window + 1 > 0) w0 = ((w.p_min - a.window + 1) >> 6) - w.first_b;
+  w0 = w0 > 0 ? w0 : 0;
+  if (w0 >= w1) w0 = w1 = T + 2;
+
+  // X^T of block t: product i is channels 16 (i / 2) .. of the half i % 2 of its keys
+  constexpr int NK = D / 8, RK = 8, EP = 32 / NK;
+  const char* k_src = lds + w.c * LY::KLD + 16 * w.hf;
+  auto read_k = [&](const char* kl, int i) {
+    return *reinterpret_cast<const bf16x8*>(kl + 32 * (i & 1) * LY::KLD + 32 * (i >> 1));
+  };
+  // O^T: product i is keys 16 (i / ND) .. of the block, channels 32 (i % ND) ..
+  constexpr int ND = D / 32, NV = 4 * ND, RV = 4;
+  const char* v_src = vlds + (4 * w.hf + (w.lane & 15) / 4) * LY::VLD + ((w.lane >> 4) & 1) * 32 + (w.lane & 3) * 8;
+  auto read_v = [&](const char* vl, int i, s16x4 (&v)[2]) {
+    const char* at = vl + 16 * (i / ND) * LY::VLD + 64 * (i % ND);
+    v[0] = read_tr(at);
+    v[1] = read_tr(at + 8 * LY::VLD);
+  };
+
+  // step t: cur holds X(t), nxt takes X(t + 1)
+  auto step = [&](int t, f32x16 (&cur)[2], f32x16 (&nxt)[2]) {
+    __syncthreads();
+    const char* kl = k_src + ((t + 1) & 1) * LY::k_bytes;
+    const char* vl = v_src + (t & 1) * LY::v_bytes;
+    bf16x8 kf[RK];
+    const bool on = t >= w0 && t < w1;
+    if (on || t + 1 == w0) {
+#pragma unroll
+      for (int i = 0; i < RK; ++i) kf[i] = read_k(kl, i);
     }
-    if (hf == 0) ro.stats(at, r, m, l);
-  }
-  unsigned long long again = __ballot(nf);
-  again = (again | again >> 32) & 0xffffffffull;
-  const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
-  const int64_t k1_ = (int64_t)last_b * LY::BN;
-  const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
-  while (again) {
-    const int i = __ffsll((unsigned long long)again) - 1;
-    again &= again - 1;
-    careful_row<E, D>(ro, x, wave * 32 + i, k0, k1);
-  }
+    next_pair();
+    if (on) {
+      w.rescale(top, m, l, o);
+      const float mc = m * a.c;
+      float sum[2] = {0.f, 0.f};
+      bf16x8 pb[4];
+      s16x4 vf[RV][2];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) nxt[0][u] = nxt[1][u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NK + 2; ++i) {
+        if (i < NK) {
+          nxt[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % RK], w.q[i >> 1], nxt[i & 1], 0, 0, 0);
+          if (i + RK < NK) kf[i % RK] = read_k(kl, i + RK);
+        }
+        if (i >= NK - RV && i < NK) read_v(vl, i - (NK - RV), vf[i - (NK - RV)]);
+        // element e of cur in three turns: argument, power, sum and rounding
+#pragma unroll
+        for (int u = 0; u < EP; ++u) {
+          if (i < NK) {
+            const int e = EP * i + u;
+            cur[e >> 4][e & 15] = cur[e >> 4][e & 15] * a.c - mc;
+          }
+          if (i >= 1 && i <= NK) {
+            const int e = EP * (i - 1) + u;
+            cur[e >> 4][e & 15] = fast_exp2(cur[e >> 4][e & 15]);
+          }
+          if (i >= 2) {
+            const int e = EP * (i - 2) + u;
+            sum[u & 1] += cur[e >> 4][e & 15];
+            pb[e >> 3][e & 7] = (bf16)cur[e >> 4][e & 15];
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      l += sum[0] + sum[1];
+      w.mask(t + 1, ok_last, nxt);
+      float top2 = nxt[0][0];
+      top = nxt[1][0];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bf16x4 b0 = __builtin_bit_cast(bf16x4, vf[i % RV][0]), b1 = __builtin_bit_cast(bf16x4, vf[i % RV][1]);
+        o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            bf16x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]}, pb[i / ND], o[i % ND], 0, 0, 0);
+        if (i + RV < NV) read_v(vl, i + RV, vf[i % RV]);
+        // from product 2 on, the maxima: X(t + 1) has left the matrix unit by then
+        constexpr int MP = (16 + NV - 3) / (NV - 2);
+#pragma unroll
+        for (int u = 0; u < MP; ++u) {
+          const int e = MP * (i - 2) + u;
+          if (i >= 2 && e < 16) {
+            top2 = fmaxf(top2, nxt[0][e]);
+            top = fmaxf(top, nxt[1][e]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      top = fmaxf(top, top2);
+      top = fmaxf(top, __shfl_xor(top, 32));
+    } else if (t + 1 == w0) {                       // the wave's first block
+#pragma unroll
+      for (int u = 0; u < 16; ++u) nxt[0][u] = nxt[1][u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        nxt[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % RK], w.q[i >> 1], nxt[i & 1], 0, 0, 0);
+        if (i + RK < NK) kf[i % RK] = read_k(kl, i + RK);
+      }
+      w.mask(t + 1, ok_last, nxt);
+      top = nxt[0][0];
+#pragma unroll
+      for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) top = fmaxf(top, nxt[kb2][u]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+    }
+  };
+  f32x16 s0[2], s1[2];
+  if (T > 0)
+    for (int t = -1; t < T; t += 2) {
+      step(t, s0, s1);
+      if (t + 1 < T) step(t + 1, s1, s0);
+    }
+  w.finish(o, m, l);
 }
 
 // ---------------------------------------------------------------------------
