@@ -54,7 +54,9 @@ bool bad_rows(int64_t n, int64_t row, int64_t len, int dtype, bool written) {
   return row < 0 || (written && n > 1 && row < len) || off16(row, dtype);
 }
 
-int blocks_for(int64_t rows, int per) { return (int)((rows + per - 1) / per); }
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kFewWaves = 4096;   // four waves per SIMD
 
 // Blocks of the gradient: four per CU share the rows of q and k in proportion,
 // each tensor at least one where it has rows.
@@ -62,7 +64,7 @@ constexpr int kBwdBlocks = 1024;
 void bwd_blocks(const carve_rope_config* c, int* nq, int* nk) {
   const int per = carve::kRopeThreads / (c->d * (int)elem_bytes(c->dtype) / 16);
   const int64_t rq = c->N * c->Hq, rk = c->N * c->Hk;
-  int64_t bq = blocks_for(rq, per), bk = blocks_for(rk, per);
+  int64_t bq = up(rq, per), bk = up(rk, per);
   if (bq + bk > kBwdBlocks) {
     const int64_t s = (kBwdBlocks * rq + rq + rk - 1) / (rq + rk);
     bk = bk < kBwdBlocks - s ? bk : kBwdBlocks - s;
@@ -105,6 +107,27 @@ hipError_t by_type(int dtype, int d, F&& f) {
     return d == 64 ? f(carve::bf16{}, std::integral_constant<int, 64>{})
                    : f(carve::bf16{}, std::integral_constant<int, 128>{});
   return d == 64 ? f(float{}, std::integral_constant<int, 64>{}) : f(float{}, std::integral_constant<int, 128>{});
+}
+
+// Pieces per lane of the kernels that take a token's rows by waves. Few waves: one
+// piece each, for the shortest chain (64 tokens of 18 heads of 128: 3.6 us against 5.3). Many:
+// up to four, which shares the token's angles and keeps four loads in flight, in
+// the fewest waves per token.
+struct TokenWaves { int per_lane; unsigned per_token; };
+TokenWaves token_waves(int64_t tokens, int64_t heads, int d, int dtype) {
+  const int64_t passes = up(heads * (d * (int64_t)elem_bytes(dtype) / 16), 64);
+  if (passes * tokens <= kFewWaves) return {1, (unsigned)passes};
+  const int64_t waves = up(passes, carve::kRopePieces);
+  return {(int)up(passes, waves), (unsigned)waves};
+}
+template <typename F>
+hipError_t by_pieces(int n, F&& f) {
+  switch (n) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    default: return f(std::integral_constant<int, 4>{});
+  }
 }
 
 int check_paged(const carve_paged_config* c) {
@@ -165,8 +188,6 @@ struct Plan {
   int64_t rows;              // partial results
   int64_t bytes;
 };
-
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_of(const carve_paged_config* c) {
   Plan p{};
@@ -264,13 +285,15 @@ extern "C" int carve_qk_norm_rope_fwd(const carve_rope_config* cfg, const void* 
   a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight;
   a.cos = cos; a.sin = sin; a.positions = positions;
   a.qo = q_out; a.ko = k_out;
-  const int per = carve::kRopeThreads / (c.d * (int)es / 16) * carve::kRopeRows;
-  a.blocks_q = blocks_for(c.N * c.Hq, per);
-  a.blocks = a.blocks_q + blocks_for(c.N * c.Hk, per);
+  const TokenWaves w = token_waves(c.N, (int64_t)c.Hq + c.Hk, c.d, c.dtype);
+  if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
-    hipLaunchKernelGGL((carve::norm_rope_kernel<decltype(t), decltype(d)::value>), dim3(a.blocks),
-                       dim3(carve::kRopeThreads), 0, reinterpret_cast<hipStream_t>(stream), a);
-    return hipGetLastError();
+    return by_pieces(w.per_lane, [&](auto u) {
+      hipLaunchKernelGGL((carve::norm_rope_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
+                         dim3((unsigned)up(c.N, carve::kRopeThreads / 64), w.per_token), dim3(carve::kRopeThreads), 0,
+                         reinterpret_cast<hipStream_t>(stream), a);
+      return hipGetLastError();
+    });
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);
 }
@@ -413,14 +436,15 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   a.interleaved = (c.flags & CARVE_ROPE_INTERLEAVED) != 0;
   a.norm = norm;
   a.eps = c.eps;
-  const int64_t pieces = ((int64_t)c.Hq + 2 * (int64_t)c.Hk) * (c.d * (int)es / 16);
-  const int64_t parts = (pieces + 64 * carve::kAppendPieces - 1) / (64 * carve::kAppendPieces);
-  if (parts > 65535) return CARVE_EUNSUPPORTED;
+  const TokenWaves w = token_waves(c.N, (int64_t)c.Hq + 2 * (int64_t)c.Hk, c.d, c.dtype);
+  if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
-    hipLaunchKernelGGL((carve::paged_append_kernel<decltype(t), decltype(d)::value>),
-                       dim3((unsigned)((c.N + 3LL) / 4), (unsigned)parts), dim3(256), 0,
-                       reinterpret_cast<hipStream_t>(stream), a);
-    return hipGetLastError();
+    return by_pieces(w.per_lane, [&](auto u) {
+      hipLaunchKernelGGL((carve::paged_append_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
+                         dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                         a);
+      return hipGetLastError();
+    });
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);
 }

@@ -694,17 +694,22 @@ struct TileWork {
   // Scores of block t that a row does not see. Lane: row c, keys 32 kb2 + 8 (u / 4) + 4 hf + u % 4.
   __device__ __forceinline__ void mask(int t, unsigned long long ok, f32x16 (&s)[2]) const {
     const int j0 = (first_b + t) * LY::BN;
-    if (ok != ~0ull || j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+    if (ok != ~0ull) {                              // keys that do not exist
       const unsigned long long mine = ok >> (4 * hf);
-      const int far = p - j0 - 4 * hf, near = a.window > 0 ? far - a.window : -1000000;   // visible: near < key <= far
 #pragma unroll
       for (int kb2 = 0; kb2 < 2; ++kb2)
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int kk = 32 * kb2 + 8 * (u / 4) + u % 4;
-          const bool see = ((mine >> kk) & 1ull) && kk <= far && kk > near;
-          s[kb2][u] = see ? s[kb2][u] : -__builtin_inff();
-        }
+        for (int u = 0; u < 16; ++u)
+          s[kb2][u] = (mine >> (32 * kb2 + 8 * (u / 4) + u % 4)) & 1ull ? s[kb2][u] : -__builtin_inff();
+    }
+    if (j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+      const int far = p - j0 - 4 * hf;              // visible: far - window < key <= far
+      const unsigned wide = a.window > 0 ? a.window : 0x7fffffff;
+#pragma unroll
+      for (int kb2 = 0; kb2 < 2; ++kb2)
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          s[kb2][u] = (unsigned)(far - (32 * kb2 + 8 * (u / 4) + u % 4)) < wide ? s[kb2][u] : -__builtin_inff();
     }
   }
   // Moves the row's reference up to `top` where that has grown far enough.

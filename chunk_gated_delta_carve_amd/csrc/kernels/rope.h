@@ -11,11 +11,14 @@
 // dn = dz w:  dx = r (dn - n mean(dn n)).
 //
 // Every lane holds one 16-byte piece of a row, so a row is D sizeof(E) / 16
-// neighbouring lanes and its sums are xor shuffles inside them. In the
-// half-split form a lane gets its partner piece from the lane that holds it
-// (one shuffle per dword of raw input), so each input byte is read once.
-// All of it is bound by memory: about 25 vector instructions per 16 bytes
-// read against the ~60 that fit in the time HBM needs for them.
+// neighbouring lanes, its sums are lane exchanges inside them, and in the
+// half-split form a lane gets its partner channels from the lane that holds them:
+// each input byte is read once. Forward, a wave takes the heads of one token, so
+// the position, the angles and (for the cache) the page are found once for up to
+// 256 pieces. All of it is bound by memory once an instruction count of about 120
+// per piece is out of the way: a wave per token took the forward pass of 8192
+// tokens, 24 heads of 64 from 15.6 us (a lane per row piece, 250 instructions) to
+// 12.4 us.
 #pragma once
 #include "common.h"
 
@@ -66,23 +69,29 @@ template <> struct Piece<float> {
 // sum over the W neighbouring lanes of a row (W = 8, 16 or 32), in each of them
 template <int W>
 __device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < W; m <<= 1) x += __shfl_xor(x, m);
+  x += dpp_mov<0xB1>(x);                            // lane xor 1
+  x += dpp_mov<0x4E>(x);                            // xor 2: the quads' sums
+  x += dpp_mov<0x141>(x);                           // mirrored in 8 lanes: the other quad's
+  if constexpr (W > 8) x += dpp_mov<0x140>(x);      // mirrored in 16
+  if constexpr (W > 16) x = sum_row_pairs(x);
   return x;
 }
 
-// What a lane does in a rotation: which piece holds its partners and where its angles are.
+// What a lane does in a rotation: which piece it holds, which lane holds the
+// partners of its channels, and where its angles are.
 template <typename E, int D>
 struct Turn {
   static constexpr int V = Piece<E>::V, LPR = D / V;
-  int c, partner;                      // own piece of the row, the lane that holds the partners
+  int c, partner;
   int angle;                           // first table column
-  bool turns;                          // whether the piece is rotated at all
+  bool turns, all;                     // whether the piece is rotated at all; whether every piece of a row is
+  bool inter;
   float sign;                          // half-split: -1 in the first half, +1 in the second
-  __device__ __forceinline__ Turn(int rot, bool inter) {
+  __device__ __forceinline__ Turn(int rot, bool interleaved) : inter(interleaved) {
     const int lane = lane_id(), half = rot / 2 / V;          // pieces per half
     c = lane % LPR;
     turns = c * V < rot;
+    all = rot == D;
     if (inter) {
       partner = lane; angle = c * (V / 2); sign = 0.f;
     } else {
@@ -92,16 +101,11 @@ struct Turn {
       sign = up ? 1.f : -1.f;
     }
   }
-  __device__ __forceinline__ u32x4 swap(u32x4 r) const {     // the partner's raw piece
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (unsigned)__shfl((int)r[i], partner);
-    return o;
-  }
-  // Cosines and sines of the lane's channels at position p; a position outside
-  // the table turns by NaN, so its outputs are NaN.
+  // Cosines of the lane's channels at position p and sines with the sign that
+  // y = z cos + partner sin has them with (back: of the inverse rotation). A
+  // position outside the table turns by NaN, so its outputs are NaN.
   __device__ __forceinline__ void angles(const float* cos, const float* sin, int rot, int table_len, int64_t p,
-                                         bool inter, float (&cs)[V], float (&sn)[V]) const {
+                                         bool back, float (&cs)[V], float (&sn)[V]) const {
 #pragma unroll
     for (int i = 0; i < V; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
     if (!turns) return;
@@ -112,112 +116,101 @@ struct Turn {
     }
     const float* pc = cos + p * (rot / 2) + angle;
     const float* ps = sin + p * (rot / 2) + angle;
+    const float b = back ? -1.f : 1.f;
     if (inter) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) { cs[2 * i] = cs[2 * i + 1] = pc[i]; sn[2 * i] = sn[2 * i + 1] = ps[i]; }
+      for (int i = 0; i < V / 2; ++i) {
+        cs[2 * i] = cs[2 * i + 1] = pc[i];
+        sn[2 * i] = -b * ps[i];
+        sn[2 * i + 1] = b * ps[i];
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(pc + i), b = *reinterpret_cast<const f32x4*>(ps + i);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(pc + i), y = *reinterpret_cast<const f32x4*>(ps + i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) { cs[i + j] = a[j]; sn[i + j] = b[j]; }
+        for (int j = 0; j < 4; ++j) { cs[i + j] = x[j]; sn[i + j] = b * sign * y[j]; }
       }
     }
   }
-  // y = R z (back: R^T z) from the lane's channels z and the partners' zp
-  __device__ __forceinline__ void turn(const float (&z)[V], const float (&zp)[V], const float (&cs)[V],
-                                       const float (&sn)[V], bool inter, bool back, float (&y)[V]) const {
+  // y = z cos + partner sin, rounded in this order for every caller
+  __device__ __forceinline__ void turn(const float (&z)[V], const float (&cs)[V], const float (&sn)[V],
+                                       float (&y)[V]) const {
 #pragma clang fp contract(off)
-    if (!turns) {
+    float zp[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = z[i];
-    } else if (inter) {
+    for (int i = 0; i < V; ++i) zp[i] = inter ? z[i ^ 1] : __shfl(z[i], partner);
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float s = back ? -sn[i] : sn[i];
-        y[i] = __builtin_fmaf(z[i], cs[i], -(z[i + 1] * s));
-        y[i + 1] = __builtin_fmaf(z[i + 1], cs[i], z[i] * s);
-      }
-    } else {
-      const float sg = back ? -sign : sign;
+    for (int i = 0; i < V; ++i) y[i] = __builtin_fmaf(z[i], cs[i], zp[i] * sn[i]);
+    if (!all) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = __builtin_fmaf(z[i], cs[i], sg * (zp[i] * sn[i]));
+      for (int i = 0; i < V; ++i) y[i] = turns ? y[i] : z[i];
     }
   }
 };
 
-// Weights of a lane's own piece and of its partners' piece (1 when absent).
+// A lane's piece of a weight vector, or of ones.
 template <typename E, int D>
-__device__ __forceinline__ void load_weights(const void* w, const Turn<E, D>& t, float (&wo)[Piece<E>::V],
-                                             float (&wp)[Piece<E>::V]) {
-  constexpr int V = Piece<E>::V, LPR = D / V;
-  if (w) {
-    const u32x4* p = static_cast<const u32x4*>(w);
-    Piece<E>::open(p[t.c], wo);
-    Piece<E>::open(p[t.partner % LPR], wp);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) wo[i] = wp[i] = 1.f;
-  }
+__device__ __forceinline__ u32x4 weight_piece(const void* w, int c) {
+  constexpr unsigned one = sizeof(E) == 2 ? 0x3f803f80u : 0x3f800000u;
+  return w ? static_cast<const u32x4*>(w)[c] : u32x4{one, one, one, one};
 }
 
 // The one place that norms and rotates forward, for both entry points that do:
 // products and sums are fused where they say so and nowhere else, so both give
 // the same bits.
 template <typename E, int D>
-__device__ __forceinline__ u32x4 norm_rope_piece(u32x4 raw, const Turn<E, D>& t, const float (&wo)[Piece<E>::V],
-                                                 const float (&wp)[Piece<E>::V], const float (&cs)[Piece<E>::V],
-                                                 const float (&sn)[Piece<E>::V], bool norm, bool inter, float eps) {
+__device__ __forceinline__ u32x4 norm_rope_piece(u32x4 raw, const Turn<E, D>& t, u32x4 weight,
+                                                 const float (&cs)[Piece<E>::V], const float (&sn)[Piece<E>::V],
+                                                 bool norm, float eps) {
 #pragma clang fp contract(off)
   constexpr int V = Piece<E>::V, LPR = D / V;
-  float x[V], xp[V], y[V];
+  float x[V], y[V];
   Piece<E>::open(raw, x);
-  Piece<E>::open(inter ? raw : t.swap(raw), xp);
-  float r = 1.f;
   if (norm) {
+    float w[V];
+    Piece<E>::open(weight, w);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
-    r = 1.f / sqrtf(__builtin_fmaf(row_sum<LPR>(ss), 1.f / D, eps));
-  }
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum<LPR>(ss), 1.f / D, eps));   // within 2^-23
 #pragma unroll
-  for (int i = 0; i < V; ++i) { x[i] = x[i] * r * wo[i]; xp[i] = xp[i] * r * wp[i]; }
-  t.turn(x, xp, cs, sn, inter, false, y);
+    for (int i = 0; i < V; ++i) x[i] = x[i] * r * w[i];
+  }
+  t.turn(x, cs, sn, y);
   return Piece<E>::close(y);
 }
 
-constexpr int kRopeThreads = 256, kRopeRows = 2;   // rows per row slot of a forward block
+constexpr int kRopeThreads = 256, kRopePieces = 4;   // most pieces per lane of a forward wave
 
-template <typename E, int D>
+// One wave per token and 64 U pieces of its rows (q's heads, then k's).
+template <typename E, int D, int U>
 __global__ __launch_bounds__(kRopeThreads) void norm_rope_kernel(RopeArgs a) {
-  constexpr int V = Piece<E>::V, LPR = D / V, RPB = kRopeThreads / LPR;
-  const bool isq = (int)blockIdx.x < a.blocks_q;
-  const unsigned H = isq ? a.Hq : a.Hk;
-  const int64_t rows = a.N * H, in_row = isq ? a.q_row : a.k_row, out_row = isq ? a.qo_row : a.ko_row;
-  const E* in = static_cast<const E*>(isq ? a.q : a.k);
-  E* out = static_cast<E*>(isq ? a.qo : a.ko);
+  constexpr int V = Piece<E>::V, LPR = D / V;
+  const int64_t n = (int64_t)blockIdx.x * (kRopeThreads / 64) + wave_id();
+  if (n >= a.N) return;
   const Turn<E, D> t(a.rot, a.interleaved);
-  float wo[V], wp[V];
-  load_weights<E, D>(isq ? a.wq : a.wk, t, wo, wp);
-  const int64_t first = (int64_t)(isq ? blockIdx.x : blockIdx.x - a.blocks_q) * (RPB * kRopeRows) + threadIdx.x / LPR;
-  u32x4 raw[kRopeRows];
-  int64_t n[kRopeRows], p[kRopeRows];
-  unsigned h[kRopeRows];
+  const int heads = a.Hq + a.Hk;
+  u32x4 raw[U];
 #pragma unroll
-  for (int j = 0; j < kRopeRows; ++j) {
-    int64_t row = first + j * RPB;
-    if (row >= rows) row = rows - 1;               // computed again, not stored
-    n[j] = (unsigned)row / H;                      // rows < 2^31, checked on the host
-    h[j] = (unsigned)row - (unsigned)n[j] * H;
-    raw[j] = *reinterpret_cast<const u32x4*>(in + n[j] * in_row + (int64_t)h[j] * D + t.c * V);
-    p[j] = a.positions ? a.positions[n[j]] : (unsigned)n[j] % (unsigned)a.T;
+  for (int u = 0; u < U; ++u) {
+    const int hh = ((blockIdx.y * U + u) * 64 + lane_id()) / LPR, h = hh < heads ? hh : heads - 1;
+    const E* src = h < a.Hq ? static_cast<const E*>(a.q) + n * a.q_row + h * D
+                            : static_cast<const E*>(a.k) + n * a.k_row + (h - a.Hq) * D;
+    raw[u] = *reinterpret_cast<const u32x4*>(src + t.c * V);
   }
+  const int64_t p = a.positions ? a.positions[n] : n % a.T;
+  float cs[V], sn[V];
+  t.angles(a.cos, a.sin, a.rot, a.table_len, p, false, cs, sn);
+  const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
 #pragma unroll
-  for (int j = 0; j < kRopeRows; ++j) {
-    float cs[V], sn[V];
-    t.angles(a.cos, a.sin, a.rot, a.table_len, p[j], a.interleaved, cs, sn);
-    const u32x4 y = norm_rope_piece<E, D>(raw[j], t, wo, wp, cs, sn, a.norm, a.interleaved, a.eps);
-    if (first + j * RPB < rows) *reinterpret_cast<u32x4*>(out + n[j] * out_row + (int64_t)h[j] * D + t.c * V) = y;
+  for (int u = 0; u < U; ++u) {
+    const int h = ((blockIdx.y * U + u) * 64 + lane_id()) / LPR;
+    const u32x4 y = norm_rope_piece<E, D>(raw[u], t, h < a.Hq ? wq : wk, cs, sn, a.norm, a.eps);
+    if (h >= heads) continue;
+    E* dst = h < a.Hq ? static_cast<E*>(a.qo) + n * a.qo_row + h * D
+                      : static_cast<E*>(a.ko) + n * a.ko_row + (h - a.Hq) * D;
+    *reinterpret_cast<u32x4*>(dst + t.c * V) = y;
   }
 }
 
@@ -238,8 +231,8 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_bwd_kernel(RopeArgs a)
   E* dx_ = static_cast<E*>(isq ? a.dq : a.dk);
   const void* w = isq ? a.wq : a.wk;
   const Turn<E, D> t(a.rot, a.interleaved);
-  float wo[V], wp[V], dw[V];
-  load_weights<E, D>(w, t, wo, wp);
+  float wo[V], dw[V];
+  Piece<E>::open(weight_piece<E, D>(w, t.c), wo);
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = 0.f;
   const int block = isq ? blockIdx.x : blockIdx.x - a.blocks_q, blocks = isq ? a.blocks_q : a.blocks - a.blocks_q;
@@ -252,19 +245,18 @@ __global__ __launch_bounds__(kRopeThreads) void norm_rope_bwd_kernel(RopeArgs a)
     const u32x4 xr = *reinterpret_cast<const u32x4*>(x_ + n * x_row + h * D + t.c * V);
     const u32x4 gr = *reinterpret_cast<const u32x4*>(dy_ + n * dy_row + h * D + t.c * V);
     const int64_t p = a.positions ? a.positions[n] : (unsigned)n % (unsigned)a.T;
-    float cs[V], sn[V], x[V], g[V], gp[V], dz[V];
-    t.angles(a.cos, a.sin, a.rot, a.table_len, p, a.interleaved, cs, sn);
+    float cs[V], sn[V], x[V], g[V], dz[V];
+    t.angles(a.cos, a.sin, a.rot, a.table_len, p, true, cs, sn);
     Piece<E>::open(xr, x);
     Piece<E>::open(gr, g);
-    Piece<E>::open(a.interleaved ? gr : t.swap(gr), gp);
-    t.turn(g, gp, cs, sn, a.interleaved, true, dz);
+    t.turn(g, cs, sn, dz);
     if (a.norm) {
       float ss = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) { ss += x[i] * x[i]; dot += dz[i] * wo[i] * x[i]; }
       ss = row_sum<LPR>(ss);
       dot = row_sum<LPR>(dot);
-      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      const float r = __builtin_amdgcn_rsqf(ss * (1.f / D) + a.eps);
       const float m = dot * r * (1.f / D);         // mean(dn n)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -343,13 +335,11 @@ struct AppendArgs {
   float eps;
 };
 
-constexpr int kAppendPieces = 4;                    // 16-byte pieces per lane
-
-// One wave per token and 256 pieces of its rows (q's, k's and v's heads): the
+// One wave per token and 64 U pieces of its rows (q's, k's and v's heads): the
 // sequence, position and page are found once per wave. A token whose position
 // is negative, lies past the block table or falls on a page number outside the
 // cache is not stored.
-template <typename E, int D>
+template <typename E, int D, int U>
 __global__ __launch_bounds__(256) void paged_append_kernel(AppendArgs a) {
   constexpr int V = Piece<E>::V, LPR = D / V;
   const int n = blockIdx.x * 4 + wave_id();
@@ -369,12 +359,13 @@ __global__ __launch_bounds__(256) void paged_append_kernel(AppendArgs a) {
   const Turn<E, D> t(a.rot, a.interleaved);
   const int heads = a.Hq + 2 * a.Hk;
   float cs[V], sn[V];
-  t.angles(a.cos, a.sin, a.rot, a.table_len, pos, a.interleaved, cs, sn);
-  u32x4 raw[kAppendPieces];
-  int hh[kAppendPieces];
+  t.angles(a.cos, a.sin, a.rot, a.table_len, pos, false, cs, sn);
+  const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
+  u32x4 raw[U];
+  int hh[U];
 #pragma unroll
-  for (int u = 0; u < kAppendPieces; ++u) {
-    hh[u] = ((blockIdx.y * kAppendPieces + u) * 64 + lane_id()) / LPR;
+  for (int u = 0; u < U; ++u) {
+    hh[u] = ((blockIdx.y * U + u) * 64 + lane_id()) / LPR;
     const int h = hh[u] < heads ? hh[u] : heads - 1;
     const E* src = h < a.Hq ? static_cast<const E*>(a.q) + n * a.q_row + h * D
                    : h < a.Hq + a.Hk ? static_cast<const E*>(a.k) + n * a.k_row + (h - a.Hq) * D
@@ -382,11 +373,9 @@ __global__ __launch_bounds__(256) void paged_append_kernel(AppendArgs a) {
     raw[u] = *reinterpret_cast<const u32x4*>(src + t.c * V);
   }
 #pragma unroll
-  for (int u = 0; u < kAppendPieces; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int h = hh[u];
-    float wo[V], wp[V];
-    load_weights<E, D>(h < a.Hq ? a.wq : a.wk, t, wo, wp);
-    const u32x4 y = norm_rope_piece<E, D>(raw[u], t, wo, wp, cs, sn, a.norm, a.interleaved, a.eps);
+    const u32x4 y = norm_rope_piece<E, D>(raw[u], t, h < a.Hq ? wq : wk, cs, sn, a.norm, a.eps);
     if (h < a.Hq) {
       *reinterpret_cast<u32x4*>(static_cast<E*>(a.qo) + n * a.qo_row + h * D + t.c * V) = y;
     } else if (h < heads && stored) {
