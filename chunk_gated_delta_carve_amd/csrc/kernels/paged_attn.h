@@ -13,9 +13,10 @@
 // c = scale log2 e. Products run transposed, X^T = K Q^T and O^T = V^T P^T: a
 // lane then owns one row (a column of the C tile), its maximum needs one or two
 // cross-lane steps, rescaling is lane-local, and P^T leaves the first product
-// in the very registers the second one wants as its B operand. Its only loss is
-// P rounded to the input type (bf16: half a step is 2^-9 of each weight; l sums
-// the unrounded ones).
+// in the very registers the second one wants as its B operand. In bf16 P has to be
+// rounded for that: with few rows it goes in as two parts of 8 bits each (free
+// beside the loads), with many as one, off by at most 2^-8 of each weight (a
+// second product would cost a third of the matrix time); l sums it unrounded.
 //
 // Masked keys never reach a row: their scores are replaced before use, pages
 // outside the cache and keys no row of the tile may see are loaded as zeros,
@@ -264,7 +265,7 @@ struct RowsLayout {
   static constexpr int BM = 16, KT = 32, BN = 128;                               // BN: keys per round of four waves
   // Workgroups per CU that registers allow without spills in the loop; so many
   // are launched, one stretch of the work each.
-  static constexpr int PER_CU = D == 128 ? 2 : sizeof(E) == 4 ? 3 : 4;
+    static constexpr int PER_CU = D == 128 ? 2 : 3;
   static constexpr int NP = D * (int)sizeof(E) / 64;                             // pieces per lane and key
   static constexpr int VLD = D * (int)sizeof(E) + (sizeof(E) == 2 ? 32 : 16);    // bytes per value row: spread banks
   static constexpr int OLD = D + 4;                                              // floats per row of a wave's result
@@ -499,13 +500,23 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
         l += s[b][i];
       }
     if constexpr (sizeof(E) == 2) {
+      // The weights go in as two bf16 parts, which leaves them 16 bits: the second
+      // product costs nothing beside the loads, and the output's own rounding is
+      // then the only one that counts.
       const bf16x8 pb = Mma<bf16>::pack(s);
+      f32x4 rest[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rest[b][i] = s[b][i] - (float)pb[4 * b + i];
+      const bf16x8 pr = Mma<bf16>::pack(rest);
       const char* src = vl + (4 * g + (lane & 15) / 4) * LY::VLD + (lane & 3) * 8;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         const s16x4 v0 = read_tr(src + 32 * d), v1 = read_tr(src + 32 * d + 16 * LY::VLD);
         const bf16x4 b0 = __builtin_bit_cast(bf16x4, v0), b1 = __builtin_bit_cast(bf16x4, v1);
-        o[d] = Mma<bf16>::mma(bf16x8{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]}, pb, o[d]);
+        const bf16x8 v = {b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+        o[d] = Mma<bf16>::mma(v, pr, Mma<bf16>::mma(v, pb, o[d]));
       }
     } else {
 #pragma unroll

@@ -432,6 +432,111 @@ def test_rows_behind_the_last_sequence_are_left(torch):
         assert (out[n:] == 5.0).all() and not (out[:n] == 5.0).all()
 
 
+@pytest.mark.parametrize("case", [
+    # dtype, Hq, Hk, d, page, sequences, window, step: more sequences than a wave has lanes
+    ("bf16", 4, 2, 64, 16, 150, 0, True),
+    ("bf16", 4, 2, 128, 16, 70, 20, False),
+    ("bf16", 8, 1, 64, 32, 90, 0, False),
+    ("f32", 2, 2, 64, 16, 129, 0, False),
+], ids=["step", "ragged", "tiles", "f32"])
+def test_many_sequences(torch, case):
+    from chunk_gated_delta_carve_amd import paged_append, paged_attention
+    dtype, Hq, Hk, d, page, S, window, step = case
+    rng = np.random.default_rng(18)
+    top = 14 if Hq // Hk < 8 else 60
+    n = [1] * S if step else list(rng.integers(0, top, S))
+    kv = [int(x + rng.integers(0, 90)) if x else 0 for x in n]
+    cu, lens, table, pages = ragged(torch, 19, S, n, kv, page)
+    kc, vc = cache(torch, "plain", pages, page, Hk, d, dtype, 190)
+    N = sum(n)
+    q, k, v = (rand(torch, 192 + i, (N, h, d), dtype) for i, h in enumerate((Hq, Hk, Hk)))
+    args = (ints(torch, table), ints(torch, lens), None if step else ints(torch, cu))
+    before = f64(kc), f64(vc)
+    paged_append(k, v, kc, vc, *args)
+    ref = orc.paged_append(f64(k), f64(v), *before, table, lens, cu, page)
+    assert np.array_equal(f64(kc), ref[0]) and np.array_equal(f64(vc), ref[1])
+    out, lse = paged_attention(q, kc, vc, *args, window=window, return_lse=True)
+    check_attention(torch, out, lse, q, kc, vc, table, lens, cu, d ** -0.5, window, dtype)
+
+
+@pytest.mark.parametrize("dtype,d,n,growth", [("bf16", 64, 1, 3.0), ("bf16", 128, 3, 12.0), ("f32", 64, 2, 3.0),
+                                              ("bf16", 64, 100, 3.0), ("bf16", 128, 100, 0.5), ("bf16", 128, 100, 12.0),
+                                              ("bf16", 64, 100, -3.0)])
+def test_scores_that_grow_along_the_context(torch, dtype, d, n, growth):
+    """Scores that rise (or fall) by `growth` every 64 keys: the reference of the running softmax follows in small
+    steps, in large ones, or stays."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    kv = 700
+    cu, lens, table, pages = ragged(torch, 20, 1, [n], [kv], 16)
+    kc, vc = cache(torch, "plain", pages, 16, 1, d, dtype, 200)
+    q = rand(torch, 202, (n, 4, d), dtype, 0.3)
+    q[..., 0] = 4.0
+    j = torch.arange(len(table[0]) * 16, device="cuda").view(-1, 16)
+    kc[ints(torch, table[0]).long(), :, 0, 0] = (j * (growth / 64 / 4)).to(kc.dtype)
+    out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), scale=1.0,
+                               return_lse=True)
+    check_attention(torch, out, lse, q, kc, vc, table, lens, cu, 1.0, 0, dtype)
+
+
+def test_extreme_scores(torch):
+    """One weight of 1 and the rest 0; scores far beyond what fp32 exponentials reach, at the largest scale."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    for dtype, n in (("bf16", 2), ("bf16", 90), ("f32", 2)):
+        cu, lens, table, pages = ragged(torch, 21, 1, [n], [200], 16)
+        kc, vc = cache(torch, "plain", pages, 16, 1, 64, dtype, 210)
+        q = rand(torch, 212, (n, 2, 64), dtype, 3.0)
+        out, lse = paged_attention(q, kc * 3, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), scale=16.0,
+                                   return_lse=True)
+        ref = orc.paged_attention(f64(q), f64(kc * 3), f64(vc), table, lens, cu, 16.0, 0)
+        # the score error e moves weight between values that differ by up to 2 max|v|, where the mean of |v| that
+        # the bound counts can be small
+        bo, bl = attention_bounds(dtype, 64, 16.0, *ref)
+        close("lse", lse, ref[1], bl)
+        close("o", out, ref[0], bo + 2 * np.abs(bl)[..., None] * np.max(np.abs(f64(vc))))
+
+
+def test_offsets_past_32_bits(torch):
+    """Pages whose elements lie past 2^31 (and bytes past 2^32) of a cache of 2.3 * 10^9 elements."""
+    from chunk_gated_delta_carve_amd import paged_append, paged_attention
+    page, Hk, d = 64, 4, 128
+    pages = 71000
+    kc = torch.empty(pages, page, Hk, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    assert kc.numel() > 2 ** 31
+    small = list(range(pages - 6, pages))
+    for c, seed in ((kc, 220), (vc, 221)):
+        c[small] = rand(torch, seed, (6, page, Hk, d), "bf16")
+    for n, kv in ((1, 300), (70, 300)):
+        table = np.array([[pages - 1, pages - 5, pages - 3, pages - 2, pages - 6]])
+        lens, cu = ints(torch, [kv]), ints(torch, [0, n])
+        q, k, v = (rand(torch, 222 + i, (n, h, d), "bf16") for i, h in enumerate((8, Hk, Hk)))
+        paged_append(k, v, kc, vc, ints(torch, table), lens, cu)
+        out, lse = paged_attention(q, kc, vc, ints(torch, table), lens, cu, return_lse=True)
+        lo = table - (pages - 6)                 # the same six pages as a cache of their own
+        assert torch.equal(kc[int(table[0, (kv - 1) // page]), (kv - 1) % page], k[-1])
+        check_attention(torch, out, lse, q, kc[small], vc[small], lo, [kv], [0, n], d ** -0.5, 0, "bf16")
+
+
+def test_calls_on_two_streams(torch):
+    """Two calls under way at once, each with a workspace of its own, have the bits of calls one by one."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    calls = []
+    for seed, (n, kv, d) in enumerate(((1, 9000, 128), (200, 4000, 64))):
+        cu, lens, table, pages = ragged(torch, 23 + seed, 2, [n, n], [kv, kv - 7], 16)
+        kc, vc = cache(torch, "plain", pages, 16, 2, d, "bf16", 230 + 2 * seed)
+        calls.append((rand(torch, 235 + seed, (2 * n, 8, d), "bf16"), kc, vc, ints(torch, table), ints(torch, lens),
+                      ints(torch, cu)))
+    want = [paged_attention(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        got = [paged_attention(*c, stream=s) for c, s in zip(calls, streams)]
+        for s in streams:
+            s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_strided_queries_and_outputs(torch):
     """q as a part of one projection's output, o into a part of a wider tensor, a table that is a slice."""
     from chunk_gated_delta_carve_amd import paged_attention
