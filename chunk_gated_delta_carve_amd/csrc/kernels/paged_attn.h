@@ -979,7 +979,7 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
     return *reinterpret_cast<const bf16x8*>(kl + 32 * (i & 1) * LY::KLD + 32 * (i >> 1));
   };
   // O^T: product i is keys 16 (i / ND) .. of the block, channels 32 (i % ND) ..
-  constexpr int ND = D / 32, NV = 4 * ND, RV = 4;
+  constexpr int ND = D / 32, NV = 4 * ND, RV = 6;
   const char* v_src = vlds + (4 * w.hf + (w.lane & 15) / 4) * LY::VLD + ((w.lane >> 4) & 1) * 32 + (w.lane & 3) * 8;
   auto read_v = [&](const char* vl, int i, s16x4 (&v)[2]) {
     const char* at = vl + 16 * (i / ND) * LY::VLD + 64 * (i % ND);
