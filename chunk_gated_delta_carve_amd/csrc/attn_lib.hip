@@ -195,7 +195,7 @@ Plan plan_of(const carve_paged_config* c) {
   const int64_t G = c->Hq / c->Hk;
   const bool step = (c->flags & CARVE_PAGED_STEP) != 0;
   p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)kRowsPerSeq * c->S;
-  const int waves = c->d == 64 ? kTileWaves<64> : kTileWaves<128>, per_cu = c->d == 64 ? 3 : 1;   // of the tile kernels
+  const int waves = c->d == 64 ? kTileWaves<64> : kTileWaves<128>, per_cu = c->d == 64 ? 4 : 1;   // of the tile kernels
   const int BM = p.tile ? 32 * waves : 16, BN = p.tile ? 64 : 128;
   p.tiles = step ? c->S * up(G, BM) : (int64_t)c->N * G / BM + c->S;
   int64_t keys = (int64_t)c->width * c->page_size;

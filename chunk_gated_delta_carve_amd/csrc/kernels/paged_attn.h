@@ -96,22 +96,37 @@ __device__ __forceinline__ AttnTile find_tile(const PagedArgs& a, int t, int BM)
     if (s >= a.S || s >= a.N) return none;
     return tile_of_rows(a, s, s, 1, first_position(a, s, 1), (t - s * per) * BM, BM);
   }
-  int lo = 0, len = a.S;                            // as find_sequence, over the tiles' starts
-  while (len > 0) {
-    const int step = (len + 63) >> 6, at = (lane_id() + 1) * step;
-    const bool past = at <= len && (int64_t)a.cu[lo + at] * a.G / BM + lo + at <= t;
-    const int k = __popcll(__ballot(past));
-    lo += k * step;
-    len = step - 1 < len - k * step ? step - 1 : len - k * step;
+  int lo = 0, n0, n1, pos0;
+  if (a.S <= 64) {                                  // a lane per sequence: everything about it in one trip to memory
+    const int s = lane_id() < a.S ? lane_id() : a.S - 1;
+    const int c0 = a.cu[s], c1 = a.cu[s + 1], kv = a.kv_lens[s];
+    const bool past = lane_id() < a.S && (int64_t)c1 * a.G / BM + lane_id() + 1 <= t;
+    lo = __popcll(__ballot(past));
+    if (lo >= a.S) return none;
+    n0 = __builtin_amdgcn_readlane(c0, lo);
+    n1 = __builtin_amdgcn_readlane(c1, lo);
+    pos0 = __builtin_amdgcn_readlane(kv, lo);
+    n1 = n1 < a.N ? n1 : a.N;
+    pos0 = (pos0 > 0 ? pos0 : 0) - (n1 - n0);
+  } else {                                          // as find_sequence, over the tiles' starts
+    int len = a.S;
+    while (len > 0) {
+      const int step = (len + 63) >> 6, at = (lane_id() + 1) * step;
+      const bool past = at <= len && (int64_t)a.cu[lo + at] * a.G / BM + lo + at <= t;
+      const int k = __popcll(__ballot(past));
+      lo += k * step;
+      len = step - 1 < len - k * step ? step - 1 : len - k * step;
+    }
+    if (lo >= a.S) return none;
+    n0 = a.cu[lo];
+    n1 = a.cu[lo + 1];
+    n1 = n1 < a.N ? n1 : a.N;
+    pos0 = first_position(a, lo, n1 - n0);
   }
-  if (lo >= a.S) return none;
-  const int n0 = a.cu[lo];
-  int n1 = a.cu[lo + 1];
-  n1 = n1 < a.N ? n1 : a.N;
   if (n0 < 0 || n1 <= n0) return none;
   const int64_t row0 = (t - ((int64_t)n0 * a.G / BM + lo)) * BM;
   if (row0 < 0 || row0 >= (int64_t)(n1 - n0) * a.G) return none;
-  return tile_of_rows(a, lo, n0, n1 - n0, first_position(a, lo, n1 - n0), (int)row0, BM);
+  return tile_of_rows(a, lo, n0, n1 - n0, pos0, (int)row0, BM);
 }
 
 // Blocks of BN keys per workgroup when a tile's keys are dealt to several: the
@@ -260,6 +275,8 @@ __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x)
 // see, are laid end to end, and every workgroup takes an equal stretch of blocks.
 // An item that ends up in several workgroups leaves partial results: a workgroup
 // has at most two, the item its stretch starts inside of and the one it ends in.
+// 64 sequences of 200 to 8192 keys, 4 heads of 128 (551 MB): 110 us, 5.0 TB/s, the
+// rate of a large copy; with a fixed number of shares per sequence 132 us.
 template <typename E, int D>
 struct RowsLayout {
   static constexpr int BM = 16, KT = 32, BN = 128;                               // BN: keys per round of four waves
@@ -780,13 +797,16 @@ struct TileWork {
   }
 };
 
-// d = 64: four waves, each block in turn (products, softmax, products), three
+// d = 64: four waves, each block in turn (products, softmax, products), four
 // workgroups per CU that fill each other's waits. Vector work outweighs the
 // products here (130 vector instructions of a softmax block against 16 products),
-// and three waves per SIMD issue it faster than two that interleave: the kernel
-// below took 133 us on the windowed prompts (51 GFLOP), this one 107 us.
+// and four waves per SIMD issue it faster than two that interleave: on ragged
+// windowed prompts (51 GFLOP) the kernel below took 133 us when this one, then
+// with three workgroups per CU, took 107 us; now about 98 us. In the loop the matrix
+// units are busy 57% of the time; a workgroup of 18 blocks spends an eighth of its
+// time on finding its tile and its first loads.
 template <int D, bool WIDE>
-__global__ __launch_bounds__(256, 2) void paged_tile_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, 4) void paged_tile_kernel(PagedArgs a) {
   using W = TileWork<D, 4, WIDE>;
   using LY = typename W::LY;
   extern __shared__ __align__(16) char lds[];
@@ -900,8 +920,9 @@ __global__ __launch_bounds__(256, 2) void paged_tile_kernel(PagedArgs a) {
 // "pair p" is keys p + 1 and values p. Step t, between two barriers, writes pair
 // t + 1 (keys t + 2 over keys t, read in step t - 1; values t + 1 over values
 // t - 1, likewise) while it reads keys t + 1 and values t.
-// 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 544 us, 885 TFLOP/s, where
-// the kernel above takes 620 us.
+// 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 528 us, 911 TFLOP/s, where
+// the kernel above takes 600 us. Those are 256 workgroups of 192 to 256 blocks on
+// 256 CUs: the longest decides, an eighth above the mean.
 template <int D, bool WIDE>
 __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
   using W = TileWork<D, 8, WIDE>;
@@ -1089,7 +1110,7 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
 // Joins the partial results of one (token, query head) per workgroup. Every wave
 // forms the joint statistics (a lane per share) and takes every fourth share's
 // output with eight loads in flight; the four sums meet in LDS. The order is
-// fixed by the lengths alone.
+// fixed by the lengths alone. 4 to 7 us, of which finding the shares is most.
 template <typename E, int D>
 __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t first, int64_t next, int64_t stride, int count) {
   // partial index of share i: first for i = 0, next + (i - 1) stride from there on
