@@ -92,7 +92,8 @@ class _On:
         self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(device))
         if handle is not None and handle != torch._C._cuda_getCurrentRawStream(device.index):
-            self.stack.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)))
+            s = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+            self.stack.enter_context(torch.cuda.stream(s))
 
     def __enter__(self):
         return self

@@ -57,6 +57,7 @@ bool bad_rows(int64_t n, int64_t row, int64_t len, int dtype, bool written) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kFewWaves = 4096;   // four waves per SIMD
+constexpr int kWideJoin = 32;          // shares per item from which a workgroup joins a row, not a wave
 
 // Blocks of the gradient: four per CU share the rows of q and k in proportion,
 // each tensor at least one where it has rows.
@@ -217,7 +218,7 @@ Plan plan_of(const carve_paged_config* c) {
     p.shares = (int)(blocks < want ? blocks : want);
     p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
   }
-  p.bytes = p.rows * (c->d + 2) * 4;
+  p.bytes = (p.rows * (c->d + 2) + (p.tile || p.shares < 2 ? 0 : (int64_t)p.shares * carve::kCutInts)) * 4;
   return p;
 }
 
@@ -237,7 +238,7 @@ hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL((carve::paged_tile_combine_kernel<LY::BM, LY::BN, LY::LEAST, D>),
-                     dim3((unsigned)((int64_t)a.N * a.Hq)), dim3(256), 0, s, a);
+                     dim3((unsigned)up((int64_t)a.N * a.Hq, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -248,8 +249,14 @@ hipError_t dispatch_attention(const carve::PagedArgs& a, bool tile, hipStream_t 
   hipLaunchKernelGGL((carve::paged_rows_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.shares == 1) return e;
-  hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D>), dim3((unsigned)((int64_t)a.N * a.Hq)), dim3(256), 0, s,
-                     a);
+  constexpr int BM = carve::RowsLayout<E, D>::BM;
+  const int64_t most = (a.cu ? a.N : 1) * (int64_t)a.G;      // rows of an item
+  const int rows = (int)(most < BM ? most : BM);
+  const int64_t items = a.Hk * (up((int64_t)a.N * a.G, BM) > a.S ? up((int64_t)a.N * a.G, BM) : a.S);
+  if (a.shares >= kWideJoin * items)
+    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(a.shares, rows), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 1>), dim3(a.shares, up(rows, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -514,6 +521,7 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
   a.o = o; a.lse = lse;
   a.po = static_cast<float*>(workspace);
   a.pml = plan.bytes ? a.po + plan.rows * c.d : nullptr;
+  a.cuts = plan.bytes ? reinterpret_cast<int*>(a.pml + plan.rows * 2) : nullptr;
   a.q_row = c.q_row; a.o_row = c.o_row; a.table_row = c.table_row;
   a.kc_page = c.kc_page; a.kc_tok = c.kc_tok; a.kc_head = c.kc_head;
   a.vc_page = c.vc_page; a.vc_tok = c.vc_tok; a.vc_head = c.vc_head;

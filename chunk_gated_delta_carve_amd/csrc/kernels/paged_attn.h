@@ -43,6 +43,7 @@ struct PagedArgs {
   void* o;
   float* lse;                                       // [N][Hq] or NULL
   float *po, *pml;                                  // partial results (o, and m with l)
+  int* cuts;                                        // row kernel: kCutInts per workgroup
   int64_t q_row, o_row, table_row;
   int64_t kc_page, kc_tok, kc_head, vc_page, vc_tok, vc_head;
   int N, S, Hq, Hk, G, width, pages, page_shift, window;
@@ -354,9 +355,11 @@ __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN
   p.run = (a.S + 63) >> 6;
   p.own = RowsWork{};
   int sum = 0;
+#pragma unroll 4
   for (int i = 0; i < p.run; ++i) {
     const int s = lane_id() * p.run + i;
-    if (s < a.S) { p.own = rows_work(a, s, BM, BN); sum += p.own.blocks(); }
+    const RowsWork w = rows_work(a, s < a.S ? s : a.S - 1, BM, BN);
+    if (s < a.S) { p.own = w; sum += w.blocks(); }
   }
   int incl = sum;
 #pragma unroll
@@ -372,6 +375,11 @@ __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN
   return p;
 }
 
+// What a workgroup notes down about the item that starts in its stretch and goes on
+// behind it: first token of the sequence, first row, rows (0: there is none), head,
+// and the number of workgroups that hold parts of it.
+constexpr int kCutInts = 8;                         // of workspace per workgroup
+
 template <typename E, int D>
 __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
@@ -381,6 +389,8 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   __shared__ int bad[16];
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
+  int* cut = a.cuts + blockIdx.x * kCutInts;
+  if (threadIdx.x == 0 && a.shares > 1) cut[2] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);
   const int end_block = plan.start(blockIdx.x + 1);
@@ -396,12 +406,17 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   }
   const int item = (at_block - seq_block) / w.nb, blk = at_block - seq_block - item * w.nb;
   const int take = w.nb - blk < end_block - at_block ? w.nb - blk : end_block - at_block;
+  const int last_block = at_block - blk + w.nb - 1;  // of the item
   at_block += take;
   const int h = item % a.Hk;
   const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
   const int64_t k0_ = (int64_t)(w.b0 + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
   const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
+  if (threadIdx.x == 0 && blk == 0 && take < w.nb) {
+    cut[0] = x.n0; cut[1] = x.row0; cut[2] = x.rows; cut[3] = h;
+    cut[4] = plan.share(last_block) - blockIdx.x + 1;
+  }
 
   // this lane's row and its queries, in the pieces the keys come in
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
@@ -1107,60 +1122,86 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins the partial results of one (token, query head) per workgroup. Every wave
-// forms the joint statistics (a lane per share) and takes every fourth share's
-// output with eight loads in flight; the four sums meet in LDS. The order is
-// fixed by the lengths alone. 4 to 7 us, of which finding the shares is most.
-template <typename E, int D>
-__device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t first, int64_t next, int64_t stride, int count) {
-  // partial index of share i: first for i = 0, next + (i - 1) stride from there on
-  constexpr int PER = D / 64, U = 8;
-  __shared__ float sum[4][D];
-  const int lane = lane_id(), wave = wave_id();
+// Joins the partial results of one (token, query head). Each of WAVES waves takes a
+// run of the shares, 64 at a time: a lane per share for the statistics, then the
+// shares' outputs weighted by them, 32 loads in flight. The runs' sums meet in LDS;
+// the sizes and lengths alone decide the order. Partial index of share i: first for
+// i = 0, next + (i - 1) stride from there on.
+template <typename E, int D, int WAVES>
+__device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int64_t first, int64_t next,
+                                            int64_t stride, int count) {
+  constexpr int PER = D / 64, U = 8, GROUPS = 4;
+  using V = __attribute__((ext_vector_type(PER))) float;
+  const int lane = lane_id(), wave = WAVES > 1 ? wave_id() : 0;
   auto slot = [&](int i) { return i == 0 ? first : next + (i - 1) * stride; };
   float M = kNoMax, L = 0.f;
-  for (int i = lane; i < count; i += 64) M = fmaxf(M, a.pml[slot(i) * 2]);
+  V o = 0.f;
+  const int run = (count + WAVES - 1) / WAVES, end = run * (wave + 1) < count ? run * (wave + 1) : count;
+  for (int c0 = run * wave; c0 < end; c0 += 64) {
+    const int left = end - c0 < 64 ? end - c0 : 64;
+    const int64_t own = slot(c0 + (lane < left ? lane : 0));
+    const float m = a.pml[own * 2], l = a.pml[own * 2 + 1];
+    V v[GROUPS * U];
+    auto load = [&](int i0) {
 #pragma unroll
-  for (int w = 1; w < 64; w <<= 1) M = fmaxf(M, __shfl_xor(M, w));
-  for (int i = lane; i < count; i += 64) L += a.pml[slot(i) * 2 + 1] * fast_exp2((a.pml[slot(i) * 2] - M) * a.c);
-  L = wave_sum(L);
-  float o[PER];
+      for (int q = 0; q < GROUPS; ++q)
+        if (q == 0 || i0 + q * U < left)
 #pragma unroll
-  for (int k = 0; k < PER; ++k) o[k] = 0.f;
-  for (int i0 = wave; i0 < count; i0 += 4 * U) {
-    float v[U][PER], f[U];
+          for (int u = 0; u < U; ++u) {
+            const int i = i0 + q * U + u;
+            v[q * U + u] = *reinterpret_cast<const V*>(a.po + slot(c0 + (i < left ? i : left - 1)) * D + lane * PER);
+          }
+    };
+    load(0);
+    float M1 = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t p = slot(i0 + 4 * u < count ? i0 + 4 * u : count - 1);
-      f[u] = a.pml[p * 2];
+    for (int w = 1; w < 64; w <<= 1) M1 = fmaxf(M1, __shfl_xor(M1, w));
+    M1 = fmaxf(M1, M);
+    const float f = fast_exp2((M - M1) * a.c), e = lane < left ? fast_exp2((m - M1) * a.c) : 0.f;
+    L = L * f + wave_sum(l * e);
+    M = M1;
+    o *= f;
+    for (int i0 = 0; i0 < left; i0 += GROUPS * U) {
+      if (i0) load(i0);
 #pragma unroll
-      for (int k = 0; k < PER; ++k) v[u][k] = a.po[p * D + lane * PER + k];
+      for (int q = 0; q < GROUPS; ++q)
+        if (q == 0 || i0 + q * U < left)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (i0 + q * U + u < left) o += v[q * U + u] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(e), i0 + q * U + u));
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + 4 * u < count) {
-        const float e = fast_exp2((f[u] - M) * a.c);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) o[k] += v[u][k] * e;
-      }
   }
+  if constexpr (WAVES > 1) {
+    __shared__ float ml[WAVES][2];
+    __shared__ V part[WAVES][64];
+    if (lane == 0) { ml[wave][0] = M; ml[wave][1] = L; }
+    part[wave][lane] = o;
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) sum[wave][lane * PER + k] = o[k];
-  __syncthreads();
-  const int64_t at = blockIdx.x;
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
-    const float t = (sum[0][d] + sum[1][d]) + (sum[2][d] + sum[3][d]);
-    E* out = static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D + d;
-    *out = from_f32<E>(L == 0.f ? 0.f : t / L);
+    for (int w = 1; w < WAVES; ++w) M = fmaxf(M, ml[w][0]);
+    L = 0.f;
+    o = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float f = fast_exp2((ml[w][0] - M) * a.c);
+      L += ml[w][1] * f;
+      o += part[w][lane] * f;
+    }
   }
-  if (threadIdx.x == 0 && a.lse)
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  E* out = static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D + lane * PER;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) out[k] = from_f32<E>(o[k] * inv);
+  if (lane == 0 && a.lse)
     a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
 }
 
 template <int BM, int BN, int LEAST, int D>
 __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
-  const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
+  if (at >= (int64_t)a.N * a.Hq) return;
+  const int n = (int)(at / a.Hq), hq = (int)(at % a.Hq);
   int s = n, i = 0, cnt = 1, n0 = n;
   if (a.cu) {
     s = find_sequence(a.cu, a.S, n);
@@ -1176,28 +1217,24 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
   const int count = share_of(x.lo, x.hi, BN, share_blocks(a, BM, BN, LEAST)).count;
   if (count <= 1) return;
   const int64_t stride = (int64_t)a.N * a.Hq;
-  join_shares<bf16, D>(a, blockIdx.x, blockIdx.x + stride, stride, count);
+  join_shares<bf16, D, 1>(a, at, at, at + stride, stride, count);
 }
 
-template <typename E, int D>
+// The rows of the item, if any, that starts in workgroup blockIdx.x's stretch of the
+// row kernel and goes on behind it: what that workgroup noted down. A wave per row
+// (d = 64, fp32, 768 workgroups: 5.2 us, 9.5 with WAVES = 4), or a workgroup per row
+// where few items leave many shares to each (d = 128, 128 shares: 6.1 us, 12 in a
+// wave).
+template <typename E, int D, int WAVES>
 __global__ __launch_bounds__(256) void paged_rows_combine_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
-  const int n = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-  const int s = a.cu ? find_sequence(a.cu, a.S, n) : n;
-  const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
-  if (s >= a.S) return;
-  const RowsWork w = plan.work(a, s, LY::BM, LY::BN);
-  const int i = n - w.n0;
-  if (i < 0 || i >= w.cnt) return;
-  const int run0 = s / plan.run;
-  int b = __builtin_amdgcn_readlane(plan.before, run0);     // the item's first block
-  for (int u = run0 * plan.run; u < s; ++u) b += rows_work(a, u, LY::BM, LY::BN).blocks();
-  const int row = i * a.G + hq % a.G;
-  b += (row / LY::BM * a.Hk + hq / a.G) * w.nb;
-  const int64_t w0 = plan.share(b), w1 = plan.share(b + w.nb - 1);
-  if (w0 == w1) return;
-  const int64_t r = row % LY::BM;
-  join_shares<E, D>(a, (2 * w0 + 1) * LY::BM + r, 2 * (w0 + 1) * LY::BM + r, 2 * LY::BM, (int)(w1 - w0) + 1);
+  const int64_t w = blockIdx.x;
+  const int* cut = a.cuts + w * kCutInts;
+  const int r = WAVES > 1 ? blockIdx.y : blockIdx.y * 4 + wave_id();
+  if (r >= cut[2]) return;
+  const int row = cut[1] + r;
+  const int64_t at = (int64_t)(cut[0] + row / a.G) * a.Hq + cut[3] * a.G + row % a.G;
+  join_shares<E, D, WAVES>(a, at, (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r, 2 * LY::BM, cut[4]);
 }
 
 }  // namespace carve

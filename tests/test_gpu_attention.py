@@ -438,7 +438,8 @@ def test_rows_behind_the_last_sequence_are_left(torch):
     ("bf16", 4, 2, 128, 16, 70, 20, False),
     ("bf16", 8, 1, 64, 32, 90, 0, False),
     ("f32", 2, 2, 64, 16, 129, 0, False),
-], ids=["step", "ragged", "tiles", "f32"])
+    ("bf16", 2, 2, 64, 16, 1500, 0, True),
+], ids=["step", "ragged", "tiles", "f32", "more"])
 def test_many_sequences(torch, case):
     from chunk_gated_delta_carve_amd import paged_append, paged_attention
     dtype, Hq, Hk, d, page, S, window, step = case
@@ -727,3 +728,8 @@ def test_another_stream(torch):
         s.synchronize()
         for g in (*got, out):
             assert torch.equal(g, want)
+    with torch.cuda.stream(s):                   # 0 is the default stream, whichever is current
+        got = paged_attention(*args, stream=0)
+        assert torch.cuda.current_stream() == s
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(got, want)
