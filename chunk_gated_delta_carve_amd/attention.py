@@ -245,6 +245,11 @@ def _sequences(block_table, kv_lens, cu_seqlens, N, dev):
             block_table.data_ptr())
 
 
+def _window(n):
+    """A window as the library takes it: beyond 32 bits it hides nothing that one of 32 bits shows."""
+    return max(-1, min(n, 2**31 - 1))
+
+
 def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None, q=None,
                  q_weight=None, k_weight=None, norm=False, eps=1e-6, interleaved=False, q_out=None, stream=None):
     """Stores new tokens in a paged cache, their keys (and q, where given) normed and rotated on the way as by
@@ -307,7 +312,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     lse = pl = None
     with _on(dev, stream):
         out = _dense(q) if out is None else out
-        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, 0, 0, window, _DTYPES[dt], step, 0.0,
+        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, 0, 0, _window(window), _DTYPES[dt], step, 0.0,
                                   d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0,
                                   _rows(out, "out", sq, dt, dev), table_row, *ks[:3], *vs[:3])
         if return_lse:
@@ -329,9 +334,12 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
 def paged_workspace_bytes(N, S, Hq, Hk, d, page_size, width, dtype=torch.bfloat16, window=0, step=False):
     """Bytes of workspace paged_attention needs for N new tokens of S sequences (step: one each) with a block table
     `width` pages wide."""
+    for name, n in (("N", N), ("S", S), ("Hq", Hq), ("Hk", Hk), ("d", d), ("page_size", page_size), ("width", width)):
+        if not 0 <= n < 2**31:
+            raise ValueError(f"{name}: expected a size of 32 bits, got {n}")
     c = _lib.CarvePagedConfig()
     c.N, c.S, c.Hq, c.Hk, c.d, c.page_size, c.pages, c.width = N, S, Hq, Hk, d, page_size, 1, width
-    c.window, c.dtype, c.scale = window, _DTYPES[dtype], 1.0
+    c.window, c.dtype, c.scale = _window(window), _DTYPES[dtype], 1.0
     c.flags = _lib.CARVE_PAGED_STEP if step else 0
     c.table_row = width
     c.kc_page = c.kc_tok = c.kc_head = c.vc_page = c.vc_tok = c.vc_head = d

@@ -1,5 +1,8 @@
 // Host side of the attention layer's entry points: validation, plan, dispatch.
 // Every check runs before the first HIP call.
+#include <algorithm>
+#include <cfloat>
+
 #include "host.h"
 #include "kernels/paged_attn.h"
 #include "kernels/rope.h"
@@ -9,6 +12,8 @@ namespace {
 using namespace carve_host;
 
 constexpr int64_t kMaxInt = 0x7fffffffLL;
+constexpr int64_t kMaxThreads = 0xffffffffLL;                // of a launch, in x
+constexpr int64_t kMaxTokens = kMaxThreads / 256 * 4;        // a wave each, in workgroups of 256
 
 bool off16(int64_t stride, int dtype) { return (stride * (int64_t)elem_bytes(dtype)) & 15; }
 
@@ -35,6 +40,9 @@ bool overlaps(const Rows& a, const Rows& b) {
   return d < la || d + lb > R;
 }
 
+// eps carries a row of zeros through the inverse root, which takes denormals as 0.
+bool bad_eps(float eps) { return !(eps >= FLT_MIN); }
+
 bool bad_rot(int rot, int d) { return rot < 0 || rot > d || rot % 16; }
 
 int check_rope(const carve_rope_config* c) {
@@ -42,11 +50,13 @@ int check_rope(const carve_rope_config* c) {
   if (c->N < 0 || c->Hq < 0 || c->Hk < 0 || c->rot < 0 || c->table_len < 0) return CARVE_EINVAL;
   if (c->dtype != CARVE_F32 && c->dtype != CARVE_BF16) return CARVE_EINVAL;
   if (c->flags & ~(CARVE_ROPE_INTERLEAVED | CARVE_ROPE_NORM)) return CARVE_EINVAL;
-  if ((c->flags & CARVE_ROPE_NORM) && !(c->eps > 0.f)) return CARVE_EINVAL;
+  if ((c->flags & CARVE_ROPE_NORM) && bad_eps(c->eps)) return CARVE_EINVAL;
   if ((c->d != 64 && c->d != 128) || bad_rot(c->rot, c->d)) return CARVE_EUNSUPPORTED;
   if (c->Hq > kMaxInt / c->d || c->Hk > kMaxInt / c->d) return CARVE_EUNSUPPORTED;
   const int64_t H = c->Hq > c->Hk ? c->Hq : c->Hk;
-  if (c->N > kMaxInt || c->N * H > kMaxInt) return CARVE_EUNSUPPORTED;   // rows are numbered in 32 bits
+  if (c->N > kMaxTokens || c->N * H > kMaxInt) return CARVE_EUNSUPPORTED;   // rows are numbered in 32 bits
+  for (int64_t r : {c->q_row, c->k_row, c->qo_row, c->ko_row, c->dq_row, c->dk_row})
+    if (r > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
 
@@ -144,6 +154,8 @@ int check_paged(const carve_paged_config* c) {
   if ((int64_t)c->width * c->page_size > (1 << 30)) return CARVE_EUNSUPPORTED;
   const int64_t heads = (int64_t)c->Hq + 2 * (int64_t)c->Hk;
   if (heads * c->d > kMaxInt || (int64_t)c->N * heads > kMaxInt) return CARVE_EUNSUPPORTED;
+  for (int64_t r : {c->q_row, c->k_row, c->v_row, c->o_row, c->table_row})
+    if (r > kMaxInt) return CARVE_EUNSUPPORTED;
   if (c->q_row < 0 || c->k_row < 0 || c->v_row < 0 || c->o_row < 0 || c->table_row < 0 ||
       (c->S > 1 && c->table_row < c->width))
     return CARVE_EINVAL;
@@ -166,6 +178,20 @@ int shift_of(int page_size) {
   int s = 0;
   while ((1 << s) < page_size) ++s;
   return s;
+}
+
+// Whether two entries of a cache may share channels: ordered by stride, every
+// dimension has to step past all that the ones before it reach.
+bool entries_overlap(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {
+  struct Dim { int64_t n, stride; } dims[3] = {{c->pages, page}, {c->page_size, tok}, {c->Hk, head}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t reach = c->d;
+  for (const Dim& x : dims) {
+    if (x.n < 2) continue;
+    if (x.stride < reach) return true;
+    reach += (x.n - 1) * x.stride;
+  }
+  return false;
 }
 
 size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {
@@ -396,7 +422,10 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   const carve_paged_config& c = *cfg;
   const bool step = (c.flags & CARVE_PAGED_STEP) != 0, norm = (c.flags & CARVE_ROPE_NORM) != 0;
   if (bad_rot(c.rot, c.d)) return CARVE_EUNSUPPORTED;
-  if (norm && !(c.eps > 0.f)) return CARVE_EINVAL;
+  if (norm && bad_eps(c.eps)) return CARVE_EINVAL;
+  if (c.N > kMaxTokens) return CARVE_EUNSUPPORTED;
+  if (entries_overlap(cfg, c.kc_page, c.kc_tok, c.kc_head) || entries_overlap(cfg, c.vc_page, c.vc_tok, c.vc_head))
+    return CARVE_EINVAL;
   if (!norm && (q_weight || k_weight)) return CARVE_EINVAL;
   const bool work = c.N > 0 && c.S > 0 && c.Hq + c.Hk > 0;
   if (work) {
@@ -464,7 +493,8 @@ int check_attention(const carve_paged_config* c) {
   if (!(c->scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c->Hq > 0 && (c->Hk == 0 || c->Hq % c->Hk)) return CARVE_EINVAL;
   const Plan p = plan_of(c);
-  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxInt) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
+  const int threads = 64 * (c->d == 64 ? kTileWaves<64> : kTileWaves<128>);
+  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / threads) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
 }  // namespace

@@ -25,7 +25,7 @@
 // would have put a NaN there.
 //
 // Long contexts are split over `splits` workgroups per tile, each leaving
-// (o, m, l) in fp32; paged_combine_kernel joins them in a fixed order. Every
+// (o, m, l) in fp32; a second kernel joins them in a fixed order. Every
 // tile works out from its own key range how many of them it needs, so no length
 // is read on the host and a captured graph follows the lengths on the device.
 #pragma once
@@ -67,8 +67,6 @@ struct AttnTile {
   int lo, hi;                                       // keys some row may see
 };
 
-// Tiles are numbered without knowing the lengths: sequence s starts at tile
-// floor(cu[s] G / BM) + s, which leaves room for its ceil(n G / BM) tiles.
 __device__ __forceinline__ int first_position(const PagedArgs& a, int s, int cnt) {
   const int kv = a.kv_lens[s];
   return (kv > 0 ? kv : 0) - cnt;
@@ -89,6 +87,8 @@ __device__ __forceinline__ AttnTile tile_of_rows(const PagedArgs& a, int s, int 
   return x;
 }
 
+// Tiles are numbered without knowing the lengths: sequence s starts at tile
+// floor(cu[s] G / BM) + s, which leaves room for its ceil(n G / BM) tiles.
 __device__ __forceinline__ AttnTile find_tile(const PagedArgs& a, int t, int BM) {
   AttnTile none;
   none.rows = 0;
@@ -283,7 +283,7 @@ struct RowsLayout {
   static constexpr int BM = 16, KT = 32, BN = 128;                               // BN: keys per round of four waves
   // Workgroups per CU that registers allow without spills in the loop; so many
   // are launched, one stretch of the work each.
-    static constexpr int PER_CU = D == 128 ? 2 : 3;
+  static constexpr int PER_CU = D == 128 ? 2 : 3;
   static constexpr int NP = D * (int)sizeof(E) / 64;                             // pieces per lane and key
   static constexpr int VLD = D * (int)sizeof(E) + (sizeof(E) == 2 ? 32 : 16);    // bytes per value row: spread banks
   static constexpr int OLD = D + 4;                                              // floats per row of a wave's result

@@ -260,7 +260,11 @@ int carve_recurrent_step(const carve_config* cfg, int32_t pos,
  * d channels of a head are contiguous, a token's heads follow each other, and
  * the `*_row` fields give the elements from one token to the next (so q and k
  * can be parts of one projection's output). Every stride is a multiple of 16
- * bytes. d is 64 or 128. */
+ * bytes and below 2^31 elements. d is 64 or 128.
+ * CARVE_EUNSUPPORTED also stands for calls larger than the launches take: more
+ * than 2^26 - 4 tokens to norm, rotate or append, 2^31 rows (tokens x heads), or,
+ * with few rows a sequence, 2^31 blocks of 128 keys over all heads and sequences
+ * at the longest lengths that the table and window allow. */
 
 /* Bits of carve_rope_config.flags and carve_paged_config.flags.
  *   CARVE_ROPE_INTERLEAVED  a rotated pair is channels (2i, 2i + 1); without it
@@ -281,7 +285,7 @@ typedef struct {
   int32_t rot;              /* rotated channels: a multiple of 16 up to d, 0 for none */
   int32_t table_len;        /* rows of cos and sin */
   int32_t dtype, flags;
-  float eps;                /* under the root, > 0 with CARVE_ROPE_NORM */
+  float eps;                /* under the root; with CARVE_ROPE_NORM a normal number > 0 */
 } carve_rope_config;
 
 /* Norm and rotation of queries and keys in one pass. For each head x of each
@@ -342,7 +346,7 @@ typedef struct {
  *   k, v [N,Hk,d], q [N,Hq,d] or NULL (Hq = 0); q_out may be q itself
  * A token whose position is negative or lies past the table, or whose page
  * number is outside [0, pages), is not stored. No page may be shared by two
- * sequences that store to it. */
+ * sequences that store to it, and no two entries of a cache may overlap. */
 int carve_paged_append(const carve_paged_config* cfg, const void* k, const void* v, const void* q,
                        const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                        const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* k_cache, void* v_cache,
@@ -354,7 +358,8 @@ int carve_paged_workspace(const carve_paged_config* cfg, int64_t* bytes);
 /* Attention of the new tokens over the cache (which holds them already): a token
  * at position p sees the keys j <= p with j > p - window.
  *   o = softmax(scale q k^T) v,   lse = log sum exp(scale q k^T)
- *   q [N,Hq,d], o [N,Hq,d] dtype (o overlaps no input); lse [N,Hq] fp32 or NULL
+ *   q [N,Hq,d], o [N,Hq,d] dtype (o overlaps no input); lse [N,Hq] fp32 or NULL;
+ *   the caches have at least one page
  * Softmax statistics and sums are fp32; in bf16 the weights are rounded to bf16
  * for the product with v. A token that sees no key (a negative position) has o = 0
  * and lse = -inf. Keys whose page number is outside [0, pages) or past the table

@@ -323,3 +323,60 @@ def test_paged_workspace_is_bounded(L):
     # more blocks of keys than 32 bits count
     c = paged_cfg(N=1 << 20, S=1 << 20, width=1 << 26, flags=_lib.CARVE_PAGED_STEP)
     assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_EUNSUPPORTED
+
+
+def test_sizes_past_the_launches_refused(L):
+    """A wave per token in workgroups of four: 2^26 tokens are 2^32 threads, one more than a launch counts. The tile
+    kernels' workgroups are counted the same way."""
+    most = (1 << 26) - 4
+    c = rope_cfg(N=most + 1, Hq=1, Hk=0)
+    assert fwd(L, c, k=None, k_out=None) == _lib.CARVE_EUNSUPPORTED
+    assert bwd(L, c, k=None, d_k_out=None, dk=None) == _lib.CARVE_EUNSUPPORTED
+    assert append(L, paged_cfg(N=most + 1, Hq=0, Hk=1, flags=0), q=None, q_out=None, q_weight=None,
+                  k_weight=None) == _lib.CARVE_EUNSUPPORTED
+    need = ctypes.c_int64()
+    for d, tiles in ((64, (1 << 24) - 1), (128, (1 << 23) - 1)):
+        rows = 33                                                    # per sequence: one tile and the numbering's slack
+        S = tiles * 128 * (d // 64) // (rows + 128 * (d // 64))
+        for more, code in ((0, _lib.CARVE_OK), (S // 50, _lib.CARVE_EUNSUPPORTED)):
+            c = paged_cfg(N=(S + more) * rows, S=S + more, Hq=1, Hk=1, d=d)
+            assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == code, (d, more)
+
+
+@pytest.mark.parametrize("name", ["q_row", "k_row", "qo_row", "ko_row", "dq_row", "dk_row"])
+def test_far_rope_strides_refused(L, name):
+    c = rope_cfg(**{name: 1 << 31})
+    assert fwd(L, c) == bwd(L, c) == _lib.CARVE_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["q_row", "k_row", "v_row", "o_row", "table_row", "kc_page", "vc_tok"])
+def test_far_paged_strides_refused(L, name):
+    c = paged_cfg(**{name: 1 << 31})
+    assert append(L, c) == attention(L, c) == _lib.CARVE_EUNSUPPORTED
+
+
+def test_denormal_eps_refused(L):
+    """The inverse root takes a denormal as 0, so a row of zeros would come out as NaN."""
+    assert fwd(L, rope_cfg(eps=1e-39)) == bwd(L, rope_cfg(eps=1e-39)) == _lib.CARVE_EINVAL
+    assert append(L, paged_cfg(eps=1e-39)) == _lib.CARVE_EINVAL
+    assert fwd(L, rope_cfg(eps=1.2e-38, N=0)) == _lib.CARVE_OK
+
+
+def test_append_refuses_caches_whose_entries_overlap(L):
+    for kw in (dict(kc_tok=128, kc_head=128), dict(vc_page=1024, vc_tok=128), dict(kc_page=64, kc_tok=768, kc_head=64),
+               dict(vc_head=1024)):
+        assert append(L, paged_cfg(**kw)) == _lib.CARVE_EINVAL, kw
+    # heads before tokens, tokens before pages, and gaps are fine (refused later, for the missing k)
+    for kw in (dict(kc_head=1024, kc_tok=64), dict(kc_page=128, kc_tok=12 * 128), dict(vc_page=4096, vc_tok=192)):
+        assert append(L, paged_cfg(N=0, **kw)) == _lib.CARVE_OK, kw
+
+
+def test_sizes_past_32_bits_in_python():
+    from chunk_gated_delta_carve_amd import paged_workspace_bytes
+    from chunk_gated_delta_carve_amd.attention import _window
+    assert [_window(n) for n in (-2**32, -1, 0, 7, 2**31, 2**32 + 5)] == [-1, -1, 0, 7, 2**31 - 1, 2**31 - 1]
+    ok = dict(N=64, S=64, Hq=8, Hk=2, d=64, page_size=16, width=256)
+    assert paged_workspace_bytes(**ok) > 0
+    for name in ok:
+        with pytest.raises(ValueError):
+            paged_workspace_bytes(**{**ok, name: 2**32 + ok[name]})
