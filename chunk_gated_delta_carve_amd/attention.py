@@ -60,10 +60,10 @@ def _rows(t, name, shape, dtype, device):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype or t.device != device:
         _like(t, name, dtype, device)
-    stride = t.stride()
     H, d = shape[-2], shape[-1]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return H * d
+    stride = t.stride()
     if stride[-1] != 1 or (H > 1 and stride[-2] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     row, size = H * d, 0                 # the token dimensions must step evenly
@@ -187,10 +187,12 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, cos=None, sin=None, positions=None,
         dq = _dense(q) if dq is None else dq
         dk = _dense(k) if dk is None else dk
         c.dq_row, c.dk_row = _rows(dq, "dq", sq, dt, dev), _rows(dk, "dk", sk, dt, dev)
-        dqw = torch.empty(sq[-1], dtype=torch.float32, device=dev) if q_weight is not None else None
-        dkw = torch.empty(sq[-1], dtype=torch.float32, device=dev) if k_weight is not None else None
+        dqw = None if q_weight is None else torch.empty_like(q_weight, dtype=torch.float32)
+        dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=torch.float32)
         need = ctypes.c_int64()
-        _lib.check(L.carve_qk_norm_rope_workspace(c, int(dqw is not None or dkw is not None), need))
+        code = L.carve_qk_norm_rope_workspace(c, dqw is not None or dkw is not None, need)
+        if code:
+            _lib.check(code)
         workspace, ws = _workspace(workspace, need.value, dev)
         code = L.carve_qk_norm_rope_bwd(
             c, *args, d_q_out.data_ptr(), d_k_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
