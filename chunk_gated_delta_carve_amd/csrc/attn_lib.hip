@@ -204,12 +204,19 @@ size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_
 // (tokens x grouped heads). Measured on 16 sequences of up to 4096 keys, row kernel
 // against tile kernel: 4 heads of 128, 32 rows 55 and 62 us, 48 rows 73 and 65 us;
 // 4 heads of 64, 24 rows 31 and 30 us, 36 rows 39 and 34 us.
+// Tiles have 128 rows (four waves) at d = 64. At d = 128 they have 256 (eight) where
+// those occupy more than half of the CUs, and 128 otherwise, two workgroups to a CU:
+// twice as many parts to spread, fewer rows wasted in a sequence's last tile, a
+// shorter start. With 256 and 128 rows, all launches, heads of 128: 64 tokens of 16 on
+// 2 heads over 4096 keys 27 and 23 us, 8 times 128 tokens of 16 on 4 over 4096 keys 93
+// and 85, 256 tokens over 32768 keys 123 and 118; 22 times 100 tokens of 16 on 2 over
+// 3600 keys, 180 tiles of 256 rows, 134 and 144.
 constexpr int kRowsPerSeq = 32;
 constexpr int kTileSplits = 128;
-template <int D> constexpr int kTileWaves = D == 64 ? 4 : 8;
 constexpr int kCUs = 256;
 struct Plan {
   bool tile;
+  int waves;                 // tile kernels: of a workgroup
   int64_t tiles, most;       // row kernel: blocks of keys at most, over all items
   int splits, shares;
   int64_t rows;              // partial results
@@ -222,9 +229,11 @@ Plan plan_of(const carve_paged_config* c) {
   const int64_t G = c->Hq / c->Hk;
   const bool step = (c->flags & CARVE_PAGED_STEP) != 0;
   p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)kRowsPerSeq * c->S;
-  const int waves = c->d == 64 ? kTileWaves<64> : kTileWaves<128>, per_cu = c->d == 64 ? 4 : 1;   // of the tile kernels
-  const int BM = p.tile ? 32 * waves : 16, BN = p.tile ? 64 : 128;
-  p.tiles = step ? c->S * up(G, BM) : (int64_t)c->N * G / BM + c->S;
+  auto tiles = [&](int BM) { return step ? c->S * up(G, BM) : up((int64_t)c->N * G, BM) + c->S - 1; };
+  p.waves = c->d == 128 && 2 * tiles(256) * c->Hk > kCUs ? 8 : 4;
+  const int per_cu = p.waves == 8 ? 1 : c->d == 64 ? 4 : 2;   // workgroups of the tile kernels
+  const int BM = p.tile ? 32 * p.waves : 16, BN = p.tile ? 64 : 128;
+  p.tiles = tiles(BM);
   int64_t keys = (int64_t)c->width * c->page_size;
   if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
   if (p.tile) {
@@ -248,16 +257,16 @@ Plan plan_of(const carve_paged_config* c) {
   return p;
 }
 
-template <int D, bool WIDE>
+template <int D, int WAVES, bool WIDE>
 constexpr auto tile_kernel() {
-  if constexpr (D == 64) return carve::paged_tile_kernel<D, WIDE>;
-  else return carve::paged_step_kernel<D, WIDE>;
+  if constexpr (WAVES == 8) return carve::paged_step_kernel<D, WIDE>;
+  else return carve::paged_tile_kernel<D, WIDE>;
 }
 
-template <int D, bool WIDE>
+template <int D, int WAVES, bool WIDE>
 hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
-  using LY = carve::TileLayout<D, kTileWaves<D>>;
-  constexpr auto kern = tile_kernel<D, WIDE>();
+  using LY = carve::TileLayout<D, WAVES>;
+  constexpr auto kern = tile_kernel<D, WAVES, WIDE>();
   hipError_t e = set_lds<kern>(LY::bytes);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(LY::NT), LY::bytes, s, a);
@@ -269,9 +278,12 @@ hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
 }
 
 template <typename E, int D>
-hipError_t dispatch_attention(const carve::PagedArgs& a, bool tile, hipStream_t s) {
+hipError_t dispatch_attention(const carve::PagedArgs& a, const Plan& plan, hipStream_t s) {
+  const bool wide = a.page_shift >= 3;
+  if constexpr (sizeof(E) == 2 && D == 128)
+    if (plan.tile && plan.waves == 8) return wide ? launch_tiles<D, 8, true>(a, s) : launch_tiles<D, 8, false>(a, s);
   if constexpr (sizeof(E) == 2)
-    if (tile) return a.page_shift >= 3 ? launch_tiles<D, true>(a, s) : launch_tiles<D, false>(a, s);
+    if (plan.tile) return wide ? launch_tiles<D, 4, true>(a, s) : launch_tiles<D, 4, false>(a, s);
   hipLaunchKernelGGL((carve::paged_rows_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.shares == 1) return e;
@@ -493,8 +505,7 @@ int check_attention(const carve_paged_config* c) {
   if (!(c->scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c->Hq > 0 && (c->Hk == 0 || c->Hq % c->Hk)) return CARVE_EINVAL;
   const Plan p = plan_of(c);
-  const int threads = 64 * (c->d == 64 ? kTileWaves<64> : kTileWaves<128>);
-  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / threads) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
+  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / (64 * p.waves)) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
 }  // namespace
@@ -561,7 +572,7 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
   a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
   a.scale = c.scale; a.c = c.scale * carve::kLog2e;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
-    return dispatch_attention<decltype(t), decltype(d)::value>(a, plan.tile, reinterpret_cast<hipStream_t>(stream));
+    return dispatch_attention<decltype(t), decltype(d)::value>(a, plan, reinterpret_cast<hipStream_t>(stream));
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);
 }

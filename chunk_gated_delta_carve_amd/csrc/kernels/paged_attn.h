@@ -819,9 +819,10 @@ struct TileWork {
 // windowed prompts (51 GFLOP) the kernel below took 133 us when this one, then
 // with three workgroups per CU, took 107 us; now about 98 us. In the loop the matrix
 // units are busy 57% of the time; a workgroup of 18 blocks spends an eighth of its
-// time on finding its tile and its first loads.
+// time on finding its tile and its first loads. d = 128: two workgroups per CU, for
+// calls of few tiles.
 template <int D, bool WIDE>
-__global__ __launch_bounds__(256, 4) void paged_tile_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedArgs a) {
   using W = TileWork<D, 4, WIDE>;
   using LY = typename W::LY;
   extern __shared__ __align__(16) char lds[];
@@ -922,7 +923,7 @@ __global__ __launch_bounds__(256, 4) void paged_tile_kernel(PagedArgs a) {
   w.finish(o, m, l);
 }
 
-// d = 128: eight waves, two blocks under way in each. A wave issues an
+// d = 128, many tiles: eight waves, two blocks under way in each. A wave issues an
 // instruction every five cycles or so and a 32x32x16 product occupies the matrix
 // unit for 32, so the vector work has to stand between the products of the same
 // wave: in step t the products X(t+1) are dealt among the exponentials of block t,

@@ -294,6 +294,11 @@ ATTENTION = [
     ("bf16", 3, 1, 64, 256, [150], [1500], 0, "plain", False),
     ("bf16", 2, 1, 128, 16, [129], [129], 1, "plain", False),
     ("bf16", 2, 2, 64, 32, [300, 40], [100, 40], 0, "plain", False),      # more new tokens than the length: empty rows
+    # more than 128 tiles of 256 rows at d = 128
+    ("bf16", 130, 130, 128, 16, [40], [40], 0, "plain", False),
+    ("bf16", 16, 16, 128, 1, [40, 9, 70, 0, 33, 64, 33, 41, 36, 39], [300, 9, 70, 5, 65, 200, 64, 500, 30, 39], 0, "joint", False),
+    ("bf16", 32, 16, 128, 64, [257, 129, 20, 1, 2, 50, 33, 64], [700, 129, 400, 90, 2, 64, 100, 333], 90, "heads", False),
+    ("bf16", 64, 32, 128, 8, [513], [600], 0, "plain", False),
     ("f32", 12, 4, 64, 16, [5, 1, 40], [5, 129, 140], 0, "plain", False),
     ("f32", 4, 2, 128, 32, [17, 3], [200, 3], 33, "heads", False),
     ("f32", 16, 2, 128, 16, [1, 1, 1], [1, 400, 65], 0, "joint", True),
@@ -394,16 +399,17 @@ def test_nothing_to_see(torch):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("dtype,n", [("bf16", 6), ("bf16", 150), ("f32", 6)])
-def test_a_bad_value_reaches_only_the_rows_that_see_it(torch, bad, dtype, n):
+@pytest.mark.parametrize("dtype,n,Hk,d", [("bf16", 6, 2, 64), ("bf16", 150, 2, 64), ("f32", 6, 2, 64),
+                                          ("bf16", 150, 2, 128), ("bf16", 150, 66, 128)])
+def test_a_bad_value_reaches_only_the_rows_that_see_it(torch, bad, dtype, n, Hk, d):
     """A token's infinite or NaN key or value, inside the blocks that other rows of the same tile share, leaves the
     rows before it (and, with a window, those past it) as they are."""
     from chunk_gated_delta_carve_amd import paged_attention
-    kv, window, d = n + 20, 10, 64
+    kv, window, Hq = n + 20, 10, 2 * Hk
     cu, lens, table, pages = ragged(torch, 11, 1, [n], [kv], 16)
     for which in (0, 1):
-        pair = cache(torch, "plain", pages, 16, 2, d, dtype, 100)
-        q = rand(torch, 102, (n, 4, d), dtype)
+        pair = cache(torch, "plain", pages, 16, Hk, d, dtype, 100)
+        q = rand(torch, 102, (n, Hq, d), dtype)
         args = (ints(torch, table), ints(torch, lens), ints(torch, cu))
         clean, clean_lse = paged_attention(q, *pair, *args, window=window, return_lse=True)
         j = kv - n // 2                          # that position's page entry
@@ -460,20 +466,21 @@ def test_many_sequences(torch, case):
     check_attention(torch, out, lse, q, kc, vc, table, lens, cu, d ** -0.5, window, dtype)
 
 
-@pytest.mark.parametrize("dtype,d,n,growth", [("bf16", 64, 1, 3.0), ("bf16", 128, 3, 12.0), ("f32", 64, 2, 3.0),
-                                              ("bf16", 64, 100, 3.0), ("bf16", 128, 100, 0.5), ("bf16", 128, 100, 12.0),
-                                              ("bf16", 64, 100, -3.0)])
-def test_scores_that_grow_along_the_context(torch, dtype, d, n, growth):
+@pytest.mark.parametrize("dtype,d,n,growth,Hk", [
+    ("bf16", 64, 1, 3.0, 1), ("bf16", 128, 3, 12.0, 1), ("f32", 64, 2, 3.0, 1), ("bf16", 64, 100, 3.0, 1),
+    ("bf16", 128, 100, 0.5, 1), ("bf16", 128, 100, 12.0, 1), ("bf16", 64, 100, -3.0, 1), ("bf16", 128, 100, 0.5, 66),
+    ("bf16", 128, 100, 12.0, 66), ("bf16", 128, 100, -3.0, 66)])
+def test_scores_that_grow_along_the_context(torch, dtype, d, n, growth, Hk):
     """Scores that rise (or fall) by `growth` every 64 keys: the reference of the running softmax follows in small
     steps, in large ones, or stays."""
     from chunk_gated_delta_carve_amd import paged_attention
     kv = 700
     cu, lens, table, pages = ragged(torch, 20, 1, [n], [kv], 16)
-    kc, vc = cache(torch, "plain", pages, 16, 1, d, dtype, 200)
-    q = rand(torch, 202, (n, 4, d), dtype, 0.3)
+    kc, vc = cache(torch, "plain", pages, 16, Hk, d, dtype, 200)
+    q = rand(torch, 202, (n, 4 * Hk, d), dtype, 0.3)
     q[..., 0] = 4.0
     j = torch.arange(len(table[0]) * 16, device="cuda").view(-1, 16)
-    kc[ints(torch, table[0]).long(), :, 0, 0] = (j * (growth / 64 / 4)).to(kc.dtype)
+    kc[ints(torch, table[0]).long(), :, :, 0] = (j * (growth / 64 / 4)).to(kc.dtype)[..., None]
     out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), scale=1.0,
                                return_lse=True)
     check_attention(torch, out, lse, q, kc, vc, table, lens, cu, 1.0, 0, dtype)
