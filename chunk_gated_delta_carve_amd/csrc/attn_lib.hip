@@ -200,10 +200,13 @@ size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_
 }
 
 // Kernel and split of an attention call, from sizes alone. The row kernel takes
-// fp32 and, in bf16, batches whose sequences average at most kRowsPerSeq rows
-// (tokens x grouped heads). Measured on 16 sequences of up to 4096 keys, row kernel
-// against tile kernel: 4 heads of 128, 32 rows 55 and 62 us, 48 rows 73 and 65 us;
-// 4 heads of 64, 24 rows 31 and 30 us, 36 rows 39 and 34 us.
+// fp32 and, in bf16, batches whose sequences average at most 16 rows (tokens x
+// grouped heads, one tile of it), or 32 where their tables or the window hold fewer
+// than kLongKeys keys, which is too short to pay for the tile kernels' start. Row and
+// tile kernel, all launches, 4 heads: of 128, 16 sequences of 4096 keys with 16 rows
+// 35 and 37 us, 24 rows 44 and 37, 32 rows 45 and 41; 64 of 2048 with 32 rows 93 and
+// 78; 4 of 1000 with 32 rows 14 and 18; of 64, 16 of 4096 with 32 rows 35 and 27, 4 of
+// 1000 with 32 rows 11 and 15.
 // Tiles have 128 rows (four waves) at d = 64. At d = 128 they have 256 (eight) where
 // those occupy more than half of the CUs, and 128 otherwise, two workgroups to a CU:
 // twice as many parts to spread, fewer rows wasted in a sequence's last tile, a
@@ -211,7 +214,7 @@ size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_
 // 2 heads over 4096 keys 27 and 23 us, 8 times 128 tokens of 16 on 4 over 4096 keys 93
 // and 85, 256 tokens over 32768 keys 123 and 118; 22 times 100 tokens of 16 on 2 over
 // 3600 keys, 180 tiles of 256 rows, 134 and 144.
-constexpr int kRowsPerSeq = 32;
+constexpr int kRowsShort = 32, kRowsLong = 16, kLongKeys = 2048;
 constexpr int kTileSplits = 128;
 constexpr int kCUs = 256;
 struct Plan {
@@ -228,13 +231,14 @@ Plan plan_of(const carve_paged_config* c) {
   if (c->N == 0 || c->S == 0 || c->Hk == 0 || c->Hq == 0) return p;
   const int64_t G = c->Hq / c->Hk;
   const bool step = (c->flags & CARVE_PAGED_STEP) != 0;
-  p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)kRowsPerSeq * c->S;
+  int64_t keys = (int64_t)c->width * c->page_size;
+  const int64_t seen = c->window > 0 && c->window < keys ? c->window : keys;
+  p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)(seen < kLongKeys ? kRowsShort : kRowsLong) * c->S;
   auto tiles = [&](int BM) { return step ? c->S * up(G, BM) : up((int64_t)c->N * G, BM) + c->S - 1; };
   p.waves = c->d == 128 && 2 * tiles(256) * c->Hk > kCUs ? 8 : 4;
   const int per_cu = p.waves == 8 ? 1 : c->d == 64 ? 4 : 2;   // workgroups of the tile kernels
   const int BM = p.tile ? 32 * p.waves : 16, BN = p.tile ? 64 : 128;
   p.tiles = tiles(BM);
-  int64_t keys = (int64_t)c->width * c->page_size;
   if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
   if (p.tile) {
     const int64_t most = up(keys, (int64_t)BN * 4);
