@@ -258,9 +258,9 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     qk_norm_rope_fwd, at their own positions. Shapes: k, v [N, Hk, d], packed sequence after sequence; caches
     [pages, page_size, Hk, d], page_size a power of two; block_table int32 [S, pages each]; kv_lens int32 [S], the
     lengths with the new tokens counted; cu_seqlens int32 [S + 1], where each sequence's new tokens start (None:
-    one each); q [N, Hq, d], q_out may be q itself. A token whose position is negative or past its table, or whose
-    page number is not in [0, pages), is not stored; tokens behind cu_seqlens[S] are left alone. Returns q_out
-    (None without q)."""
+    one each); q [N, Hq, d], q_out may be q itself. No two entries of a cache may overlap. A token whose position
+    is negative or past its table, or whose page number is not in [0, pages), is not stored; tokens behind
+    cu_seqlens[S] are left alone. Returns q_out (None without q)."""
     dt, dev = _first(k, "k", "paged_append")
     sk = k.shape
     if len(sk) != 3:
@@ -314,8 +314,8 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     lse = pl = None
     with _on(dev, stream):
         out = _dense(q) if out is None else out
-        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, 0, 0, _window(window), _DTYPES[dt], step, 0.0,
-                                  d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0,
+        c = _lib.CarvePagedConfig(N, S, Hq, Hk, d, cache[1], cache[0], width, 0, 0, _window(window), _DTYPES[dt],
+                                  step, 0.0, d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0,
                                   _rows(out, "out", sq, dt, dev), table_row, *ks[:3], *vs[:3])
         if return_lse:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)

@@ -251,8 +251,9 @@ Plan plan_of(const carve_paged_config* c) {
     // a workgroup per block of keys at most
     const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1);
     const bool f32 = c->dtype == CARVE_F32;
-    const int64_t want = kCUs * (c->d == 128 ? (f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU)
-                                             : (f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU));
+    const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;
+    const int slim = f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU;
+    const int64_t want = kCUs * (c->d == 128 ? wide : slim);
     p.most = blocks;
     p.shares = (int)(blocks < want ? blocks : want);
     p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
@@ -509,7 +510,8 @@ int check_attention(const carve_paged_config* c) {
   if (!(c->scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c->Hq > 0 && (c->Hk == 0 || c->Hq % c->Hk)) return CARVE_EINVAL;
   const Plan p = plan_of(c);
-  if ((p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / (64 * p.waves)) || p.most > kMaxInt) return CARVE_EUNSUPPORTED;
+  if (p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / (64 * p.waves)) return CARVE_EUNSUPPORTED;
+  if (p.most > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
 }  // namespace

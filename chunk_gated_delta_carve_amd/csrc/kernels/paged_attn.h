@@ -1169,7 +1169,8 @@ __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int6
         if (q == 0 || i0 + q * U < left)
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (i0 + q * U + u < left) o += v[q * U + u] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(e), i0 + q * U + u));
+            if (i0 + q * U + u < left)
+              o += v[q * U + u] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(e), i0 + q * U + u));
     }
   }
   if constexpr (WAVES > 1) {

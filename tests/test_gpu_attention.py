@@ -296,8 +296,10 @@ ATTENTION = [
     ("bf16", 2, 2, 64, 32, [300, 40], [100, 40], 0, "plain", False),      # more new tokens than the length: empty rows
     # more than 128 tiles of 256 rows at d = 128
     ("bf16", 130, 130, 128, 16, [40], [40], 0, "plain", False),
-    ("bf16", 16, 16, 128, 1, [40, 9, 70, 0, 33, 64, 33, 41, 36, 39], [300, 9, 70, 5, 65, 200, 64, 500, 30, 39], 0, "joint", False),
-    ("bf16", 32, 16, 128, 64, [257, 129, 20, 1, 2, 50, 33, 64], [700, 129, 400, 90, 2, 64, 100, 333], 90, "heads", False),
+    ("bf16", 16, 16, 128, 1, [40, 9, 70, 0, 33, 64, 33, 41, 36, 39], [300, 9, 70, 5, 65, 200, 64, 500, 30, 39], 0,
+     "joint", False),
+    ("bf16", 32, 16, 128, 64, [257, 129, 20, 1, 2, 50, 33, 64], [700, 129, 400, 90, 2, 64, 100, 333], 90, "heads",
+     False),
     ("bf16", 64, 32, 128, 8, [513], [600], 0, "plain", False),
     ("f32", 12, 4, 64, 16, [5, 1, 40], [5, 129, 140], 0, "plain", False),
     ("f32", 4, 2, 128, 32, [17, 3], [200, 3], 33, "heads", False),
