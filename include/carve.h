@@ -363,7 +363,8 @@ int carve_paged_workspace(const carve_paged_config* cfg, int64_t* bytes);
  * Softmax statistics and sums are fp32; in bf16 the weights are rounded to bf16
  * for the product with v. A token that sees no key (a negative position) has o = 0
  * and lse = -inf. Keys whose page number is outside [0, pages) or past the table
- * are not seen. What is not seen does not matter, infinities and NaN included.
+ * are not seen, and neither is a key whose score is -inf. What is not seen does not
+ * matter, infinities and NaN included.
  * The workspace may be shared by calls that do not overlap in time. Results are
  * deterministic (no atomics). */
 int carve_paged_attention(const carve_paged_config* cfg, const void* q, const void* k_cache, const void* v_cache,

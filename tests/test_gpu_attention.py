@@ -429,6 +429,71 @@ def test_a_bad_value_reaches_only_the_rows_that_see_it(torch, bad, dtype, n, Hk,
             assert not np.isfinite(seen[:, :, 3]).any() and np.isfinite(np.delete(seen, 3, 2)).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,n,d", [("bf16", 6, 64), ("bf16", 6, 128), ("bf16", 100, 64), ("bf16", 100, 128),
+                                       ("f32", 6, 64), ("f32", 6, 128)])
+def test_a_bad_value_in_a_context_that_is_split(torch, bad, dtype, n, d):
+    """As above, with the context dealt to many workgroups: the part that holds the bad value is computed again by the
+    row, the others join it."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    kv, window = 4000, 2000
+    cu, lens, table, pages = ragged(torch, 13, 1, [n], [kv], 16)
+    pair = cache(torch, "plain", pages, 16, 1, d, dtype, 114)
+    q = rand(torch, 116, (n, 2, d), dtype)
+    args = (ints(torch, table), ints(torch, lens), ints(torch, cu))
+    p = np.arange(kv - n, kv)
+    first = p - window + 1
+    edge = kv - n // 2 - window                  # falls out of the window half-way through the new tokens
+    for j in (edge, 3000):
+        _, vc = (x.clone() for x in pair)
+        vc[table[0, j // 16], j % 16, :, 3] = bad
+        out, lse = paged_attention(q, pair[0], vc, *args, window=window, return_lse=True)
+        sees = j >= first
+        ref = orc.paged_attention(f64(q), f64(pair[0]), f64(pair[1]), table, lens, cu, d ** -0.5, window)
+        bo, bl = attention_bounds(dtype, d, d ** -0.5, *ref)
+        close("lse", lse, ref[1], bl)
+        got = f64(out)
+        assert not np.isfinite(got[sees][:, :, 3]).any() and (j != edge or 0 < sees.sum() < n)
+        for rows, chans in ((~sees, slice(None)), (sees, np.arange(d) != 3)):
+            assert np.all(np.abs(got[rows][..., chans] - ref[0][rows][..., chans]) <= bo[rows][..., chans])
+
+
+@pytest.mark.parametrize("dtype,n,Hk,d", [("bf16", 4, 1, 64), ("bf16", 4, 2, 128), ("bf16", 90, 1, 64),
+                                          ("bf16", 90, 2, 128), ("bf16", 90, 130, 128), ("f32", 4, 1, 64)])
+def test_infinite_scores(torch, dtype, n, Hk, d):
+    """A key whose score is -inf counts for nothing, as one that does not exist (the same bits); a row whose keys all
+    are such sees nothing; a score of +inf makes the rows that see it NaN."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    kv, page = 300, 4
+    cu, lens, table, pages = ragged(torch, 14, 1, [n], [kv], page)
+    kc, vc = cache(torch, "plain", pages, page, Hk, d, dtype, 118)
+    q = rand(torch, 120, (n, Hk, d), dtype)
+    q[..., 5] = 1.0
+    args = (ints(torch, lens), ints(torch, cu))
+    j = kv - n // 2 - 1                          # the first row does not see this key's page
+    holes = table.copy()
+    holes[0, [2, j // page]] = -1
+    want = paged_attention(q, kc, vc, ints(torch, holes), *args, return_lse=True)
+    low = kc.clone()
+    low[table[0, [2, j // page]], ..., 5] = float("-inf")
+    got = paged_attention(q, low, vc, ints(torch, table), *args, return_lse=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.isfinite(got[0]).all()
+    low[..., 5] = float("-inf")
+    out, lse = paged_attention(q, low, vc, ints(torch, table), *args, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    high = kc.clone()
+    high[table[0, j // page], j % page, :, 5] = float("inf")
+    out, lse = paged_attention(q, high, vc, ints(torch, table), *args, return_lse=True)
+    sees = torch.arange(kv - n, kv, device="cuda") >= j
+    assert out[sees].isnan().all() and lse[sees].isnan().all()
+    plain = paged_attention(q, kc, vc, ints(torch, table), *args)
+    ref = orc.paged_attention(f64(q), f64(kc), f64(vc), table, lens, cu, d ** -0.5, 0)
+    bo, _ = attention_bounds(dtype, d, d ** -0.5, *ref)
+    rows = ~sees.cpu().numpy()
+    close("rows before it", out[~sees], ref[0][rows], bo[rows])
+    close("without it", plain, ref[0], bo)
+
+
 def test_rows_behind_the_last_sequence_are_left(torch):
     from chunk_gated_delta_carve_amd import paged_attention
     for n, extra in ((3, 5), (140, 9)):
