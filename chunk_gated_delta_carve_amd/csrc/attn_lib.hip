@@ -67,6 +67,7 @@ bool bad_rows(int64_t n, int64_t row, int64_t len, int dtype, bool written) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kFewWaves = 4096;   // four waves per SIMD
+constexpr int64_t kManyRows = 16384;   // rows to join: eight to a wave are two waves per SIMD
 constexpr int kWideJoin = 32;          // shares per item from which a workgroup joins a row, not a wave
 
 // Blocks of the gradient: four per CU share the rows of q and k in proportion,
@@ -258,7 +259,8 @@ Plan plan_of(const carve_paged_config* c) {
     p.shares = (int)(blocks < want ? blocks : want);
     p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
   }
-  p.bytes = (p.rows * (c->d + 2) + (p.tile || p.shares < 2 ? 0 : (int64_t)p.shares * carve::kCutInts)) * 4;
+  const int64_t cuts = p.rows == 0 ? 0 : p.tile ? p.tiles * c->Hk : p.shares;
+  p.bytes = (p.rows * (c->d + 2) + cuts * carve::kCutInts) * 4;
   return p;
 }
 
@@ -277,8 +279,11 @@ hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(LY::NT), LY::bytes, s, a);
   e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((carve::paged_tile_combine_kernel<LY::BM, LY::BN, LY::LEAST, D>),
-                     dim3((unsigned)up((int64_t)a.N * a.Hq, 4)), dim3(256), 0, s, a);
+  const unsigned tiles = a.tiles * a.Hk;
+  if (a.splits > carve::kFewShares || (int64_t)a.N * a.Hq < kManyRows)
+    hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 1>), dim3(tiles, LY::BM / 4), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 8>), dim3(tiles, LY::BM / 32), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -43,7 +43,7 @@ struct PagedArgs {
   void* o;
   float* lse;                                       // [N][Hq] or NULL
   float *po, *pml;                                  // partial results (o, and m with l)
-  int* cuts;                                        // row kernel: kCutInts per workgroup
+  int* cuts;                                        // notes on items with partial results
   int64_t q_row, o_row, table_row;
   int64_t kc_page, kc_tok, kc_head, vc_page, vc_tok, vc_head;
   int N, S, Hq, Hk, G, width, pages, page_shift, window;
@@ -165,6 +165,16 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int s, int j) {   // 
   if (j < 0 || slot >= a.width) return -1;
   const int id = a.table[s * a.table_row + slot];
   return id >= 0 && id < a.pages ? id : -1;
+}
+
+// What is noted down about an item (rows of one key/value head) whose keys several
+// workgroups share: first token of the sequence, first row, rows (0: no such item),
+// head, and the number of workgroups that hold parts of it. The row kernel's
+// workgroups note the item that starts in their stretch and goes on behind it, the
+// tile kernels' first share of every tile notes that.
+constexpr int kCutInts = 8;                         // of workspace
+__device__ __forceinline__ void note_cut(int* cut, const AttnTile& x, int h, int count) {
+  cut[0] = x.n0; cut[1] = x.row0; cut[2] = x.rows; cut[3] = h; cut[4] = count;
 }
 
 // Where a row's results go: the output itself when one workgroup sees all of
@@ -375,11 +385,6 @@ __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN
   return p;
 }
 
-// What a workgroup notes down about the item that starts in its stretch and goes on
-// behind it: first token of the sequence, first row, rows (0: there is none), head,
-// and the number of workgroups that hold parts of it.
-constexpr int kCutInts = 8;                         // of workspace per workgroup
-
 template <typename E, int D>
 __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
@@ -413,10 +418,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   const int64_t k0_ = (int64_t)(w.b0 + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
   const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
-  if (threadIdx.x == 0 && blk == 0 && take < w.nb) {
-    cut[0] = x.n0; cut[1] = x.row0; cut[2] = x.rows; cut[3] = h;
-    cut[4] = plan.share(last_block) - blockIdx.x + 1;
-  }
+  if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
 
   // this lane's row and its queries, in the pieces the keys come in
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
@@ -654,8 +656,11 @@ struct TileWork {
     // the last tiles of a sequence see the most keys: start with them
     x = find_tile(a, a.tiles - 1 - rest % a.tiles, LY::BM);
     T = 0;
+    int* cut = a.splits > 1 && sp == 0 && threadIdx.x == 0 ? a.cuts + (int64_t)blockIdx.x * kCutInts : nullptr;
+    if (cut) cut[2] = 0;
     if (x.rows <= 0) return;
     const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
+    if (cut && sh.count > 1) note_cut(cut, x, h, sh.count);
     if (sp > 0 && sp >= sh.count) { x.rows = 0; return; }
     whole = sh.count <= 1;
     first_b = sh.b0 + sp * sh.per;
@@ -1199,27 +1204,72 @@ __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int6
     a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
 }
 
-template <int BM, int BN, int LEAST, int D>
+// The rows of a tile whose keys were shared, as its first share noted it down: one
+// to a wave, or, where there are many rows and at most kFewShares shares, eight, four
+// at a time with a lane per row and share for the statistics. 4000 tokens over
+// themselves, 12 heads of 64 in two shares: 9.6 us, a row to a wave 30; 256 tokens of
+// 16 heads of 128 in 16 shares 16 and 9.
+constexpr int kFewShares = 16;
+template <int D, int ROWS>
 __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
-  if (at >= (int64_t)a.N * a.Hq) return;
-  const int n = (int)(at / a.Hq), hq = (int)(at % a.Hq);
-  int s = n, i = 0, cnt = 1, n0 = n;
-  if (a.cu) {
-    s = find_sequence(a.cu, a.S, n);
-    if (s >= a.S) return;
-    n0 = a.cu[s];
-    int n1 = a.cu[s + 1];
-    n1 = n1 < a.N ? n1 : a.N;
-    i = n - n0; cnt = n1 - n0;
-    if (n0 < 0 || i < 0 || i >= cnt) return;
-  } else if (s >= a.S) return;
-  const int row = i * a.G + hq % a.G;
-  const AttnTile x = tile_of_rows(a, s, n0, cnt, first_position(a, s, cnt), row / BM * BM, BM);
-  const int count = share_of(x.lo, x.hi, BN, share_blocks(a, BM, BN, LEAST)).count;
-  if (count <= 1) return;
+  const int* cut = a.cuts + (int64_t)blockIdx.x * kCutInts;
+  const int n0 = cut[0], row0 = cut[1], rows = cut[2], h = cut[3], count = cut[4];
   const int64_t stride = (int64_t)a.N * a.Hq;
-  join_shares<bf16, D, 1>(a, at, at, at + stride, stride, count);
+  auto index = [&](int r) {
+    const int row = row0 + r;
+    return (int64_t)(n0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+  };
+  const int first = (blockIdx.y * 4 + wave_id()) * ROWS;
+  if (first >= rows) return;
+  if constexpr (ROWS == 1) {
+    const int64_t at = index(first);
+    join_shares<bf16, D, 1>(a, at, at, at + stride, stride, count);
+  } else {
+    constexpr int PER = D / 64, R = 4, U = 4;       // rows and shares of a round of loads
+    using V = __attribute__((ext_vector_type(PER))) float;
+    const int lane = lane_id(), own = lane & (kFewShares - 1);
+    for (int r0 = first; r0 < first + ROWS && r0 < rows; r0 += R) {
+      int64_t at[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) at[r] = index(r0 + r < rows ? r0 + r : rows - 1);
+      const int mine = r0 + lane / kFewShares;
+      const int64_t my = index(mine < rows ? mine : rows - 1);
+      const int64_t p = my + (own < count ? own : 0) * stride;
+      const float m = a.pml[p * 2], l = a.pml[p * 2 + 1];
+      V o[R] = {};
+      float M = m;
+#pragma unroll
+      for (int w = 1; w < kFewShares; w <<= 1) M = fmaxf(M, __shfl_xor(M, w));
+      float f = own < count ? fast_exp2((m - M) * a.c) : 0.f, L = l * f;
+#pragma unroll
+      for (int w = 1; w < kFewShares; w <<= 1) L += __shfl_xor(L, w);
+      f *= L == 0.f ? 0.f : 1.f / L;
+      for (int i0 = 0; i0 < count; i0 += U) {
+        V v[U][R];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            v[u][r] = *reinterpret_cast<const V*>(
+                a.po + (at[r] + (i0 + u < count ? i0 + u : count - 1) * stride) * D + lane * PER);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u < count)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              o[r] += v[u][r] * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), r * kFewShares + i0 + u));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r0 + r < rows) {
+          bf16* out = static_cast<bf16*>(a.o) + at[r] / a.Hq * a.o_row + at[r] % a.Hq * D + lane * PER;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) out[k] = (bf16)o[r][k];
+        }
+      if (a.lse && own == 0 && mine < rows)
+        a.lse[my] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+    }
+  }
 }
 
 // The rows of the item, if any, that starts in workgroup blockIdx.x's stretch of the

@@ -356,7 +356,8 @@ def test_attention(torch, case):
 
 
 @pytest.mark.parametrize("dtype,d,kv,n,Hq,Hk", [("bf16", 64, 9000, 1, 12, 12), ("bf16", 128, 20011, 1, 16, 2),
-                                                ("bf16", 128, 5001, 300, 4, 1), ("f32", 64, 3001, 2, 4, 2)])
+                                                ("bf16", 128, 5001, 300, 4, 1), ("f32", 64, 3001, 2, 4, 2),
+                                                ("bf16", 64, 2000, 1999, 12, 4), ("bf16", 128, 2300, 1030, 16, 8)])
 def test_attention_split_over_a_long_context(torch, dtype, d, kv, n, Hq, Hk):
     """Few rows over many keys are split over workgroups and joined; the same bits every time."""
     from chunk_gated_delta_carve_amd import paged_attention
