@@ -249,7 +249,7 @@ Plan plan_of(const carve_paged_config* c) {
     p.splits = s < 1 ? 1 : (int)s;
     p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
   } else {
-    // a workgroup per block of keys at most
+    // a workgroup per block of keys at most; no item has more blocks than this counts
     const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1);
     const bool f32 = c->dtype == CARVE_F32;
     const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;

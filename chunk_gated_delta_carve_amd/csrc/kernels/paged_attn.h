@@ -283,7 +283,8 @@ __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x)
 //
 // Lengths differ, so the work is dealt evenly: the items (sequence, tile of 16
 // rows, key/value head), each as many blocks of BN keys as its sequence's rows
-// see, are laid end to end, and every workgroup takes an equal stretch of blocks.
+// see (with a window, as 16 rows can see at most, from the item's own first key),
+// are laid end to end, and every workgroup takes an equal stretch of blocks.
 // An item that ends up in several workgroups leaves partial results: a workgroup
 // has at most two, the item its stretch starts inside of and the one it ends in.
 // 64 sequences of 200 to 8192 keys, 4 heads of 128 (551 MB): 110 us, 5.0 TB/s, the
@@ -319,9 +320,10 @@ __device__ __forceinline__ s16x4 read_tr(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
 }
 
-// A sequence's part of the work: `items` times `nb` blocks, from key block b0.
+// A sequence's part of the work: `items` times `nb` blocks, each item's from the
+// block of its first key on.
 struct RowsWork {
-  int n0, cnt, pos0, items, b0, nb;
+  int n0, cnt, pos0, items, nb;
   __device__ __forceinline__ int blocks() const { return items * nb; }
 };
 __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM, int BN) {
@@ -332,18 +334,21 @@ __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM,
     const int n1 = a.cu[s + 1];
     w.cnt = w.n0 < 0 ? 0 : (n1 < a.N ? n1 : a.N) - w.n0;
   }
-  if (w.cnt <= 0) { w.pos0 = w.items = w.nb = w.b0 = w.cnt = 0; return w; }
+  if (w.cnt <= 0) { w.pos0 = w.items = w.nb = w.cnt = 0; return w; }
   w.pos0 = first_position(a, s, w.cnt);
   const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, 0, 0x7fffffff);
   w.items = (w.cnt * a.G + BM - 1) / BM * a.Hk;
-  w.b0 = x.lo / BN;
-  w.nb = x.hi > x.lo ? (x.hi + BN - 1) / BN - w.b0 : 1;    // rows without keys are an item too
+  w.nb = x.hi > x.lo ? (x.hi + BN - 1) / BN - x.lo / BN : 1;    // rows without keys are an item too
+  if (a.window > 0) {                               // BM rows see window + BM - 1 keys at most, starting inside a block
+    const int most = (int)(((unsigned)a.window + BM + BN - 3) / BN) + 1;
+    w.nb = w.nb < most ? w.nb : most;
+  }
   return w;
 }
 
 // Prefix sums of the sequences' blocks, a lane per run of sequences; with one
 // sequence a lane, `own` keeps what the lane worked out. Counts stay below 2^31
-// (checked on the host for the longest lengths that fit the table).
+// (checked on the host for the most keys that the table and the window let an item see).
 struct RowsPlan {
   int run, before;                                  // sequences per lane, blocks before this lane's run
   RowsWork own;
@@ -357,7 +362,7 @@ struct RowsPlan {
   __device__ __forceinline__ RowsWork work(const PagedArgs& a, int s, int BM, int BN) const {
     if (run > 1) return rows_work(a, s, BM, BN);
     auto at = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
-    return RowsWork{at(own.n0), at(own.cnt), at(own.pos0), at(own.items), at(own.b0), at(own.nb)};
+    return RowsWork{at(own.n0), at(own.cnt), at(own.pos0), at(own.items), at(own.nb)};
   }
 };
 __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN) {
@@ -415,7 +420,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   at_block += take;
   const int h = item % a.Hk;
   const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
-  const int64_t k0_ = (int64_t)(w.b0 + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
+  const int64_t k0_ = (int64_t)(x.lo / LY::BN + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
   const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
   if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);

@@ -380,3 +380,26 @@ def test_sizes_past_32_bits_in_python():
     for name in ok:
         with pytest.raises(ValueError):
             paged_workspace_bytes(**{**ok, name: 2**32 + ok[name]})
+
+
+def test_the_row_kernels_blocks_fit_32_bits(L):
+    """What the host accepts the row kernel counts in 32 bits: an item (16 rows of a key/value head) has the blocks of
+    128 keys that its sequence's rows see, and with a window no more than 16 rows can."""
+    need = ctypes.c_int64()
+    rng = np.random.default_rng(31)
+    codes = set()
+    cases = [(524288, w, 64) for w in (0, 256, 1024)] + [(1 << 20, 1024, 64), (700000, 1024, 128)]
+    cases += [(int(2.0 ** rng.uniform(10, 22)), int(rng.choice([0, 2.0 ** rng.uniform(0, 22)])), 64) for _ in range(200)]
+    for N, window, page in cases:
+        c = paged_cfg(N=N, S=1, Hq=16, Hk=4, page_size=page, pages=N // page + 1, width=N // page + 1, window=window,
+                      dtype=_lib.CARVE_F32)
+        code = L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need))
+        codes.add(code)
+        items, blocks = -(-N * 4 // 16) * 4, -(-N // 128)
+        if window:
+            blocks = min(blocks, (window + 16 + 128 - 3) // 128 + 1)
+        if code == _lib.CARVE_OK:
+            assert items * blocks < 2 ** 31, (N, window)
+        else:
+            assert code == _lib.CARVE_EUNSUPPORTED and items * (blocks + 3) >= 2 ** 31, (N, window)
+    assert codes == {_lib.CARVE_OK, _lib.CARVE_EUNSUPPORTED}

@@ -808,3 +808,41 @@ def test_another_stream(torch):
         assert torch.cuda.current_stream() == s
     torch.cuda.default_stream().synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("dtype,n,kv,Hq,Hk,d", [("f32", [700, 3, 150], [700, 900, 400], 4, 2, 64),
+                                                ("f32", [333], [333], 4, 1, 128),
+                                                ("bf16", [150] + [1] * 30, [400] + [90] * 30, 2, 2, 64)])
+def test_prompts_of_the_row_kernel(torch, dtype, n, kv, Hq, Hk, d, window):
+    """Many items to a sequence, whose rows see very different parts of it."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    cu, lens, table, pages = ragged(torch, 30, len(n), n, kv, 16)
+    kc, vc = cache(torch, "plain", pages, 16, Hk, d, dtype, 290)
+    q = rand(torch, 292, (sum(n), Hq, d), dtype)
+    out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), window=window,
+                               return_lse=True)
+    check_attention(torch, out, lse, q, kc, vc, table, lens, cu, d ** -0.5, window, dtype)
+
+
+def test_a_windowed_prompt_of_half_a_million_tokens(torch):
+    """2^31 blocks of 128 keys if every 16 rows had their sequence's; with the window they have four each."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    N, Hq, Hk, d, page, window = 524288, 16, 4, 64, 64, 256
+    g = torch.Generator(device="cuda").manual_seed(300)
+    q = torch.randn(N, Hq, d, generator=g, device="cuda")
+    kc, vc = (torch.randn(N // page, page, Hk, d, generator=g, device="cuda") for _ in range(2))
+    table = torch.randperm(N // page, generator=g, device="cuda").to(torch.int32)[None]
+    out = torch.full_like(q, float("nan"))
+    _, lse = paged_attention(q, kc, vc, table, ints(torch, [N]), ints(torch, [0, N]), window=window, out=out,
+                             return_lse=True)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for r in (0, 200, 255, 256, 70001, N // 2, N - 1):
+        t0 = max(0, r - window + 1) // page
+        part = table[0, t0:r // page + 1].long()
+        o, l, A, reach, keys = orc.paged_attention(f64(q[r:r + 1]), f64(kc[part]), f64(vc[part]),
+                                                   np.arange(len(part))[None], [r - t0 * page + 1], [0, 1], d ** -0.5,
+                                                   window)
+        bo, bl = attention_bounds("f32", d, d ** -0.5, o, l, A, reach, keys)
+        close(f"row {r}", out[r:r + 1], o, bo)
+        assert np.all(np.abs(f64(lse[r:r + 1]) - l) <= bl)
