@@ -289,7 +289,10 @@ hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
 
 template <typename E, int D>
 hipError_t dispatch_attention(const carve::PagedArgs& a, const Plan& plan, hipStream_t s) {
-  const bool wide = a.page_shift >= 3;
+  // rows of one load of a wave in one page, their offsets from its first within 32 bits
+  using LY = carve::TileLayout<D, 4>;
+  const int64_t reach = (LY::WR - 1) * 2 * std::max(a.kc_tok, a.vc_tok) + LY::CPR * 16;
+  const bool wide = a.page_shift >= 3 && reach <= 0xffffffffLL;
   if constexpr (sizeof(E) == 2 && D == 128)
     if (plan.tile && plan.waves == 8) return wide ? launch_tiles<D, 8, true>(a, s) : launch_tiles<D, 8, false>(a, s);
   if constexpr (sizeof(E) == 2)

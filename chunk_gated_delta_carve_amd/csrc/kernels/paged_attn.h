@@ -719,7 +719,8 @@ struct TileWork {
   }
   // The thread's chunk i of a block. The rows that one load of a wave covers (4, or
   // 8 at d = 64) lie in one page of at least 8 tokens (WIDE): their first row's
-  // address is a scalar then, and a lane adds a constant.
+  // address is a scalar then, and a lane adds a constant of 32 bits. Token strides
+  // that would pass those take the other form.
   __device__ __forceinline__ u32x4 load(const char* base, uint64_t at, unsigned lane_off, int i) const {
     if constexpr (WIDE) {
       const int r0 = wave * LY::WR + LY::RS * i;

@@ -846,3 +846,28 @@ def test_a_windowed_prompt_of_half_a_million_tokens(torch):
         bo, bl = attention_bounds("f32", d, d ** -0.5, o, l, A, reach, keys)
         close(f"row {r}", out[r:r + 1], o, bo)
         assert np.all(np.abs(f64(lse[r:r + 1]) - l) <= bl)
+
+
+@pytest.mark.parametrize("n,Hq,Hk,d,stride", [(1, 4, 2, 64, 310_000_000), (100, 4, 2, 64, 310_000_000),
+                                              (100, 4, 2, 128, 720_000_000), (40, 130, 130, 128, 720_000_000)])
+def test_tokens_far_apart(torch, n, Hq, Hk, d, stride):
+    """A token-major pool [page_size, pages, Hk, d] whose token stride is so wide that the eight tokens of a page span
+    more than 2^32 bytes: the bits of the same call on a cache of its own."""
+    from chunk_gated_delta_carve_amd import paged_append, paged_attention
+    kv, page = 120, 8
+    cu, lens, table, pages = ragged(torch, 24, 1, [n], [kv], page)
+    entry = pages * Hk * d
+    pool = torch.empty((page - 1) * stride + 2 * entry, dtype=torch.bfloat16, device="cuda")
+    far = [pool.as_strided((pages, page, Hk, d), (Hk * d, stride, d, 1), i * entry) for i in range(2)]
+    near = cache(torch, "plain", pages, page, Hk, d, "bf16", 240)
+    for a, b in zip(far, near):
+        a.copy_(b)
+    q, k, v = (rand(torch, 242 + i, (n, h, d), "bf16") for i, h in enumerate((Hq, Hk, Hk)))
+    args = (ints(torch, table), ints(torch, lens), ints(torch, cu))
+    for c in (far, near):
+        paged_append(k, v, *c, *args)
+    assert all(torch.equal(a, b) for a, b in zip(far, near))
+    got = paged_attention(q, *far, *args, return_lse=True)
+    want = paged_attention(q, *near, *args, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_attention(torch, *got, q, *near, table, lens, cu, d ** -0.5, 0, "bf16")
