@@ -221,7 +221,8 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   for (int j0 = first; j0 < end; j0 += 64) {
-    const int j = j0 + lane, id = j < end ? page_of(a, x.s, j) : -1;
+    const int j = j0 + lane;
+    int id = j < end ? page_of(a, x.s, j) : -1;
     const int64_t off = j & ((1 << a.page_shift) - 1);
     float s = -__builtin_inff();
     if (id >= 0) {
@@ -241,6 +242,7 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
       for (int i = 0; i < PER; ++i) o[i] = l;
       break;
     }
+    if (s == -__builtin_inff()) id = -1;            // not seen: its value stays out
     float top = s;
 #pragma unroll
     for (int w = 1; w < 64; w <<= 1) top = fmaxf(top, __shfl_xor(top, w));

@@ -871,3 +871,27 @@ def test_tokens_far_apart(torch, n, Hq, Hk, d, stride):
     want = paged_attention(q, *near, *args, return_lse=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check_attention(torch, *got, q, *near, table, lens, cu, d ** -0.5, 0, "bf16")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,n,kv,Hk,d", [
+    ("bf16", 4, 300, 1, 64), ("bf16", 4, 300, 2, 128), ("bf16", 90, 300, 1, 64), ("bf16", 90, 300, 2, 128),
+    ("bf16", 90, 300, 130, 128), ("f32", 4, 300, 1, 64), ("f32", 40, 300, 1, 128),
+    ("bf16", 4, 4000, 1, 128), ("bf16", 100, 4000, 1, 64), ("f32", 4, 4000, 1, 64)])
+def test_values_of_keys_that_count_for_nothing(torch, bad, dtype, n, kv, Hk, d):
+    """A key whose score is -inf is not seen, so its value does not matter, infinities and NaN included; contexts in
+    one piece and split ones."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    page = 4
+    cu, lens, table, pages = ragged(torch, 25, 1, [n], [kv], page)
+    kc, vc = cache(torch, "plain", pages, page, Hk, d, dtype, 250)
+    q = rand(torch, 252, (n, Hk, d), dtype)
+    q[..., 5] = 1.0
+    slots = [2, kv // 2 // page, (kv - n // 2) // page]
+    gone = table[0, slots]
+    kc[gone, ..., 5] = float("-inf")
+    vc[gone] = bad
+    out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), return_lse=True)
+    holes = table.copy()
+    holes[0, slots] = -1
+    check_attention(torch, out, lse, q, kc, vc, holes, lens, cu, d ** -0.5, 0, dtype)
