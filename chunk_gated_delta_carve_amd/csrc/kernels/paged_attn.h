@@ -22,7 +22,7 @@
 // outside the cache and keys no row of the tile may see are loaded as zeros,
 // and a row whose result is not finite is computed again over its visible keys
 // alone (careful_row), since 0 x inf inside a product that other rows need
-// would have put a NaN there.
+// would have put a NaN there. So is a row whose scores are too large for one pass.
 //
 // Long contexts are split over `splits` workgroups per tile, each leaving
 // (o, m, l) in fp32; a second kernel joins them in a fixed order. Every
@@ -57,7 +57,18 @@ struct PagedArgs {
 // bf16, whose relative step is the same everywhere) and most blocks spare the
 // rescaling of o.
 constexpr float kSlack = 8.f;
-constexpr float kNoMax = -1e37f;                    // below every score that counts; c kNoMax stays finite (c < 24)
+constexpr float kNoMax = -1e37f;                    // where m starts: c kNoMax stays finite (c < 24)
+constexpr float kLeast = -3.4028234663852886e38f;   // m of a row without weights: no finite score lies below
+
+// The weights of a row that sees keys sum to about 1 or more (its maximum's own) and
+// to less than keys 2^kSlack. Outside of these bounds the sum tells nothing: scores
+// below kNoMax leave no weights, and from scores of about 2^24 / c on, the exponent
+// c x - c m holds the rounding of c m, which may be any number. Such a row is computed
+// again by careful_row, which forms c (x - m).
+constexpr float kLeastSum = 0x1p-20f, kMostSum = 0x1p60f;
+__device__ __forceinline__ bool odd_sum(float l, bool sees) {
+  return !(l >= kLeastSum && l <= kMostSum) && (sees || l != 0.f);
+}
 
 // The tile `t` of BM rows: its sequence, its rows and the keys they see.
 struct AttnTile {
@@ -177,6 +188,20 @@ __device__ __forceinline__ void note_cut(int* cut, const AttnTile& x, int h, int
   cut[0] = x.n0; cut[1] = x.row0; cut[2] = x.rows; cut[3] = h; cut[4] = count;
 }
 
+__device__ __forceinline__ float log_sum(const PagedArgs& a, float m, float l) {
+  return l == 0.f ? -__builtin_inff() : m * a.scale + fast_log2(l) * 0.6931471805599453f;
+}
+
+// First key at or behind k0 that a token at position p sees.
+__device__ __forceinline__ int first_seen(const PagedArgs& a, int p, int k0) {
+  const int k = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+  return k > k0 ? k : k0;
+}
+// Whether it sees a key of [k0, k1), holes aside.
+__device__ __forceinline__ bool sees_any(const PagedArgs& a, int p, int k0, int k1) {
+  return first_seen(a, p, k0) < (p + 1 < k1 ? p + 1 : k1);
+}
+
 // Where a row's results go: the output itself when one workgroup sees all of
 // the row's keys, otherwise its place among the partial results.
 template <typename E, int D>
@@ -196,10 +221,11 @@ struct RowOut {
   __device__ __forceinline__ float* part(int64_t at, int r) const { return a.po + slot(at, r) * D; }
   __device__ __forceinline__ void stats(int64_t at, int r, float m, float l) const {    // one lane per row
     if (whole) {
-      if (a.lse) a.lse[at] = l == 0.f ? -__builtin_inff() : (m * a.c + fast_log2(l)) * 0.6931471805599453f;
+      if (a.lse) a.lse[at] = log_sum(a, m, l);
     } else {
       float* p = a.pml + slot(at, r) * 2;
-      p[0] = m; p[1] = l;
+      p[0] = l == 0.f ? kLeast : m;
+      p[1] = l;
     }
   }
 };
@@ -216,8 +242,8 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
   const E* q = static_cast<const E*>(a.q) + at / a.Hq * a.q_row + at % a.Hq * D;
   const E* kc = static_cast<const E*>(a.kc) + h * a.kc_head;
   const E* vc = static_cast<const E*>(a.vc) + h * a.vc_head;
-  const int first = a.window > 0 && p - a.window + 1 > k0 ? p - a.window + 1 : k0, end = p + 1 < k1 ? p + 1 : k1;
-  float m = kNoMax, l = 0.f, o[PER];
+  const int first = first_seen(a, p, k0), end = p + 1 < k1 ? p + 1 : k1;
+  float m = kLeast, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   for (int j0 = first; j0 < end; j0 += 64) {
@@ -246,6 +272,7 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
     float top = s;
 #pragma unroll
     for (int w = 1; w < 64; w <<= 1) top = fmaxf(top, __shfl_xor(top, w));
+    if (top == -__builtin_inff()) continue;
     const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
     const float e = fast_exp2((s - mn) * a.c);      // +inf - +inf: NaN, as the formula has it
     m = mn;
@@ -601,7 +628,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
       }
     }
     const int64_t at = ro.index(x, r);
-    bool nf = not_finite(L);
+    bool nf = odd_sum(L, sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
@@ -784,10 +811,13 @@ struct TileWork {
     l += __shfl_xor(l, 32);
     const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
     const int r = wave * 32 + c;
+    const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
+    const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
+    const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
     bool nf = false;
     if (r < x.rows) {
       const int64_t at = ro.index(x, r);
-      nf = not_finite(l);
+      nf = odd_sum(l, sees_any(a, p, k0, k1));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -814,9 +844,6 @@ struct TileWork {
     }
     unsigned long long again = __ballot(nf);
     again = (again | again >> 32) & 0xffffffffull;
-    const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
-    const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
-    const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
     while (again) {
       const int i = __ffsll((unsigned long long)again) - 1;
       again &= again - 1;
@@ -1148,7 +1175,7 @@ __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int6
   using V = __attribute__((ext_vector_type(PER))) float;
   const int lane = lane_id(), wave = WAVES > 1 ? wave_id() : 0;
   auto slot = [&](int i) { return i == 0 ? first : next + (i - 1) * stride; };
-  float M = kNoMax, L = 0.f;
+  float M = kLeast, L = 0.f;
   V o = 0.f;
   const int run = (count + WAVES - 1) / WAVES, end = run * (wave + 1) < count ? run * (wave + 1) : count;
   for (int c0 = run * wave; c0 < end; c0 += 64) {
@@ -1209,7 +1236,7 @@ __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int6
 #pragma unroll
   for (int k = 0; k < PER; ++k) out[k] = from_f32<E>(o[k] * inv);
   if (lane == 0 && a.lse)
-    a.lse[at] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+    a.lse[at] = log_sum(a, M, L);
 }
 
 // The rows of a tile whose keys were shared, as its first share noted it down: one
@@ -1275,7 +1302,7 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
           for (int k = 0; k < PER; ++k) out[k] = (bf16)o[r][k];
         }
       if (a.lse && own == 0 && mine < rows)
-        a.lse[my] = L == 0.f ? -__builtin_inff() : (M * a.c + fast_log2(L)) * 0.6931471805599453f;
+        a.lse[my] = log_sum(a, M, L);
     }
   }
 }

@@ -895,3 +895,35 @@ def test_values_of_keys_that_count_for_nothing(torch, bad, dtype, n, kv, Hk, d):
     holes = table.copy()
     holes[0, slots] = -1
     check_attention(torch, out, lse, q, kc, vc, holes, lens, cu, d ** -0.5, 0, dtype)
+
+
+@pytest.mark.parametrize("dtype,n,kv,Hk,d", [
+    ("bf16", 4, 300, 1, 64), ("bf16", 4, 300, 2, 128), ("bf16", 90, 300, 1, 64), ("bf16", 90, 300, 2, 128),
+    ("bf16", 90, 300, 130, 128), ("f32", 4, 300, 1, 64), ("f32", 40, 300, 1, 128),
+    ("bf16", 4, 4000, 1, 128), ("bf16", 100, 4000, 1, 64), ("f32", 4, 4000, 1, 64)])
+@pytest.mark.parametrize("size,sign", [(2.0 ** e, sign) for e in (18, 30, 50, 63) for sign in (1, -1)])
+def test_scores_of_any_finite_size(torch, size, sign, dtype, n, kv, Hk, d):
+    """Scores q k of one channel between 2^36 and 2^128, all of one sign: neighbours differ by more than any weight
+    survives, so a row is the value of its highest key and lse is that key's scaled score. The products of two 8-bit
+    factors are exact in fp32. o: half a step for a weight that is not exactly 1 (bf16, tiles) and half a step for the
+    output, 2^-22 for the division. lse: a scale of 24 bits, the weight's own error of at most 2^-24 of the score, a
+    logarithm and a sum make less than 2^-22 of it."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    cu, lens, table, pages = ragged(torch, 26, 1, [n], [kv], 16)
+    kc, vc = cache(torch, "plain", pages, 16, Hk, d, dtype, 260)
+    vc = vc.bfloat16().to(vc.dtype)
+    rng = np.random.default_rng(27)
+    steps = rng.integers(0, 120, kv)             # the highest key stands out by at least 2^-8 of itself
+    q = torch.zeros(n, Hk, d, dtype=dt(torch, dtype), device="cuda")
+    q[..., 3] = size * torch.tensor(1 + rng.integers(0, 64, n) / 128, dtype=torch.float32).to(q)[:, None]
+    best = int(rng.integers(0, kv - n))           # every row sees it
+    steps[best] = 127 if sign > 0 else -1
+    cells = np.zeros(len(table[0]) * 16, np.float32)
+    cells[:kv] = sign * size * (1 + (steps if sign > 0 else steps + 1) / 128.0)
+    kc.zero_()
+    kc[ints(torch, table[0]).long(), :, :, 3] = torch.tensor(cells, device="cuda").view(-1, 16)[..., None].to(kc.dtype)
+    out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), return_lse=True)
+    row = vc[table[0, best // 16], best % 16].double()            # [Hk, d]
+    assert torch.all((out.double() - row).abs() <= (2.1 * HALF[dtype] + 2.0 ** -22) * row.abs())
+    want = q[..., 3].double() * kc[table[0, best // 16], best % 16, :, 3].double() * d ** -0.5
+    assert torch.all((lse.double() - want).abs() <= 2.0 ** -22 * want.abs())
