@@ -582,7 +582,7 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
   a.vc_page = c.vc_page; a.vc_tok = c.vc_tok; a.vc_head = c.vc_head;
   a.N = c.N; a.S = c.S; a.Hq = c.Hq; a.Hk = c.Hk; a.G = c.Hq / c.Hk;
   a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
-  a.window = c.window < (1 << 30) ? c.window : 1 << 30;
+  a.window = c.window;
   a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
   a.scale = c.scale; a.c = c.scale * carve::kLog2e;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {

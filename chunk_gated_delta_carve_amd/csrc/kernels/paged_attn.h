@@ -458,6 +458,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
   const int p = x.pos0 + row / a.G;
   const int p_min = x.pos0 + x.row0 / a.G, p_max = x.pos0 + (x.row0 + x.rows - 1) / a.G;
+  const int lo = first_seen(a, p, 0), lo_max = first_seen(a, p_max, 0);
   const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
   u32x4 q[NP];
 #pragma unroll
@@ -535,13 +536,13 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
       id[0] = id2[0]; id[1] = id2[1];
     }
     // lane: row c, keys 16 b + 4 g + i
-    if (ok != 0xffffffffu || j0 + KT - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+    if (ok != 0xffffffffu || j0 + KT - 1 > p_min || j0 < lo_max) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = 16 * b + 4 * g + i, j = j0 + kk;
-          const bool see = ((ok >> kk) & 1u) && j <= p && (a.window <= 0 || j > p - a.window);
+          const bool see = ((ok >> kk) & 1u) && j <= p && j >= lo;
           s[b][i] = see ? s[b][i] : -__builtin_inff();
         }
     }
@@ -677,6 +678,7 @@ struct TileWork {
   bool whole;
   int lane, wave, c, hf;                            // the wave's column and half of the lane
   int p, p_min, p_max;                              // position of the lane's row, of the wave's first and last
+  int lo_min, lo_max;                               // first keys that the wave's first and last rows see
   bf16x8 q[D / 16];
   const char *kb, *vb;
   const int* trow;
@@ -709,6 +711,8 @@ struct TileWork {
     p = x.pos0 + row / a.G;
     p_min = x.pos0 + (x.row0 + wr0) / a.G;
     p_max = x.pos0 + (x.row0 + wr1) / a.G;
+    lo_min = first_seen(a, p_min, 0);
+    lo_max = first_seen(a, p_max, 0);
     const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
@@ -785,7 +789,7 @@ struct TileWork {
         for (int u = 0; u < 16; ++u)
           s[kb2][u] = (mine >> (32 * kb2 + 8 * (u / 4) + u % 4)) & 1ull ? s[kb2][u] : -__builtin_inff();
     }
-    if (j0 + LY::BN - 1 > p_min || (a.window > 0 && j0 <= p_max - a.window)) {
+    if (j0 + LY::BN - 1 > p_min || j0 < lo_max) {
       const int far = p - j0 - 4 * hf;              // visible: far - window < key <= far
       const unsigned wide = a.window > 0 ? a.window : 0x7fffffff;
 #pragma unroll
@@ -913,7 +917,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedA
     fetch(t + 1, idn);
     idn = id2;
     const int j0 = (w.first_b + t) * LY::BN;
-    if (j0 <= w.p_max && (a.window <= 0 || j0 + LY::BN - 1 > w.p_min - a.window)) {
+    if (j0 <= w.p_max && j0 + LY::BN > w.lo_min) {
       const char* kl = lds + buf * buf_bytes;
       const char* vl = kl + LY::k_bytes;
       f32x16 s[2];
@@ -1043,9 +1047,9 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
   w.have_queries();
 
   // the blocks [w0, w1) of the workgroup's that some row of the wave sees
-  int w0 = 0, w1 = w.p_max < 0 ? 0 : (w.p_max >> 6) + 1 - w.first_b;
+  int w0, w1 = w.p_max < 0 ? 0 : (w.p_max >> 6) + 1 - w.first_b;
   w1 = w1 < T ? w1 : T;
-  if (a.window > 0 && w.p_min - a.window + 1 > 0) w0 = ((w.p_min - a.window + 1) >> 6) - w.first_b;
+  w0 = (w.lo_min >> 6) - w.first_b;
   w0 = w0 > 0 ? w0 : 0;
   if (w0 >= w1) w0 = w1 = T + 2;
 

@@ -927,3 +927,35 @@ def test_scores_of_any_finite_size(torch, size, sign, dtype, n, kv, Hk, d):
     assert torch.all((out.double() - row).abs() <= (2.1 * HALF[dtype] + 2.0 ** -22) * row.abs())
     want = q[..., 3].double() * kc[table[0, best // 16], best % 16, :, 3].double() * d ** -0.5
     assert torch.all((lse.double() - want).abs() <= 2.0 ** -22 * want.abs())
+
+
+@pytest.mark.parametrize("dtype,n,d", [("bf16", 1, 64), ("bf16", 100, 64), ("bf16", 100, 128), ("f32", 3, 128)])
+def test_a_window_wider_than_any_table(torch, dtype, n, d):
+    """Lengths far past the table with windows above 2^30: the keys in the table that the windows reach are seen."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    width, page, pages = 8, 16, 8
+    kc, vc = cache(torch, "plain", pages, page, 2, d, dtype, 270)
+    q = rand(torch, 272, (n, 4, d), dtype)
+    table, cu = np.random.default_rng(28).permutation(pages)[None], [0, n]
+    for kv, window in ((2 ** 30 + 200, 2 ** 30 + 50), (2 ** 30 + 100, 2 ** 30 + 50), (2 ** 31 - 1, 2 ** 31 - 1),
+                       (2 ** 31 - 1, 2 ** 31 - 60), (50, 2 ** 31 - 1), (5, 2 ** 31 - 1)):
+        out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, [kv]), ints(torch, cu), window=window,
+                                   return_lse=True)
+        # the same rows one by one over the part of the table that each sees
+        want, wl = np.zeros((n, 4, d)), np.full((n, 4), -np.inf)
+        bo, bl = np.zeros((n, 4, d)), np.zeros((n, 4))
+        for i in range(n):
+            p = kv - n + i
+            seen = [j for j in range(max(0, p - window + 1), min(p + 1, width * page))]
+            if not seen:
+                continue
+            o, l, A, reach, keys = orc.paged_attention(
+                f64(q[i:i + 1]), *(f64(c[table[0]]).reshape(1, width * page, 2, d)[:, seen] for c in (kc, vc)),
+                np.array([[0]]), [len(seen)], [0, 1], d ** -0.5, 0)
+            want[i], wl[i] = o[0], l[0]
+            b = attention_bounds(dtype, d, d ** -0.5, o, l, A, reach, keys)
+            bo[i], bl[i] = b[0][0], b[1][0]
+        close("o", out, want, bo)
+        empty = np.isneginf(wl)
+        assert np.array_equal(np.isneginf(f64(lse)), empty) and (kv == 2 ** 30 + 200 or not empty.all())
+        assert np.all(np.abs(f64(lse)[~empty] - wl[~empty]) <= bl[~empty])
