@@ -66,8 +66,8 @@ constexpr float kLeast = -3.4028234663852886e38f;   // m of a row without weight
 // c x - c m holds the rounding of c m, which may be any number. Such a row is computed
 // again by careful_row, which forms c (x - m).
 constexpr float kLeastSum = 0x1p-20f, kMostSum = 0x1p60f;
-__device__ __forceinline__ bool odd_sum(float l, bool sees) {
-  return !(l >= kLeastSum && l <= kMostSum) && (sees || l != 0.f);
+__device__ __forceinline__ bool odd_sum(float l) {   // 0, which rows that see nothing have, apart
+  return !(l >= kLeastSum && l <= kMostSum) && l != 0.f;
 }
 
 // The tile `t` of BM rows: its sequence, its rows and the keys they see.
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
       }
     }
     const int64_t at = ro.index(x, r);
-    bool nf = odd_sum(L, sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
+    bool nf = odd_sum(L) || (L == 0.f && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
@@ -815,13 +815,11 @@ struct TileWork {
     l += __shfl_xor(l, 32);
     const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
     const int r = wave * 32 + c;
-    const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
-    const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
-    const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
-    bool nf = false;
+    bool nf = false, none = false;
     if (r < x.rows) {
       const int64_t at = ro.index(x, r);
-      nf = odd_sum(l, sees_any(a, p, k0, k1));
+      nf = odd_sum(l);
+      none = l == 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -846,7 +844,11 @@ struct TileWork {
       }
       if (hf == 0) ro.stats(at, r, m, l);
     }
+    const int k0 = first_b * LY::BN > x.lo ? first_b * LY::BN : x.lo;
+    const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
+    const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
     unsigned long long again = __ballot(nf);
+    if (__ballot(none)) again |= __ballot(none && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
     again = (again | again >> 32) & 0xffffffffull;
     while (again) {
       const int i = __ffsll((unsigned long long)again) - 1;
