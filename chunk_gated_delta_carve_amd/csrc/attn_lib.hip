@@ -237,13 +237,13 @@ Plan plan_of(const carve_paged_config* c) {
   p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)(seen < kLongKeys ? kRowsShort : kRowsLong) * c->S;
   auto tiles = [&](int BM) { return step ? c->S * up(G, BM) : up((int64_t)c->N * G, BM) + c->S - 1; };
   p.waves = c->d == 128 && 2 * tiles(256) * c->Hk > kCUs ? 8 : 4;
-  const int per_cu = p.waves == 8 ? 1 : c->d == 64 ? 4 : 2;   // workgroups of the tile kernels
   const int BM = p.tile ? 32 * p.waves : 16, BN = p.tile ? 64 : 128;
   p.tiles = tiles(BM);
   if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
   if (p.tile) {
+    // four waves: as many workgroups as the CUs hold at once; eight fill them with a tile each
     const int64_t most = up(keys, (int64_t)BN * 4);
-    int64_t s = kCUs * per_cu / (p.tiles * c->Hk);
+    int64_t s = p.waves == 8 ? 1 : kCUs * (c->d == 64 ? 4 : 2) / (p.tiles * c->Hk);
     s = s < most ? s : most;
     s = s < kTileSplits ? s : kTileSplits;
     p.splits = s < 1 ? 1 : (int)s;
@@ -278,13 +278,16 @@ hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(LY::NT), LY::bytes, s, a);
   e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const unsigned tiles = a.tiles * a.Hk;
-  if (a.splits > carve::kFewShares || (int64_t)a.N * a.Hq < kManyRows)
-    hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 1>), dim3(tiles, LY::BM / 4), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 8>), dim3(tiles, LY::BM / 32), dim3(256), 0, s, a);
-  return hipGetLastError();
+  if constexpr (WAVES == 4) {
+    if (e != hipSuccess || a.splits == 1) return e;
+    const unsigned tiles = a.tiles * a.Hk;
+    if (a.splits > carve::kFewShares || (int64_t)a.N * a.Hq < kManyRows)
+      hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 1>), dim3(tiles, LY::BM / 4), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 8>), dim3(tiles, LY::BM / 32), dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 template <typename E, int D>

@@ -24,10 +24,10 @@
 // alone (careful_row), since 0 x inf inside a product that other rows need
 // would have put a NaN there. So is a row whose scores are too large for one pass.
 //
-// Long contexts are split over `splits` workgroups per tile, each leaving
-// (o, m, l) in fp32; a second kernel joins them in a fixed order. Every
-// tile works out from its own key range how many of them it needs, so no length
-// is read on the host and a captured graph follows the lengths on the device.
+// Where rows are few, long contexts are split over workgroups, each leaving
+// (o, m, l) in fp32; a second kernel joins them in a fixed order. How many a tile
+// needs is worked out from its own key range on the device, so no length is read
+// on the host and a captured graph follows the lengths there.
 #pragma once
 #include "common.h"
 #include "rope.h"
@@ -672,6 +672,7 @@ template <int D, int NW, bool WIDE>
 struct TileWork {
   using LY = TileLayout<D, NW>;
   using E = bf16;
+  static constexpr bool SPLIT = NW == 4;            // eight waves run where tiles fill the CUs: one workgroup each
   const PagedArgs& a;
   AttnTile x;
   int h, sp, first_b, T;                            // key/value head, share, first block, blocks
@@ -688,21 +689,28 @@ struct TileWork {
   __device__ __forceinline__ TileWork(const PagedArgs& a_) : a(a_) {
     h = blockIdx.x % a.Hk;
     const int rest = blockIdx.x / a.Hk;
-    sp = rest / a.tiles;
+    sp = SPLIT ? rest / a.tiles : 0;
     // the last tiles of a sequence see the most keys: start with them
-    x = find_tile(a, a.tiles - 1 - rest % a.tiles, LY::BM);
+    x = find_tile(a, a.tiles - 1 - (SPLIT ? rest % a.tiles : rest), LY::BM);
     T = 0;
-    int* cut = a.splits > 1 && sp == 0 && threadIdx.x == 0 ? a.cuts + (int64_t)blockIdx.x * kCutInts : nullptr;
-    if (cut) cut[2] = 0;
-    if (x.rows <= 0) return;
-    const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
-    if (cut && sh.count > 1) note_cut(cut, x, h, sh.count);
-    if (sp > 0 && sp >= sh.count) { x.rows = 0; return; }
-    whole = sh.count <= 1;
-    first_b = sh.b0 + sp * sh.per;
-    const int all = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN : sh.b0;
-    const int last_b = sh.per < all - first_b ? first_b + sh.per : all;
-    T = last_b > first_b ? last_b - first_b : 0;
+    if constexpr (SPLIT) {
+      int* cut = a.splits > 1 && sp == 0 && threadIdx.x == 0 ? a.cuts + (int64_t)blockIdx.x * kCutInts : nullptr;
+      if (cut) cut[2] = 0;
+      if (x.rows <= 0) return;
+      const Share sh = share_of(x.lo, x.hi, LY::BN, share_blocks(a, LY::BM, LY::BN, LY::LEAST));
+      if (cut && sh.count > 1) note_cut(cut, x, h, sh.count);
+      if (sp > 0 && sp >= sh.count) { x.rows = 0; return; }
+      whole = sh.count <= 1;
+      first_b = sh.b0 + sp * sh.per;
+      const int all = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN : sh.b0;
+      const int last_b = sh.per < all - first_b ? first_b + sh.per : all;
+      T = last_b > first_b ? last_b - first_b : 0;
+    } else {
+      if (x.rows <= 0) return;
+      whole = true;
+      first_b = x.lo / LY::BN;
+      T = x.hi > x.lo ? (x.hi + LY::BN - 1) / LY::BN - first_b : 0;
+    }
     lane = lane_id(); wave = wave_id(); c = lane & 31; hf = lane >> 5;
     // rows past the tile's end repeat the last one and are not stored
     const int wr0 = wave * 32 < x.rows ? wave * 32 : x.rows - 1;
@@ -813,7 +821,7 @@ struct TileWork {
   }
   __device__ __forceinline__ void finish(const f32x16 (&o)[D / 32], float m, float l) const {
     l += __shfl_xor(l, 32);
-    const RowOut<E, D> ro{a, h, whole, (int64_t)sp * a.N * a.Hq, 0};
+    const RowOut<E, D> ro{a, h, !SPLIT || whole, (int64_t)sp * a.N * a.Hq, 0};
     const int r = wave * 32 + c;
     bool nf = false, none = false;
     if (r < x.rows) {
@@ -824,7 +832,7 @@ struct TileWork {
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int u = 0; u < 16; ++u) nf = nf || not_finite(o[i][u]);
-      if (whole) {
+      if (!SPLIT || whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         E* out = ro.out(at) + 4 * hf;
 #pragma unroll
