@@ -22,6 +22,7 @@ from . import _lib
 from .api import _DTYPES
 
 _I32 = torch.int32
+_MOST = 2**31 - 1                        # the library's sizes have 32 bits
 
 
 def rope_tables(length, rot, base=10000.0, device="cuda"):
@@ -128,6 +129,8 @@ def _angles(cos, sin, device):
     shape = cos.shape
     if len(shape) != 2:
         raise ValueError(f"cos: expected [positions, rot / 2], got {tuple(shape)}")
+    if shape[0] > _MOST or 2 * shape[1] > _MOST:
+        raise ValueError(f"cos: sizes past 32 bits: {tuple(shape)}")
     return (_flat(cos, "cos", shape, torch.float32, device), _flat(sin, "sin", shape, torch.float32, device),
             2 * shape[1], shape[0])
 
@@ -235,6 +238,8 @@ def _sequences(block_table, kv_lens, cu_seqlens, N, dev):
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected [sequences, pages each], got {tuple(block_table.shape)}")
     S, width = block_table.shape
+    if S > _MOST or width > _MOST or N > _MOST:
+        raise ValueError(f"sizes past 32 bits: {N} tokens, a block_table of {tuple(block_table.shape)}")
     row, step = block_table.stride()
     if block_table.dtype is not _I32 or block_table.device != dev:
         _like(block_table, "block_table", _I32, dev)
@@ -249,7 +254,7 @@ def _sequences(block_table, kv_lens, cu_seqlens, N, dev):
 
 def _window(n):
     """A window as the library takes it: beyond 32 bits it hides nothing that one of 32 bits shows."""
-    return max(-1, min(n, 2**31 - 1))
+    return max(-1, min(n, _MOST))
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None, q=None,
@@ -337,7 +342,7 @@ def paged_workspace_bytes(N, S, Hq, Hk, d, page_size, width, dtype=torch.bfloat1
     """Bytes of workspace paged_attention needs for N new tokens of S sequences (step: one each) with a block table
     `width` pages wide."""
     for name, n in (("N", N), ("S", S), ("Hq", Hq), ("Hk", Hk), ("d", d), ("page_size", page_size), ("width", width)):
-        if not 0 <= n < 2**31:
+        if not 0 <= n <= _MOST:
             raise ValueError(f"{name}: expected a size of 32 bits, got {n}")
     c = _lib.CarvePagedConfig()
     c.N, c.S, c.Hq, c.Hk, c.d, c.page_size, c.pages, c.width = N, S, Hq, Hk, d, page_size, 1, width

@@ -403,3 +403,21 @@ def test_the_row_kernels_blocks_fit_32_bits(L):
         else:
             assert code == _lib.CARVE_EUNSUPPORTED and items * (blocks + 3) >= 2 ** 31, (N, window)
     assert codes == {_lib.CARVE_OK, _lib.CARVE_EUNSUPPORTED}
+
+
+def test_tensors_past_32_bits_in_python():
+    """Sizes that the library would take modulo 2^32: a table of 2^32 + 4 pages is none of four."""
+    torch = pytest.importorskip("torch")
+    from chunk_gated_delta_carve_amd.attention import _angles, _sequences
+    meta = torch.device("meta")
+    ints = lambda *shape: torch.empty(shape, dtype=torch.int32, device=meta)  # noqa: E731
+    f32 = lambda *shape: torch.empty(shape, device=meta)  # noqa: E731
+    assert _sequences(ints(3, 4), ints(3), ints(4), 9, meta)[:3] == (3, 4, 4)
+    for table, lens, cu, N in ((ints(3, 2**32 + 4), ints(3), ints(4), 9), (ints(2**31, 1), ints(2**31), None, 2**31),
+                               (ints(3, 4), ints(3), ints(4), 2**32 + 9)):
+        with pytest.raises(ValueError):
+            _sequences(table, lens, cu, N, meta)
+    assert _angles(f32(10, 32), f32(10, 32), meta)[2:] == (64, 10)
+    for shape in ((2**32 + 10, 8), (1, 2**31 + 32)):
+        with pytest.raises(ValueError):
+            _angles(f32(*shape), f32(*shape), meta)
