@@ -263,7 +263,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     qk_norm_rope_fwd, at their own positions. Shapes: k, v [N, Hk, d], packed sequence after sequence; caches
     [pages, page_size, Hk, d], page_size a power of two; block_table int32 [S, pages each]; kv_lens int32 [S], the
     lengths with the new tokens counted; cu_seqlens int32 [S + 1], where each sequence's new tokens start (None:
-    one each); q [N, Hq, d], q_out may be q itself. No two entries of a cache may overlap. A token whose position
+    one each); q [N, Hq, d], q_out may be q itself. No two entries of the caches may overlap. A token whose position
     is negative or past its table, or whose page number is not in [0, pages), is not stored; tokens behind
     cu_seqlens[S] are left alone. Returns q_out (None without q)."""
     dt, dev = _first(k, "k", "paged_append")

@@ -195,6 +195,29 @@ bool entries_overlap(const carve_paged_config* c, int64_t page, int64_t tok, int
   return false;
 }
 
+// Whether an entry of k_cache and one of v_cache share channels, where both have the
+// same strides (each past what the smaller ones reach, as entries_overlap saw to):
+// the distance of the two starts is then looked for among the distances of entries,
+// from the largest stride down. Caches that interleave with different strides are
+// the caller's to keep apart.
+bool caches_overlap(const carve_paged_config* c, const void* k_cache, const void* v_cache) {
+  struct Dim { int64_t n, k, v; } dims[3] = {{c->pages, c->kc_page, c->vc_page}, {c->page_size, c->kc_tok, c->vc_tok},
+                                             {c->Hk, c->kc_head, c->vc_head}};
+  for (const Dim& x : dims)
+    if (x.n < 1) return false;
+    else if (x.n > 1 && x.k != x.v) return false;
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return (x.n > 1 ? x.k : 0) > (y.n > 1 ? y.k : 0); });
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache));
+  auto meets = [&](auto&& self, int i, int64_t left) -> bool {
+    if (i == 3 || dims[i].n < 2) return left < c->d && left > -(int64_t)c->d;
+    const int64_t s = dims[i].k, q = left / s;
+    for (int64_t m = q - 1; m <= q + 1; ++m)
+      if (m < dims[i].n && m > -dims[i].n && self(self, i + 1, left - m * s)) return true;
+    return false;
+  };
+  return meets(meets, 0, apart / (int64_t)elem_bytes(c->dtype));
+}
+
 size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {
   if (c->pages == 0 || c->Hk == 0) return 0;
   return (size_t)((c->pages - 1) * page + (c->page_size - 1) * tok + (c->Hk - 1) * head + c->d) * elem_bytes(c->dtype);
@@ -481,11 +504,11 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   if (overlaps(ro, rk) || overlaps(ro, rv) || (!same(ro, rq) && overlaps(ro, rq))) return CARVE_EINVAL;
   for (const Rows& r : side)
     if (overlaps(ro, r)) return CARVE_EINVAL;
-  // the two caches may interleave in one tensor; nothing else may lie in them
+  // the two caches may interleave in one tensor; nothing else lies in them
   for (const Rows& r : {rq, rk, rv, ro, side[0], side[1], side[2], side[3], side[4], side[5], side[6]})
     if (carve_host::overlaps(k_cache, ks, r.p, r.span()) || carve_host::overlaps(v_cache, vs, r.p, r.span()))
       return CARVE_EINVAL;
-  if (c.Hk > 0 && k_cache == v_cache && ks > 0) return CARVE_EINVAL;
+  if (k_cache && v_cache && caches_overlap(cfg, k_cache, v_cache)) return CARVE_EINVAL;
   if (!work) return CARVE_OK;
   carve::AppendArgs a{};
   a.k = k; a.v = v; a.q = q; a.wq = q_weight; a.wk = k_weight;

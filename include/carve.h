@@ -346,7 +346,8 @@ typedef struct {
  *   k, v [N,Hk,d], q [N,Hq,d] or NULL (Hq = 0); q_out may be q itself
  * A token whose position is negative or lies past the table, or whose page
  * number is outside [0, pages), is not stored. No page may be shared by two
- * sequences that store to it, and no two entries of a cache may overlap. */
+ * sequences that store to it, and no two entries of the caches may overlap
+ * (refused, between the two caches only where their strides are the same). */
 int carve_paged_append(const carve_paged_config* cfg, const void* k, const void* v, const void* q,
                        const void* q_weight, const void* k_weight, const float* cos, const float* sin,
                        const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* k_cache, void* v_cache,

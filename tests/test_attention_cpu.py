@@ -389,7 +389,8 @@ def test_the_row_kernels_blocks_fit_32_bits(L):
     rng = np.random.default_rng(31)
     codes = set()
     cases = [(524288, w, 64) for w in (0, 256, 1024)] + [(1 << 20, 1024, 64), (700000, 1024, 128)]
-    cases += [(int(2.0 ** rng.uniform(10, 22)), int(rng.choice([0, 2.0 ** rng.uniform(0, 22)])), 64) for _ in range(200)]
+    cases += [(int(2.0 ** rng.uniform(10, 22)), int(rng.choice([0, 2.0 ** rng.uniform(0, 22)])), 64)
+              for _ in range(200)]
     for N, window, page in cases:
         c = paged_cfg(N=N, S=1, Hq=16, Hk=4, page_size=page, pages=N // page + 1, width=N // page + 1, window=window,
                       dtype=_lib.CARVE_F32)
@@ -421,3 +422,31 @@ def test_tensors_past_32_bits_in_python():
     for shape in ((2**32 + 10, 8), (1, 2**31 + 32)):
         with pytest.raises(ValueError):
             _angles(f32(*shape), f32(*shape), meta)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(kc_page=4096, vc_page=4096), dict(kc_tok=256, vc_tok=256, kc_page=4096, vc_page=4096),
+    dict(kc_tok=64, vc_tok=64, kc_head=1024, vc_head=1024), dict(kc_tok=1536, vc_tok=1536, kc_page=128, vc_page=128),
+    dict(kc_head=192, vc_head=192, kc_tok=576, vc_tok=576, kc_page=9216, vc_page=9216),
+    dict(pages=1, kc_page=0, vc_page=64),
+    dict(Hk=1, Hq=4, kc_head=0, vc_head=64, kc_tok=192, vc_tok=192, kc_page=4096, vc_page=4096)],
+    ids=[str(i) for i in range(8)])
+def test_append_refuses_caches_that_share_channels(L, kw):
+    """v_cache at every distance of a step of 16 bytes from k_cache, against the entries themselves: refused where two
+    share a channel, and only there (N = 0: nothing is launched)."""
+    c = paged_cfg(N=0, **kw)
+    at = [(c.pages, c.kc_page), (c.page_size, c.kc_tok), (c.Hk, c.kc_head)]
+    starts = np.zeros(1, np.int64)
+    for n, s in at:
+        starts = (starts[:, None] + np.arange(n)[None] * s).ravel()
+    taken = np.zeros(int(starts.max()) + c.d, bool)
+    taken[(starts[:, None] + np.arange(c.d)[None]).ravel()] = True
+    mid = FAKE + 64 * MB
+    got = want = 0
+    for apart in [*range(-len(taken) - 64, len(taken) + 65, 8 if len(taken) < 10000 else 56)]:
+        a, b = max(0, apart), max(0, -apart)
+        meet = bool(np.any(taken[a:len(taken) - b] & taken[b:len(taken) - a])) if abs(apart) < len(taken) else False
+        code = append(L, c, k_cache=mid, v_cache=mid + 2 * apart)
+        assert (code == _lib.CARVE_EINVAL) == meet and code in (_lib.CARVE_OK, _lib.CARVE_EINVAL), apart
+        got, want = got + (code != _lib.CARVE_OK), want + meet
+    assert got == want > 0
