@@ -959,3 +959,79 @@ def test_a_window_wider_than_any_table(torch, dtype, n, d):
         empty = np.isneginf(wl)
         assert np.array_equal(np.isneginf(f64(lse)), empty) and (kv == 2 ** 30 + 200 or not empty.all())
         assert np.all(np.abs(f64(lse)[~empty] - wl[~empty]) <= bl[~empty])
+
+
+# the forms that large calls take: several pieces to a lane, several trips of the gradient's loop
+
+MANY = [
+    # as ROPE; waves take 2, 3, 3 (two waves to a token), 4, 4, 3 and 3 pieces a lane
+    ("bf16", (20, 150), 12, 4, 64, 64, False, True, True, False),
+    ("bf16", (1500,), 16, 4, 64, 32, True, True, True, True),
+    ("bf16", (901,), 16, 2, 128, 128, False, True, True, True),
+    ("bf16", (7, 160), 17, 13, 64, 48, False, True, False, False),
+    ("f32", (11, 100), 12, 4, 64, 64, False, True, True, False),
+    ("f32", (1401,), 5, 1, 128, 128, True, True, True, True),
+    ("f32", (1399,), 3, 2, 128, 64, False, False, False, True),
+]
+MANY_IDS = ["-".join(str(x).replace(" ", "") for x in c) for c in MANY]
+
+
+@pytest.mark.parametrize("case", MANY, ids=MANY_IDS)
+def test_norm_rope_of_many_tokens(torch, case):
+    test_norm_rope(torch, case)
+
+
+# 1024 blocks take 32, 16 or 8 rows a trip (16 and 32 lanes a row): two trips and more here
+MANY_ROWS = [("bf16", (20, 150), 12, 12, 64, 64, False, True, True, False),
+             ("bf16", (1401,), 16, 4, 128, 128, False, True, True, True),
+             ("bf16", (9, 199), 20, 1, 64, 32, True, True, True, False),
+             ("f32", (1201,), 12, 4, 64, 64, True, True, True, True),
+             ("f32", (13, 100), 12, 4, 128, 96, False, True, True, False),
+             ("f32", (1300,), 8, 2, 128, 128, False, False, False, True)]
+
+
+@pytest.mark.parametrize("case", MANY_ROWS, ids=["-".join(str(x).replace(" ", "") for x in c) for c in MANY_ROWS])
+def test_norm_rope_gradient_of_many_rows(torch, case):
+    test_norm_rope_gradient(torch, case)
+
+
+MANY_NEW = [
+    # as APPEND; 2, 3, 3 (two waves) and 4 pieces a lane
+    ("bf16", 8, 4, 64, 16, [1200, 1, 900], [1300, 50, 900], 64, False, True, "plain", False),
+    ("bf16", 0, 10, 64, 32, [1500], [1500], 32, True, False, "heads", False),
+    ("bf16", 12, 3, 128, 64, [500, 420], [700, 420], 128, False, True, "joint", False),
+    ("f32", 8, 4, 64, 16, [700, 411], [700, 600], 64, True, True, "plain", False),
+    ("f32", 2, 2, 128, 16, [900, 500], [900, 700], 128, False, False, "heads", False),
+]
+
+
+@pytest.mark.parametrize("case", MANY_NEW, ids=[str(i) for i in range(len(MANY_NEW))])
+def test_append_of_many_tokens(torch, case):
+    test_append(torch, case)
+
+
+@pytest.mark.parametrize("d,G,n,kv,page,window", [(64, 1, 1, 40, 16, 0), (64, 4, 3, 50, 4, 0), (128, 4, 1, 33, 16, 0),
+                                                  (128, 2, 6, 90, 64, 40)])
+def test_few_rows_keep_sixteen_bits_of_the_weights(torch, d, G, n, kv, page, window):
+    """With few rows the weights enter the second product as two bf16 parts: what is left of a weight is at most half a
+    step of half a step, 2^-16 of it. Small queries keep the scores' own error below that. Against outputs near 0, where
+    the output's rounding is small, one part would show: 2^-9 of |v| over the root of the number of keys."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    cu, lens, table, pages = ragged(torch, 33, 1, [n], [kv], page)
+    kc, vc = cache(torch, "plain", pages, page, 2, d, "bf16", 330)
+    q = rand(torch, 332, (n, 2 * G, d), "bf16", 0.05)
+    out, lse = paged_attention(q, kc, vc, ints(torch, table), ints(torch, lens), ints(torch, cu), window=window,
+                               return_lse=True)
+    o, l, A, reach, keys = orc.paged_attention(f64(q), f64(kc), f64(vc), table, lens, cu, d ** -0.5, window)
+    e = d ** -0.5 * (d + 4) * 2.0 ** -24 * reach + 2.0 ** -20
+    slack = 2 * e + (keys[:, None] + 64) * 2.0 ** -24 + 2.0 ** -16
+    close("o", out, o, HALF["bf16"] * np.abs(o) + slack[..., None] * A)
+    assert np.all(np.abs(f64(lse) - l) <= e + (keys[:, None] + 64) * 2.0 ** -24 + 2.0 ** -22 * np.abs(l))
+    # the bound tells the two apart: weights rounded to one part fail it
+    s0 = f64(kc)[table[0]].reshape(-1, 2, d)[:kv], f64(vc)[table[0]].reshape(-1, 2, d)[:kv]
+    p = kv - 1
+    seen = slice(max(0, p - window + 1) if window else 0, kv)
+    w = np.exp(d ** -0.5 * s0[0][seen, 0] @ f64(q)[-1, 0])
+    one = f64(torch.tensor(w / w.max(), dtype=torch.float32).bfloat16())
+    rough = one @ s0[1][seen, 0] / (w / w.max()).sum()
+    assert np.any(np.abs(rough - o[-1, 0]) > HALF["bf16"] * np.abs(o[-1, 0]) + slack[-1, 0] * A[-1, 0])
