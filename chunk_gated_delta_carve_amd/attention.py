@@ -305,6 +305,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, 
     and the lengths). q [N, Hq, d], Hq a multiple of the cache's heads (query head h reads head h // (Hq / Hk)). A
     token at position p sees the keys j <= p and, with a window, j > p - window. scale: 1 / sqrt(d) when None.
     A token that sees no key has o = 0 and lse = -inf; tokens behind cu_seqlens[S] are left as they were in `out`.
+    One kernel serves the call: a long prompt chunk beside many single tokens is faster in a call of its own.
     workspace: device scratch to use (paged_workspace_bytes of it); allocated when None. Returns o [N, Hq, d], and
     lse [N, Hq] fp32 when return_lse."""
     dt, dev = _first(q, "q", "paged_attention")

@@ -316,8 +316,8 @@ __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x)
 // are laid end to end, and every workgroup takes an equal stretch of blocks.
 // An item that ends up in several workgroups leaves partial results: a workgroup
 // has at most two, the item its stretch starts inside of and the one it ends in.
-// 64 sequences of 200 to 8192 keys, 4 heads of 128 (551 MB): 110 us, 5.0 TB/s, the
-// rate of a large copy; with a fixed number of shares per sequence 132 us.
+// 64 sequences of 200 to 8192 keys, 4 heads of 128 (551 MB): 110 to 113 us, 5.0 TB/s,
+// the rate of a large copy; with a fixed number of shares per sequence 132 us.
 template <typename E, int D>
 struct RowsLayout {
   static constexpr int BM = 16, KT = 32, BN = 128;                               // BN: keys per round of four waves
@@ -871,10 +871,10 @@ struct TileWork {
 // products here (130 vector instructions of a softmax block against 16 products),
 // and four waves per SIMD issue it faster than two that interleave: on ragged
 // windowed prompts (51 GFLOP) the kernel below took 133 us when this one, then
-// with three workgroups per CU, took 107 us; now about 98 us. In the loop the matrix
-// units are busy 57% of the time; a workgroup of 18 blocks spends an eighth of its
-// time on finding its tile and its first loads. d = 128: two workgroups per CU, for
-// calls of few tiles.
+// with three workgroups per CU, took 107 us; with four a call takes 90 to 92 us (560
+// TFLOP/s). In the loop the matrix units are busy 57% of the time; a workgroup of 18
+// blocks spends an eighth of its time on finding its tile and its first loads.
+// d = 128: two workgroups per CU, for calls of few tiles.
 template <int D, bool WIDE>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedArgs a) {
   using W = TileWork<D, 4, WIDE>;
@@ -990,9 +990,9 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedA
 // "pair p" is keys p + 1 and values p. Step t, between two barriers, writes pair
 // t + 1 (keys t + 2 over keys t, read in step t - 1; values t + 1 over values
 // t - 1, likewise) while it reads keys t + 1 and values t.
-// 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 528 us, 911 TFLOP/s, where
-// the kernel above takes 600 us. Those are 256 workgroups of 192 to 256 blocks on
-// 256 CUs: the longest decides, an eighth above the mean.
+// 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 495 to 527 us a call by card,
+// 913 to 970 TFLOP/s, where the kernel above takes 600 us. Those are 256 workgroups of
+// 192 to 256 blocks on 256 CUs: the longest decides, an eighth above the mean.
 template <int D, bool WIDE>
 __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
   using W = TileWork<D, 8, WIDE>;

@@ -361,13 +361,18 @@ int carve_paged_workspace(const carve_paged_config* cfg, int64_t* bytes);
  *   o = softmax(scale q k^T) v,   lse = log sum exp(scale q k^T)
  *   q [N,Hq,d], o [N,Hq,d] dtype (o overlaps no input); lse [N,Hq] fp32 or NULL;
  *   the caches have at least one page
- * Softmax statistics and sums are fp32; in bf16 the weights are rounded to bf16
- * for the product with v. A token that sees no key (a negative position) has o = 0
- * and lse = -inf. Keys whose page number is outside [0, pages) or past the table
- * are not seen, and neither is a key whose score is -inf. What is not seen does not
- * matter, infinities and NaN included.
+ * Softmax statistics and sums are fp32; in bf16 the weights enter the product with
+ * v as one bf16 number (off by at most 2^-8 of each), or as two (2^-16) where the
+ * call has few rows (tokens x grouped heads) per sequence. A token that sees no key
+ * (a negative position) has o = 0 and lse = -inf. Keys whose page number is outside
+ * [0, pages) or past the table are not seen, and neither is a key whose score q k is
+ * -inf; a finite score counts, however large. What is not seen does not matter,
+ * infinities and NaN included.
  * The workspace may be shared by calls that do not overlap in time. Results are
- * deterministic (no atomics). */
+ * deterministic (no atomics): a call with the same sizes and inputs gives the same
+ * bits. The kernel is chosen for the whole call from its sizes, so a sequence's last
+ * bits, and in bf16 the rounding of its weights, may depend on what it is batched
+ * with; single tokens and a long prompt chunk are faster in calls of their own. */
 int carve_paged_attention(const carve_paged_config* cfg, const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
