@@ -203,19 +203,23 @@ bool entries_overlap(const carve_paged_config* c, int64_t page, int64_t tok, int
 bool caches_overlap(const carve_paged_config* c, const void* k_cache, const void* v_cache) {
   struct Dim { int64_t n, k, v; } dims[3] = {{c->pages, c->kc_page, c->vc_page}, {c->page_size, c->kc_tok, c->vc_tok},
                                              {c->Hk, c->kc_head, c->vc_head}};
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache)) /
+                        (int64_t)elem_bytes(c->dtype);
+  auto same_place = [&](int64_t n) { return n < c->d && n > -(int64_t)c->d; };
   for (const Dim& x : dims)
     if (x.n < 1) return false;
-    else if (x.n > 1 && x.k != x.v) return false;
+  if (same_place(apart)) return true;               // the first entries
+  for (const Dim& x : dims)
+    if (x.n > 1 && x.k != x.v) return false;
   std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return (x.n > 1 ? x.k : 0) > (y.n > 1 ? y.k : 0); });
-  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache));
   auto meets = [&](auto&& self, int i, int64_t left) -> bool {
-    if (i == 3 || dims[i].n < 2) return left < c->d && left > -(int64_t)c->d;
+    if (i == 3 || dims[i].n < 2) return same_place(left);
     const int64_t s = dims[i].k, q = left / s;
     for (int64_t m = q - 1; m <= q + 1; ++m)
       if (m < dims[i].n && m > -dims[i].n && self(self, i + 1, left - m * s)) return true;
     return false;
   };
-  return meets(meets, 0, apart / (int64_t)elem_bytes(c->dtype));
+  return meets(meets, 0, apart);
 }
 
 size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {

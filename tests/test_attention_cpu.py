@@ -450,3 +450,11 @@ def test_append_refuses_caches_that_share_channels(L, kw):
         assert (code == _lib.CARVE_EINVAL) == meet and code in (_lib.CARVE_OK, _lib.CARVE_EINVAL), apart
         got, want = got + (code != _lib.CARVE_OK), want + meet
     assert got == want > 0
+
+
+def test_append_refuses_caches_that_start_alike(L):
+    """Whatever their strides, two caches whose first entries meet."""
+    c = paged_cfg(N=0, vc_page=4096, vc_tok=192, vc_head=64)
+    for apart, code in ((0, _lib.CARVE_EINVAL), (112, _lib.CARVE_EINVAL), (-112, _lib.CARVE_EINVAL),
+                        (MB, _lib.CARVE_OK)):
+        assert append(L, c, k_cache=FAKE + 64 * MB, v_cache=FAKE + 64 * MB + apart) == code, apart
