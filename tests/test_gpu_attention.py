@@ -1035,3 +1035,39 @@ def test_few_rows_keep_sixteen_bits_of_the_weights(torch, d, G, n, kv, page, win
     one = f64(torch.tensor(w / w.max(), dtype=torch.float32).bfloat16())
     rough = one @ s0[1][seen, 0] / (w / w.max()).sum()
     assert np.any(np.abs(rough - o[-1, 0]) > HALF["bf16"] * np.abs(o[-1, 0]) + slack[-1, 0] * A[-1, 0])
+
+
+@pytest.mark.parametrize("dtype,n,Hq,Hk,d,window", [("bf16", 100, 8, 2, 64, 0), ("bf16", 100, 8, 2, 128, 900),
+                                                    ("bf16", 90, 130, 130, 128, 0), ("f32", 20, 4, 2, 64, 0)])
+def test_captured_chunk_follows_the_lengths(torch, dtype, n, Hq, Hk, d, window):
+    """A prompt chunk's append and attention, and the gradient of its rotation, captured once and replayed over longer
+    and shorter contexts (in one piece, split, cut by the table), with eager work between the replays."""
+    from chunk_gated_delta_carve_amd import paged_append, paged_attention, qk_norm_rope_bwd, rope_tables
+    page, width = 16, 256
+    kc, vc = cache(torch, "joint", width, page, Hk, d, dtype, 340)
+    tab = torch.randperm(width, generator=torch.Generator().manual_seed(341)).to(torch.int32).cuda()[None]
+    lens, cu = ints(torch, [n]), ints(torch, [0, n])
+    cos, sin = rope_tables(width * page, d)
+    q, k, v, dq, dk = (rand(torch, 342 + i, (n, h, d), dtype) for i, h in enumerate((Hq, Hk, Hk, Hq, Hk)))
+    w = rand(torch, 347, (d,), dtype, 0.1, 1.0)
+
+    def work():
+        qr = paged_append(k, v, kc, vc, tab, lens, cu, cos, sin, q=q, q_weight=w, k_weight=w, norm=True)
+        out, lse = paged_attention(qr, kc, vc, tab, lens, cu, window=window, return_lse=True)
+        return [qr, out, lse, *qk_norm_rope_bwd(q, k, dq, dk, cos, sin, q_weight=w, k_weight=w).values()]
+
+    work()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = work()
+    for turn, kv in enumerate((n, 4000, n // 2, 700, width * page)):
+        lens.fill_(kv)
+        q.copy_(rand(torch, 350 + turn, (n, Hq, d), dtype))
+        g.replay()
+        got = [t.clone() for t in held]
+        want = work()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)), (turn, kv, i)
+        assert torch.isfinite(got[1]).all()
