@@ -17,7 +17,8 @@ CARVE_ROPE_INTERLEAVED, CARVE_ROPE_NORM, CARVE_PAGED_STEP = 1, 2, 4
 EXPORTED = ("carve_recurrent_ref_shapes", "carve_chunk_fwd", "carve_chunk_fwd_noalloc", "carve_chunk_bwd",
             "carve_recurrent_step", "carve_qk_norm_rope_fwd", "carve_qk_norm_rope_workspace",
             "carve_qk_norm_rope_bwd", "carve_paged_append", "carve_paged_workspace", "carve_paged_attention",
-            "carve_error_string")
+            "carve_paged_append_fp4", "carve_paged_read_fp4", "carve_paged_workspace_fp4", "carve_paged_attention_fp4",
+            "carve_paged_assign", "carve_error_string")
 
 
 class CarveConfig(ctypes.Structure):
@@ -44,6 +45,16 @@ class CarvePagedConfig(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in
                    ("q_row", "k_row", "v_row", "o_row", "table_row", "kc_page", "kc_tok", "kc_head", "vc_page",
                     "vc_tok", "vc_head")])
+
+
+class CarveFp4Config(ctypes.Structure):
+    _fields_ = ([("paged", CarvePagedConfig)]
+                + [(n, ctypes.c_int64) for n in ("ks_page", "ks_tok", "ks_head", "vs_page", "vs_tok", "vs_head")])
+
+
+class CarveAssignConfig(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("S", "N", "page_size", "width")]
+                + [(n, ctypes.c_int64) for n in ("table_row", "capacity")])
 
 
 class CarveError(RuntimeError):
@@ -83,6 +94,12 @@ def lib() -> ctypes.CDLL:
         L.carve_paged_append.argtypes = [paged] + [vp] * 14
         L.carve_paged_workspace.argtypes = [paged, bytes_out]
         L.carve_paged_attention.argtypes = [paged] + [vp] * 9 + [size, vp]
+        fp4 = ctypes.POINTER(CarveFp4Config)
+        L.carve_paged_append_fp4.argtypes = [fp4] + [vp] * 16
+        L.carve_paged_read_fp4.argtypes = [fp4] + [vp] * 8
+        L.carve_paged_workspace_fp4.argtypes = [fp4, bytes_out]
+        L.carve_paged_attention_fp4.argtypes = [fp4] + [vp] * 11 + [size, vp]
+        L.carve_paged_assign.argtypes = [ctypes.POINTER(CarveAssignConfig)] + [vp] * 12
         for name in EXPORTED[5:-1]:
             getattr(L, name).restype = ctypes.c_int
         L.carve_error_string.argtypes = [ctypes.c_int]

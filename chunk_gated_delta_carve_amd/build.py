@@ -8,7 +8,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libcarve.so")
-SOURCES = [os.path.join(PKG, "csrc", n) for n in ("carve_lib.hip", "attn_lib.hip")]
+SOURCES = [os.path.join(PKG, "csrc", n) for n in ("carve_lib.hip", "attn_lib.hip", "fp4_lib.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

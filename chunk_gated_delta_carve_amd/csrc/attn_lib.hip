@@ -1,49 +1,18 @@
 // Host side of the attention layer's entry points: validation, plan, dispatch.
 // Every check runs before the first HIP call.
-#include <algorithm>
-#include <cfloat>
-
-#include "host.h"
+#include "attn_host.h"
 #include "kernels/paged_attn.h"
-#include "kernels/rope.h"
 
 namespace {
 
 using namespace carve_host;
 
-constexpr int64_t kMaxInt = 0x7fffffffLL;
-constexpr int64_t kMaxThreads = 0xffffffffLL;                // of a launch, in x
-constexpr int64_t kMaxTokens = kMaxThreads / 256 * 4;        // a wave each, in workgroups of 256
-
-bool off16(int64_t stride, int dtype) { return (stride * (int64_t)elem_bytes(dtype)) & 15; }
-
-// Rows of `len` elements, `row` apart.
-struct Rows {
-  const void* p;
-  int64_t n, row, len;
-  size_t es;
-  size_t span() const { return p && n > 0 ? (size_t)((n - 1) * row + len) * es : 0; }
-};
-
-bool same(const Rows& a, const Rows& b) {
-  return a.p == b.p && a.n == b.n && a.len == b.len && (a.row == b.row || a.n == 1);
+Entries k_entries(const carve_paged_config* c) {
+  return {c->kc_page, c->kc_tok, c->kc_head, c->d, (int64_t)elem_bytes(c->dtype)};
 }
-
-// Whether two sets of rows share an element. Rows of one stride may interleave
-// (the parts of one projection's output).
-bool overlaps(const Rows& a, const Rows& b) {
-  if (!carve_host::overlaps(a.p, a.span(), b.p, b.span())) return false;
-  if (a.row != b.row || a.es != b.es || a.row <= 0) return true;
-  const int64_t R = a.row * (int64_t)a.es, la = a.len * (int64_t)a.es, lb = b.len * (int64_t)b.es;
-  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % R;
-  if (d < 0) d += R;
-  return d < la || d + lb > R;
+Entries v_entries(const carve_paged_config* c) {
+  return {c->vc_page, c->vc_tok, c->vc_head, c->d, (int64_t)elem_bytes(c->dtype)};
 }
-
-// eps carries a row of zeros through the inverse root, which takes denormals as 0.
-bool bad_eps(float eps) { return !(eps >= FLT_MIN); }
-
-bool bad_rot(int rot, int d) { return rot < 0 || rot > d || rot % 16; }
 
 int check_rope(const carve_rope_config* c) {
   if (!c) return CARVE_EINVAL;
@@ -60,13 +29,6 @@ int check_rope(const carve_rope_config* c) {
   return CARVE_OK;
 }
 
-bool bad_rows(int64_t n, int64_t row, int64_t len, int dtype, bool written) {
-  return row < 0 || (written && n > 1 && row < len) || off16(row, dtype);
-}
-
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-constexpr int64_t kFewWaves = 4096;   // four waves per SIMD
 constexpr int64_t kManyRows = 16384;   // rows to join: eight to a wave are two waves per SIMD
 constexpr int kWideJoin = 32;          // shares per item from which a workgroup joins a row, not a wave
 
@@ -113,118 +75,18 @@ int check_rope_inputs(const carve_rope_config* c, const void* q, const void* k, 
   return CARVE_OK;
 }
 
-template <typename F>
-hipError_t by_type(int dtype, int d, F&& f) {
-  if (dtype == CARVE_BF16)
-    return d == 64 ? f(carve::bf16{}, std::integral_constant<int, 64>{})
-                   : f(carve::bf16{}, std::integral_constant<int, 128>{});
-  return d == 64 ? f(float{}, std::integral_constant<int, 64>{}) : f(float{}, std::integral_constant<int, 128>{});
-}
-
-// Pieces per lane of the kernels that take a token's rows by waves. Few waves: one
-// piece each, for the shortest chain (64 tokens of 18 heads of 128: 3.6 us against 5.3). Many:
-// up to four, which shares the token's angles and keeps four loads in flight, in
-// the fewest waves per token.
-struct TokenWaves { int per_lane; unsigned per_token; };
-TokenWaves token_waves(int64_t tokens, int64_t heads, int d, int dtype) {
-  const int64_t passes = up(heads * (d * (int64_t)elem_bytes(dtype) / 16), 64);
-  if (passes * tokens <= kFewWaves) return {1, (unsigned)passes};
-  const int64_t waves = up(passes, carve::kRopePieces);
-  return {(int)up(passes, waves), (unsigned)waves};
-}
-template <typename F>
-hipError_t by_pieces(int n, F&& f) {
-  switch (n) {
-    case 1: return f(std::integral_constant<int, 1>{});
-    case 2: return f(std::integral_constant<int, 2>{});
-    case 3: return f(std::integral_constant<int, 3>{});
-    default: return f(std::integral_constant<int, 4>{});
-  }
-}
-
 int check_paged(const carve_paged_config* c) {
-  if (!c) return CARVE_EINVAL;
-  if (c->N < 0 || c->S < 0 || c->Hq < 0 || c->Hk < 0 || c->page_size < 1 || c->pages < 0 || c->width < 0 ||
-      c->rot < 0 || c->table_len < 0 || c->window < 0)
-    return CARVE_EINVAL;
-  if (c->dtype != CARVE_F32 && c->dtype != CARVE_BF16) return CARVE_EINVAL;
-  if (c->flags & ~(CARVE_ROPE_INTERLEAVED | CARVE_ROPE_NORM | CARVE_PAGED_STEP)) return CARVE_EINVAL;
-  if ((c->flags & CARVE_PAGED_STEP) && c->N != c->S) return CARVE_EINVAL;
-  if (c->d != 64 && c->d != 128) return CARVE_EUNSUPPORTED;
-  if (c->page_size & (c->page_size - 1)) return CARVE_EUNSUPPORTED;
-  if ((int64_t)c->width * c->page_size > (1 << 30)) return CARVE_EUNSUPPORTED;
-  const int64_t heads = (int64_t)c->Hq + 2 * (int64_t)c->Hk;
-  if (heads * c->d > kMaxInt || (int64_t)c->N * heads > kMaxInt) return CARVE_EUNSUPPORTED;
-  for (int64_t r : {c->q_row, c->k_row, c->v_row, c->o_row, c->table_row})
-    if (r > kMaxInt) return CARVE_EUNSUPPORTED;
-  if (c->q_row < 0 || c->k_row < 0 || c->v_row < 0 || c->o_row < 0 || c->table_row < 0 ||
-      (c->S > 1 && c->table_row < c->width))
-    return CARVE_EINVAL;
+  const int st = check_sequences(c);
+  if (st != CARVE_OK) return st;
   // distinct cache entries lie apart
-  const int64_t st[2][3] = {{c->kc_page, c->kc_tok, c->kc_head}, {c->vc_page, c->vc_tok, c->vc_head}};
-  for (const auto& s : st) {
-    if (s[0] < 0 || s[1] < 0 || s[2] < 0) return CARVE_EINVAL;
-    for (int64_t n : s)
-      if (n > kMaxInt) return CARVE_EUNSUPPORTED;   // a stride's bytes are counted in 32 bits (bf16)
-    if ((c->pages > 1 && s[0] < c->d) || (c->page_size > 1 && s[1] < c->d) || (c->Hk > 1 && s[2] < c->d))
-      return CARVE_EINVAL;
+  for (const Entries& e : {k_entries(c), v_entries(c)}) {
+    const int bad = check_strides(c, e);
+    if (bad != CARVE_OK) return bad;
   }
   for (int64_t s : {c->kc_page, c->kc_tok, c->kc_head, c->vc_page, c->vc_tok, c->vc_head, c->q_row, c->k_row,
                     c->v_row, c->o_row})
     if (off16(s, c->dtype)) return CARVE_EALIGN;
   return CARVE_OK;
-}
-
-int shift_of(int page_size) {
-  int s = 0;
-  while ((1 << s) < page_size) ++s;
-  return s;
-}
-
-// Whether two entries of a cache may share channels: ordered by stride, every
-// dimension has to step past all that the ones before it reach.
-bool entries_overlap(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {
-  struct Dim { int64_t n, stride; } dims[3] = {{c->pages, page}, {c->page_size, tok}, {c->Hk, head}};
-  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
-  int64_t reach = c->d;
-  for (const Dim& x : dims) {
-    if (x.n < 2) continue;
-    if (x.stride < reach) return true;
-    reach += (x.n - 1) * x.stride;
-  }
-  return false;
-}
-
-// Whether an entry of k_cache and one of v_cache share channels, where both have the
-// same strides (each past what the smaller ones reach, as entries_overlap saw to):
-// the distance of the two starts is then looked for among the distances of entries,
-// from the largest stride down. Caches that interleave with different strides are
-// the caller's to keep apart.
-bool caches_overlap(const carve_paged_config* c, const void* k_cache, const void* v_cache) {
-  struct Dim { int64_t n, k, v; } dims[3] = {{c->pages, c->kc_page, c->vc_page}, {c->page_size, c->kc_tok, c->vc_tok},
-                                             {c->Hk, c->kc_head, c->vc_head}};
-  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache)) /
-                        (int64_t)elem_bytes(c->dtype);
-  auto same_place = [&](int64_t n) { return n < c->d && n > -(int64_t)c->d; };
-  for (const Dim& x : dims)
-    if (x.n < 1) return false;
-  if (same_place(apart)) return true;               // the first entries
-  for (const Dim& x : dims)
-    if (x.n > 1 && x.k != x.v) return false;
-  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return (x.n > 1 ? x.k : 0) > (y.n > 1 ? y.k : 0); });
-  auto meets = [&](auto&& self, int i, int64_t left) -> bool {
-    if (i == 3 || dims[i].n < 2) return same_place(left);
-    const int64_t s = dims[i].k, q = left / s;
-    for (int64_t m = q - 1; m <= q + 1; ++m)
-      if (m < dims[i].n && m > -dims[i].n && self(self, i + 1, left - m * s)) return true;
-    return false;
-  };
-  return meets(meets, 0, apart);
-}
-
-size_t cache_span(const carve_paged_config* c, int64_t page, int64_t tok, int64_t head) {
-  if (c->pages == 0 || c->Hk == 0) return 0;
-  return (size_t)((c->pages - 1) * page + (c->page_size - 1) * tok + (c->Hk - 1) * head + c->d) * elem_bytes(c->dtype);
 }
 
 // Kernel and split of an attention call, from sizes alone. The row kernel takes
@@ -479,8 +341,7 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   if (bad_rot(c.rot, c.d)) return CARVE_EUNSUPPORTED;
   if (norm && bad_eps(c.eps)) return CARVE_EINVAL;
   if (c.N > kMaxTokens) return CARVE_EUNSUPPORTED;
-  if (entries_overlap(cfg, c.kc_page, c.kc_tok, c.kc_head) || entries_overlap(cfg, c.vc_page, c.vc_tok, c.vc_head))
-    return CARVE_EINVAL;
+  if (entries_overlap(cfg, k_entries(cfg)) || entries_overlap(cfg, v_entries(cfg))) return CARVE_EINVAL;
   if (!norm && (q_weight || k_weight)) return CARVE_EINVAL;
   const bool work = c.N > 0 && c.S > 0 && c.Hq + c.Hk > 0;
   if (work) {
@@ -499,7 +360,7 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   const size_t es = elem_bytes(c.dtype);
   const Rows rq{q, c.N, c.q_row, lq, es}, rk{k, c.N, c.k_row, lk, es}, rv{v, c.N, c.v_row, lk, es},
       ro{q_out, c.N, c.o_row, lq, es};
-  const size_t ks = cache_span(cfg, c.kc_page, c.kc_tok, c.kc_head), vs = cache_span(cfg, c.vc_page, c.vc_tok, c.vc_head);
+  const size_t ks = cache_span(cfg, k_entries(cfg)), vs = cache_span(cfg, v_entries(cfg));
   const Rows side[] = {{q_weight, 1, 0, c.d, es}, {k_weight, 1, 0, c.d, es},
                        {cos, 1, 0, (int64_t)c.table_len * (c.rot / 2), 4},
                        {sin, 1, 0, (int64_t)c.table_len * (c.rot / 2), 4},
@@ -512,7 +373,7 @@ extern "C" int carve_paged_append(const carve_paged_config* cfg, const void* k, 
   for (const Rows& r : {rq, rk, rv, ro, side[0], side[1], side[2], side[3], side[4], side[5], side[6]})
     if (carve_host::overlaps(k_cache, ks, r.p, r.span()) || carve_host::overlaps(v_cache, vs, r.p, r.span()))
       return CARVE_EINVAL;
-  if (k_cache && v_cache && caches_overlap(cfg, k_cache, v_cache)) return CARVE_EINVAL;
+  if (k_cache && v_cache && entries_meet(cfg, k_cache, k_entries(cfg), v_cache, v_entries(cfg))) return CARVE_EINVAL;
   if (!work) return CARVE_OK;
   carve::AppendArgs a{};
   a.k = k; a.v = v; a.q = q; a.wq = q_weight; a.wk = k_weight;
@@ -589,8 +450,8 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
                      {cu, 1, 0, step ? 0 : (int64_t)c.S + 1, 4},
                      {kv_lens, 1, 0, c.S, 4},
                      {table, c.S, c.table_row, c.width, 4},
-                     {k_cache, 1, 0, (int64_t)cache_span(cfg, c.kc_page, c.kc_tok, c.kc_head), 1},
-                     {v_cache, 1, 0, (int64_t)cache_span(cfg, c.vc_page, c.vc_tok, c.vc_head), 1}};
+                     {k_cache, 1, 0, (int64_t)cache_span(cfg, k_entries(cfg)), 1},
+                     {v_cache, 1, 0, (int64_t)cache_span(cfg, v_entries(cfg)), 1}};
   const Rows out[] = {{o, c.N, c.o_row, lq, es}, {lse, 1, 0, (int64_t)c.N * c.Hq, 4},
                       {plan.bytes ? workspace : nullptr, 1, 0, plan.bytes, 1}};
   for (int i = 0; i < 3; ++i) {

@@ -1,0 +1,311 @@
+// Host side of the 4-bit paged cache's entry points and of the room in a paged
+// cache: validation, plan, dispatch. Every check runs before the first HIP call.
+#include "attn_host.h"
+#include "kernels/assign.h"
+#include "kernels/fp4.h"
+#include "kernels/paged_fp4.h"
+
+namespace {
+
+using namespace carve_host;
+
+// The four parts of the cache: codes and scales of keys and of values.
+struct Parts { Entries kc, ks, vc, vs; };
+Parts parts_of(const carve_fp4_config* f) {
+  const carve_paged_config& c = f->paged;
+  return {{c.kc_page, c.kc_tok, c.kc_head, c.d / 2, 1},
+          {f->ks_page, f->ks_tok, f->ks_head, c.d / carve::kFp4Block, 1},
+          {c.vc_page, c.vc_tok, c.vc_head, c.d / 2, 1},
+          {f->vs_page, f->vs_tok, f->vs_head, c.d / carve::kFp4Block, 1}};
+}
+
+int check_fp4(const carve_fp4_config* f) {
+  const int st = check_sequences(f ? &f->paged : nullptr);
+  if (st != CARVE_OK) return st;
+  const carve_paged_config& c = f->paged;
+  const Parts p = parts_of(f);
+  for (const Entries& e : {p.kc, p.ks, p.vc, p.vs}) {
+    const int bad = check_strides(&c, e);
+    if (bad != CARVE_OK) return bad;
+  }
+  for (const Entries& e : {p.kc, p.vc})
+    if ((e.page | e.tok | e.head) & 15) return CARVE_EALIGN;
+  for (const Entries& e : {p.ks, p.vs})
+    if ((e.page | e.tok | e.head) & (e.len - 1)) return CARVE_EALIGN;
+  for (int64_t r : {c.q_row, c.k_row, c.v_row, c.o_row})
+    if (off16(r, c.dtype)) return CARVE_EALIGN;
+  return CARVE_OK;
+}
+
+carve::Fp4Strides strides(const Entries& e) { return {e.page, e.tok, e.head}; }
+
+}  // namespace
+
+extern "C" int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k, const void* v, const void* q,
+                                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                                      const int32_t* cu, const int32_t* kv_lens, const int32_t* table,
+                                      uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales,
+                                      void* q_out, void* stream) {
+  const int st = check_fp4(cfg);
+  if (st != CARVE_OK) return st;
+  const carve_paged_config& c = cfg->paged;
+  const bool step = (c.flags & CARVE_PAGED_STEP) != 0, norm = (c.flags & CARVE_ROPE_NORM) != 0;
+  if (bad_rot(c.rot, c.d)) return CARVE_EUNSUPPORTED;
+  if (norm && bad_eps(c.eps)) return CARVE_EINVAL;
+  if (c.N > kMaxTokens) return CARVE_EUNSUPPORTED;
+  const Parts parts = parts_of(cfg);
+  const Entries kinds[4] = {parts.kc, parts.ks, parts.vc, parts.vs};
+  for (const Entries& e : kinds)
+    if (entries_overlap(&c, e)) return CARVE_EINVAL;
+  if (!norm && (q_weight || k_weight)) return CARVE_EINVAL;
+  const void* const caches[4] = {k_codes, k_scales, v_codes, v_scales};
+  const bool work = c.N > 0 && c.S > 0 && c.Hq + c.Hk > 0;
+  if (work) {
+    if (c.Hk > 0 && (!k || !v)) return CARVE_EINVAL;
+    if (c.Hk > 0 && c.pages > 0)
+      for (const void* p : caches)
+        if (!p) return CARVE_EINVAL;
+    if (c.Hq > 0 && (!q || !q_out)) return CARVE_EINVAL;
+    if (!kv_lens || (c.width > 0 && !table) || (!step && !cu)) return CARVE_EINVAL;
+    if (c.rot > 0 && (!cos || !sin)) return CARVE_EINVAL;
+  }
+  for (const void* p : {k, v, q, q_weight, k_weight, (const void*)cos, (const void*)sin, (const void*)k_codes,
+                        (const void*)v_codes, (const void*)q_out})
+    if (misaligned(p)) return CARVE_EALIGN;
+  for (const void* p : {(const void*)cu, (const void*)kv_lens, (const void*)table, (const void*)k_scales,
+                        (const void*)v_scales})
+    if (misaligned4(p)) return CARVE_EALIGN;
+  const int64_t lq = (int64_t)c.Hq * c.d, lk = (int64_t)c.Hk * c.d;
+  if (bad_rows(c.N, c.o_row, lq, c.dtype, true)) return CARVE_EINVAL;
+  const size_t es = elem_bytes(c.dtype);
+  const Rows rq{q, c.N, c.q_row, lq, es}, ro{q_out, c.N, c.o_row, lq, es};
+  const Rows in[] = {{k, c.N, c.k_row, lk, es}, {v, c.N, c.v_row, lk, es},
+                     {q_weight, 1, 0, c.d, es}, {k_weight, 1, 0, c.d, es},
+                     {cos, 1, 0, (int64_t)c.table_len * (c.rot / 2), 4},
+                     {sin, 1, 0, (int64_t)c.table_len * (c.rot / 2), 4},
+                     {cu, 1, 0, step ? 0 : (int64_t)c.S + 1, 4}, {kv_lens, 1, 0, c.S, 4},
+                     {table, c.S, c.table_row, c.width, 4}};
+  if (!same(ro, rq) && overlaps(ro, rq)) return CARVE_EINVAL;
+  for (const Rows& r : in)
+    if (overlaps(ro, r)) return CARVE_EINVAL;
+  // the cache's parts may interleave in one tensor; nothing else lies in them
+  for (int i = 0; i < 4; ++i) {
+    const size_t span = cache_span(&c, kinds[i]);
+    for (const Rows& r : in)
+      if (carve_host::overlaps(caches[i], span, r.p, r.span())) return CARVE_EINVAL;
+    for (const Rows& r : {rq, ro})
+      if (carve_host::overlaps(caches[i], span, r.p, r.span())) return CARVE_EINVAL;
+    for (int j = i + 1; j < 4; ++j)
+      if (caches[i] && caches[j] && entries_meet(&c, caches[i], kinds[i], caches[j], kinds[j])) return CARVE_EINVAL;
+  }
+  if (!work) return CARVE_OK;
+  carve::Fp4AppendArgs f{};
+  carve::AppendArgs& a = f.a;
+  a.k = k; a.v = v; a.q = q; a.wq = q_weight; a.wk = k_weight;
+  a.cos = cos; a.sin = sin;
+  a.cu = step ? nullptr : cu; a.kv_lens = kv_lens; a.table = table;
+  a.kc = k_codes; a.vc = v_codes; a.qo = q_out;
+  a.k_row = c.k_row; a.v_row = c.v_row; a.q_row = c.q_row; a.qo_row = c.o_row; a.table_row = c.table_row;
+  a.kc_page = c.kc_page; a.kc_tok = c.kc_tok; a.kc_head = c.kc_head;
+  a.vc_page = c.vc_page; a.vc_tok = c.vc_tok; a.vc_head = c.vc_head;
+  a.N = c.N; a.S = c.S; a.Hq = c.Hq; a.Hk = c.Hk; a.rot = c.rot; a.table_len = c.table_len;
+  a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
+  a.interleaved = (c.flags & CARVE_ROPE_INTERLEAVED) != 0;
+  a.norm = norm;
+  a.eps = c.eps;
+  f.ks = k_scales; f.vs = v_scales;
+  f.k = strides(parts.ks); f.v = strides(parts.vs);
+  const TokenWaves w = token_waves(c.N, (int64_t)c.Hq + 2 * (int64_t)c.Hk, c.d, c.dtype);
+  if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
+  const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
+    return by_pieces(w.per_lane, [&](auto u) {
+      hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
+                         dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                         f);
+      return hipGetLastError();
+    });
+  });
+  return e == hipSuccess ? CARVE_OK : hip_failed(e);
+}
+
+extern "C" int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* k_codes, const uint8_t* k_scales,
+                                    const uint8_t* v_codes, const uint8_t* v_scales, const int64_t* slots, void* k,
+                                    void* v, void* stream) {
+  const int st = check_fp4(cfg);
+  if (st != CARVE_OK) return st;
+  const carve_paged_config& c = cfg->paged;
+  if (c.N > kMaxTokens) return CARVE_EUNSUPPORTED;
+  const int64_t heads = (int64_t)c.Hk * ((k != nullptr) + (v != nullptr));
+  const bool work = c.N > 0 && heads > 0;
+  if (work && !slots) return CARVE_EINVAL;
+  if (work && c.pages > 0 && ((k && (!k_codes || !k_scales)) || (v && (!v_codes || !v_scales)))) return CARVE_EINVAL;
+  for (const void* p : {(const void*)k_codes, (const void*)v_codes, (const void*)k, (const void*)v})
+    if (misaligned(p)) return CARVE_EALIGN;
+  if (misaligned4(k_scales) || misaligned4(v_scales) || (reinterpret_cast<uintptr_t>(slots) & 7u)) return CARVE_EALIGN;
+  const int64_t lk = (int64_t)c.Hk * c.d;
+  if ((k && bad_rows(c.N, c.k_row, lk, c.dtype, true)) || (v && bad_rows(c.N, c.v_row, lk, c.dtype, true)))
+    return CARVE_EINVAL;
+  const Parts parts = parts_of(cfg);
+  const size_t es = elem_bytes(c.dtype);
+  const Rows out[2] = {{k, c.N, c.k_row, lk, es}, {v, c.N, c.v_row, lk, es}};
+  const Rows in[5] = {{slots, 1, 0, c.N, 8},
+                      {k_codes, 1, 0, (int64_t)cache_span(&c, parts.kc), 1},
+                      {k_scales, 1, 0, (int64_t)cache_span(&c, parts.ks), 1},
+                      {v_codes, 1, 0, (int64_t)cache_span(&c, parts.vc), 1},
+                      {v_scales, 1, 0, (int64_t)cache_span(&c, parts.vs), 1}};
+  for (const Rows& o : out)
+    for (const Rows& r : in)
+      if (overlaps(o, r)) return CARVE_EINVAL;
+  if (overlaps(out[0], out[1])) return CARVE_EINVAL;
+  if (!work) return CARVE_OK;
+  carve::Fp4ReadArgs a{};
+  a.kc = k_codes; a.ks = k_scales; a.vc = v_codes; a.vs = v_scales;
+  a.slots = slots; a.k = k; a.v = v;
+  a.kcs = strides(parts.kc); a.kss = strides(parts.ks); a.vcs = strides(parts.vc); a.vss = strides(parts.vs);
+  a.k_row = c.k_row; a.v_row = c.v_row;
+  a.entries = (int64_t)c.pages * c.page_size;
+  a.N = c.N; a.Hk = c.Hk; a.heads = (int)heads; a.page_shift = shift_of(c.page_size);
+  const TokenWaves w = token_waves(c.N, heads, c.d, c.dtype);
+  if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
+  const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
+    return by_pieces(w.per_lane, [&](auto u) {
+      hipLaunchKernelGGL((carve::paged_read_fp4_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
+                         dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                         a);
+      return hipGetLastError();
+    });
+  });
+  return e == hipSuccess ? CARVE_OK : hip_failed(e);
+}
+
+namespace {
+int check_attention(const carve_fp4_config* f) {
+  const int st = check_fp4(f);
+  if (st != CARVE_OK) return st;
+  const carve_paged_config& c = f->paged;
+  if (!(c.scale > 0.f)) return CARVE_EINVAL;
+  if (!(c.scale <= 16.f)) return CARVE_EUNSUPPORTED;
+  if (c.Hq > 0 && (c.Hk == 0 || c.Hq % c.Hk)) return CARVE_EINVAL;
+  if (c.Hq > 65535 * 4) return CARVE_EUNSUPPORTED;
+  return CARVE_OK;
+}
+}  // namespace
+
+extern "C" int carve_paged_workspace_fp4(const carve_fp4_config* cfg, int64_t* bytes) {
+  const int st = check_attention(cfg);
+  if (st != CARVE_OK) return st;
+  if (!bytes) return CARVE_EINVAL;
+  *bytes = 0;
+  return CARVE_OK;
+}
+
+extern "C" int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void* q, const uint8_t* k_codes,
+                                         const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                                         const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* o,
+                                         float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_attention(cfg);
+  if (st != CARVE_OK) return st;
+  const carve_paged_config& c = cfg->paged;
+  const bool step = (c.flags & CARVE_PAGED_STEP) != 0;
+  const bool work = c.N > 0 && c.S > 0 && c.Hq > 0;
+  if (work) {
+    if (!q || !o || !kv_lens || (!step && !cu) || (c.width > 0 && !table)) return CARVE_EINVAL;
+    // keys that do not exist are loaded from page 0 and dropped
+    if (c.pages < 1 || !k_codes || !k_scales || !v_codes || !v_scales) return CARVE_EINVAL;
+  }
+  for (const void* p : {q, (const void*)k_codes, (const void*)v_codes, (const void*)o, (const void*)workspace})
+    if (misaligned(p)) return CARVE_EALIGN;
+  for (const void* p : {(const void*)cu, (const void*)kv_lens, (const void*)table, (const void*)lse,
+                        (const void*)k_scales, (const void*)v_scales})
+    if (misaligned4(p)) return CARVE_EALIGN;
+  const int64_t lq = (int64_t)c.Hq * c.d;
+  if (bad_rows(c.N, c.o_row, lq, c.dtype, true)) return CARVE_EINVAL;
+  const int64_t need = 0;
+  if (workspace_bytes < (size_t)need) return CARVE_EWORKSPACE;
+  if (need > 0 && !workspace) return CARVE_EINVAL;
+  const Parts parts = parts_of(cfg);
+  const size_t es = elem_bytes(c.dtype);
+  const Rows in[] = {{q, c.N, c.q_row, lq, es},
+                     {cu, 1, 0, step ? 0 : (int64_t)c.S + 1, 4},
+                     {kv_lens, 1, 0, c.S, 4},
+                     {table, c.S, c.table_row, c.width, 4},
+                     {k_codes, 1, 0, (int64_t)cache_span(&c, parts.kc), 1},
+                     {k_scales, 1, 0, (int64_t)cache_span(&c, parts.ks), 1},
+                     {v_codes, 1, 0, (int64_t)cache_span(&c, parts.vc), 1},
+                     {v_scales, 1, 0, (int64_t)cache_span(&c, parts.vs), 1}};
+  const Rows out[] = {{o, c.N, c.o_row, lq, es}, {lse, 1, 0, (int64_t)c.N * c.Hq, 4},
+                      {need ? workspace : nullptr, 1, 0, need, 1}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& r : in)
+      if (overlaps(out[i], r)) return CARVE_EINVAL;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(out[i], out[j])) return CARVE_EINVAL;
+  }
+  if (!work) return CARVE_OK;
+  carve::Fp4Args a{};
+  a.q = q; a.kc = k_codes; a.vc = v_codes; a.ks = k_scales; a.vs = v_scales;
+  a.cu = step ? nullptr : cu; a.kv_lens = kv_lens; a.table = table;
+  a.o = o; a.lse = lse;
+  a.q_row = c.q_row; a.o_row = c.o_row; a.table_row = c.table_row;
+  a.kc_page = c.kc_page; a.kc_tok = c.kc_tok; a.kc_head = c.kc_head;
+  a.vc_page = c.vc_page; a.vc_tok = c.vc_tok; a.vc_head = c.vc_head;
+  a.k = strides(parts.ks); a.v = strides(parts.vs);
+  a.N = c.N; a.S = c.S; a.Hq = c.Hq; a.Hk = c.Hk; a.G = c.Hq / c.Hk;
+  a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
+  a.window = c.window;
+  a.scale = c.scale; a.c = c.scale * carve::kLog2e;
+  const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
+    hipLaunchKernelGGL((carve::paged_each_fp4_kernel<decltype(t), decltype(d)::value>),
+                       dim3((unsigned)c.N, (unsigned)up(c.Hq, 4)), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                       a);
+    return hipGetLastError();
+  });
+  return e == hipSuccess ? CARVE_OK : hip_failed(e);
+}
+
+extern "C" int carve_paged_assign(const carve_assign_config* cfg, const int32_t* kv_lens, const int32_t* new_lens,
+                                  const int32_t* done, int32_t* table, int32_t* free_pages, const int32_t* free_count,
+                                  int32_t* kv_lens_out, int32_t* cu, int32_t* positions, int64_t* slots,
+                                  int32_t* free_count_out, void* stream) {
+  if (!cfg) return CARVE_EINVAL;
+  const carve_assign_config& c = *cfg;
+  if (c.S < 0 || c.N < 0 || c.page_size < 1 || c.width < 0 || c.table_row < 0 || c.capacity < 0 ||
+      (c.S > 1 && c.table_row < c.width))
+    return CARVE_EINVAL;
+  if ((c.page_size & (c.page_size - 1)) || (int64_t)c.width * c.page_size > (1 << 30)) return CARVE_EUNSUPPORTED;
+  if (c.table_row > kMaxInt || c.capacity > kMaxInt) return CARVE_EUNSUPPORTED;
+  if (!free_count || !cu || !free_count_out) return CARVE_EINVAL;
+  if (c.S > 0 && (!kv_lens || !new_lens || !kv_lens_out || (c.width > 0 && !table))) return CARVE_EINVAL;
+  if (c.capacity > 0 && !free_pages) return CARVE_EINVAL;
+  for (const void* p : {(const void*)kv_lens, (const void*)new_lens, (const void*)done, (const void*)table,
+                        (const void*)free_pages, (const void*)free_count, (const void*)kv_lens_out, (const void*)cu,
+                        (const void*)positions, (const void*)free_count_out})
+    if (misaligned4(p)) return CARVE_EALIGN;
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return CARVE_EALIGN;
+  const Rows in[] = {{kv_lens, 1, 0, c.S, 4}, {new_lens, 1, 0, c.S, 4}, {done, 1, 0, c.S, 4}, {free_count, 1, 0, 2, 4}};
+  const Rows out[] = {{kv_lens_out, 1, 0, c.S, 4}, {free_count_out, 1, 0, 2, 4}, {table, c.S, c.table_row, c.width, 4},
+                      {free_pages, 1, 0, c.capacity, 4}, {cu, 1, 0, (int64_t)c.S + 1, 4}, {positions, 1, 0, c.N, 4},
+                      {slots, 1, 0, c.N, 8}};
+  for (int i = 0; i < 7; ++i) {
+    for (const Rows& r : in)
+      if (overlaps(out[i], r) && !((i == 0 && kv_lens_out == kv_lens && r.p == kv_lens) ||
+                                   (i == 1 && free_count_out == free_count && r.p == free_count)))
+        return CARVE_EINVAL;
+    for (int j = i + 1; j < 7; ++j)
+      if (overlaps(out[i], out[j])) return CARVE_EINVAL;
+  }
+  carve::AssignArgs a{};
+  a.kv_lens = kv_lens; a.new_lens = new_lens; a.done = done; a.free_count = free_count;
+  a.table = table; a.free_pages = free_pages; a.kv_out = kv_lens_out; a.cu = cu;
+  a.positions = positions; a.count_out = free_count_out; a.slots = slots;
+  a.table_row = c.table_row; a.capacity = c.capacity;
+  a.S = c.S; a.N = c.N; a.width = c.width; a.page_shift = shift_of(c.page_size);
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(carve::paged_assign_kernel, dim3(1), dim3(carve::kAssignThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && (c.N > carve::kAssignTokens || c.S > carve::kAssignThreads) && c.N > 0 && (positions || slots)) {
+    hipLaunchKernelGGL(carve::paged_assign_tokens_kernel, dim3((unsigned)up(c.N, 1024)), dim3(256), 0, s, a);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? CARVE_OK : hip_failed(e);
+}

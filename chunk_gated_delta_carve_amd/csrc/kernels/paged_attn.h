@@ -230,18 +230,45 @@ struct RowOut {
   }
 };
 
+// A key/value head of a cache of E's, an entry at a time.
+template <typename E, int D>
+struct PlainEntries {
+  static constexpr int PER = D / 64;
+  const PagedArgs& a;
+  const E *kc, *vc;
+  __device__ __forceinline__ PlainEntries(const PagedArgs& a_, int h)
+      : a(a_), kc(static_cast<const E*>(a_.kc) + h * a_.kc_head), vc(static_cast<const E*>(a_.vc) + h * a_.vc_head) {}
+  __device__ __forceinline__ float score(int id, int64_t off, const E* q) const {     // q . k
+    constexpr int V = Piece<E>::V;
+    const E* k = kc + id * a.kc_page + off * a.kc_tok;
+    float s = 0.f;
+    for (int i = 0; i < D; i += V) {
+      float kx[V], qx[V];
+      Piece<E>::open(*reinterpret_cast<const u32x4*>(k + i), kx);
+      Piece<E>::open(*reinterpret_cast<const u32x4*>(q + i), qx);
+#pragma unroll
+      for (int u = 0; u < V; ++u) s += kx[u] * qx[u];
+    }
+    return s;
+  }
+  __device__ __forceinline__ void add(int id, int64_t off, float w, float (&o)[PER]) const {   // o += w v, a lane's channels
+    const E* v = vc + id * a.vc_page + off * a.vc_tok + lane_id() * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] += w * to_f32(v[i]);
+  }
+};
+
 // One row over keys [k0, k1) by a whole wave, key by key and without products
 // that other rows share: lanes score 64 keys at once, then add their values.
-template <typename E, int D>
-__device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTile& x, int r, int k0, int k1) {
-  constexpr int V = Piece<E>::V, PER = D / 64;
+template <typename E, int D, typename C>
+__device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const C& cache, const AttnTile& x, int r, int k0,
+                                            int k1) {
+  constexpr int PER = D / 64;
   const PagedArgs& a = ro.a;
   const int h = ro.h;
   const int64_t at = ro.index(x, r);
   const int p = x.pos0 + (x.row0 + r) / a.G, lane = lane_id();
   const E* q = static_cast<const E*>(a.q) + at / a.Hq * a.q_row + at % a.Hq * D;
-  const E* kc = static_cast<const E*>(a.kc) + h * a.kc_head;
-  const E* vc = static_cast<const E*>(a.vc) + h * a.vc_head;
   const int first = first_seen(a, p, k0), end = p + 1 < k1 ? p + 1 : k1;
   float m = kLeast, l = 0.f, o[PER];
 #pragma unroll
@@ -251,17 +278,7 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
     int id = j < end ? page_of(a, x.s, j) : -1;
     const int64_t off = j & ((1 << a.page_shift) - 1);
     float s = -__builtin_inff();
-    if (id >= 0) {
-      const E* k = kc + id * a.kc_page + off * a.kc_tok;
-      s = 0.f;
-      for (int i = 0; i < D; i += V) {
-        float kx[V], qx[V];
-        Piece<E>::open(*reinterpret_cast<const u32x4*>(k + i), kx);
-        Piece<E>::open(*reinterpret_cast<const u32x4*>(q + i), qx);
-#pragma unroll
-        for (int u = 0; u < V; ++u) s += kx[u] * qx[u];
-      }
-    }
+    if (id >= 0) s = cache.score(id, off, q);
     if (__ballot(s != s)) {                         // a visible score is NaN: so is the row
       l = __builtin_nanf("");
 #pragma unroll
@@ -283,9 +300,7 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const AttnTi
       const int uid = __shfl(id, u);
       if (uid < 0) continue;
       const float w = __shfl(e, u);
-      const E* v = vc + uid * a.vc_page + ((j0 + u) & ((1 << a.page_shift) - 1)) * a.vc_tok + lane * PER;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] += w * to_f32(v[i]);
+      cache.add(uid, (j0 + u) & ((1 << a.page_shift) - 1), w, o);
     }
   }
   if (ro.whole) {
@@ -647,7 +662,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   }
   __syncthreads();
   for (int i = wave; i < x.rows; i += 4)
-    if (bad[i]) careful_row<E, D>(ro, x, i, k0, k1);
+    if (bad[i]) careful_row(ro, PlainEntries<E, D>(a, h), x, i, k0, k1);
   __syncthreads();                                  // the next item writes the same LDS
   }
 }
@@ -861,7 +876,7 @@ struct TileWork {
     while (again) {
       const int i = __ffsll((unsigned long long)again) - 1;
       again &= again - 1;
-      careful_row<E, D>(ro, x, wave * 32 + i, k0, k1);
+      careful_row(ro, PlainEntries<E, D>(a, h), x, wave * 32 + i, k0, k1);
     }
   }
 };

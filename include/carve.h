@@ -377,6 +377,94 @@ int carve_paged_attention(const carve_paged_config* cfg, const void* q, const vo
                           const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged cache in 4 bits. The attention layers hold the only state of a hybrid
+ * that grows with the context; held in 4 bits it takes 17/64 of the bf16 cache's
+ * bytes, and a decode step reads that much less. Sequences, lengths and block
+ * tables are those of the calls above.
+ *
+ * A head's d channels are d / 32 blocks of 32. A block is 32 codes of 4 bits (a sign,
+ * two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte
+ * with the even channel in the low half, and one byte e, its scale 2^(e - 127); 255
+ * makes every value of the block NaN. Such a value is exact in bf16.
+ *   codes   uint8 [pages, page_size, Hk, d / 2]
+ *   scales  uint8 [pages, page_size, Hk, d / 32]
+ * for keys and for values; a head's bytes are contiguous, page, token and head strides
+ * free. Reading is fastest where a head's tokens of a page follow each other. */
+
+/* carve_paged_config with kc_* and vc_* in bytes of the codes (multiples of 16, below
+ * 2^31), and the scales' strides in bytes (multiples of d / 32, below 2^31). `dtype` is
+ * that of q, k, v and o. Codes are 16-byte aligned, scales 4-byte aligned. */
+typedef struct {
+  carve_paged_config paged;
+  int64_t ks_page, ks_tok, ks_head;
+  int64_t vs_page, vs_tok, vs_head;
+} carve_fp4_config;
+
+/* carve_paged_append into such a cache. A block takes the smallest scale 2^e with
+ * max |x| <= 7 2^e, -125 <= e <= 125; a value becomes the nearest code, the even one of
+ * two, at most 6: it is off by at most 2^e (by more only where |x| > 7 2^125), and by at
+ * most 2^e / 4 where |x| <= 2^(e+1). A block with an infinity or NaN is stored as NaN (codes 0). The keys are normed and
+ * rotated on the way where that is asked for, rounded to `dtype` as by
+ * carve_qk_norm_rope_fwd, and that is what is stored in 4 bits. The same refusals hold;
+ * codes and scales of keys and values may share one allocation. */
+int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k, const void* v, const void* q,
+                           const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                           const int32_t* cu, const int32_t* kv_lens, const int32_t* table, uint8_t* k_codes,
+                           uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, void* q_out, void* stream);
+
+/* The values that cache entries stand for: row n of k and v [N,Hk,d] dtype (rows
+ * paged.k_row and paged.v_row apart) from entry slots[n] % page_size of page
+ * slots[n] / page_size. A slot outside [0, pages page_size) gives zeros. Either of k
+ * and v may be NULL with its codes and scales. Of paged N, Hk, d, page_size, pages,
+ * dtype, k_row, v_row and the caches' strides are looked at; N at most 2^26 - 4. */
+int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* k_codes, const uint8_t* k_scales,
+                         const uint8_t* v_codes, const uint8_t* v_scales, const int64_t* slots, void* k, void* v,
+                         void* stream);
+
+/* Bytes of workspace carve_paged_attention_fp4 needs for this configuration. */
+int carve_paged_workspace_fp4(const carve_fp4_config* cfg, int64_t* bytes);
+
+/* carve_paged_attention over such a cache: what that call says holds, its results those
+ * over the values that the codes stand for (the products take them as they are, bf16
+ * with fp32 sums, or fp32). */
+int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void* q, const uint8_t* k_codes,
+                              const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                              const int32_t* cu, const int32_t* kv_lens, const int32_t* table, void* o, float* lse,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Room in a paged cache, of either kind, for the next tokens of S requests: block table,
+ * lengths, offsets, positions and slots, all worked out on the device, so that a captured
+ * step goes on from the last one's results.
+ *   old_s = 0 where the request has ended (done[s] != 0), else kv_lens[s]
+ *   kv_lens_out[s] = old_s + new_lens[s];  cu[s + 1] = cu[s] + new_lens[s], cu[0] = 0
+ * Negative lengths count as 0, sums stop at 2^31 - 1.
+ *   free_pages [capacity]  a stack: entries [0, free_count[0]) are pages nobody holds
+ *   free_count [2]         pages free; pages that were lacking so far
+ * First the pages of ended requests (the table entries >= 0 of their kv_lens[s] tokens)
+ * go on top of the stack, in the order of requests and entries; what would pass its
+ * capacity is lost. Then every request takes from the top what it needs for its tokens
+ * beyond ceil(old_s / page_size) pages, in the same order, and its table entries are
+ * written (entries past the table's width are not, and take nothing). Where the stack is
+ * empty the entry is -1 and free_count_out[1] counts one more; such tokens have no slot
+ * and neither are they stored or seen. A page that several requests hold is the caller's
+ * to keep out of ended ones.
+ *   positions [N]  of token cu[s] + i: old_s + i; 0 behind cu[S]
+ *   slots [N]      page page_size + position mod page_size, or -1 without a page and
+ *                  behind cu[S]
+ * Either of the two may be NULL. kv_lens_out may be kv_lens and free_count_out
+ * free_count; no other output overlaps anything. */
+typedef struct {
+  int32_t S, N;
+  int32_t page_size, width;          /* page_size a power of two; width * page_size <= 2^30 */
+  int64_t table_row;                 /* entries from one request's table row to the next's */
+  int64_t capacity;                  /* of free_pages, below 2^31 */
+} carve_assign_config;
+int carve_paged_assign(const carve_assign_config* cfg, const int32_t* kv_lens, const int32_t* new_lens,
+                       const int32_t* done, int32_t* table, int32_t* free_pages, const int32_t* free_count,
+                       int32_t* kv_lens_out, int32_t* cu, int32_t* positions, int64_t* slots, int32_t* free_count_out,
+                       void* stream);
+
 /* Static text for a status code. For CARVE_EHIP it returns the HIP error text
  * of the most recent failure on the calling thread. */
 const char* carve_error_string(int code);
