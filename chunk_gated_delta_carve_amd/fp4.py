@@ -220,7 +220,7 @@ def paged_assign(block_table, kv_lens, new_lens, free_pages, free_count, page_si
     if block_table.dtype is not _I32:
         _like(block_table, "block_table", _I32, dev)
     row, step = block_table.stride()
-    if width > 1 and step != 1:
+    if S and width > 1 and step != 1:
         raise ValueError("block_table: a request's entries must be contiguous")
     if free_pages.dim() != 1:
         raise ValueError(f"free_pages: expected one dimension, got {tuple(free_pages.shape)}")
