@@ -53,22 +53,283 @@ struct Fp4Entries {
   }
 };
 
-// A wave per (token, query head), key by key.
+// Few rows, as paged_rows_kernel deals them: 16 rows at a time, four waves taking
+// alternate blocks of 32 keys. A lane has key c's channels [g D/4, (g + 1) D/4), one load
+// of 16 bytes (8 at d = 64) and one scale, opened to bf16 in registers: the keys as
+// operands, the values on their way through the wave's LDS. fp32 queries and weights
+// enter the products as three bf16 parts, which hold their 24 bits; the codes are exact.
 template <typename E, int D>
-__global__ __launch_bounds__(256) void paged_each_fp4_kernel(Fp4Args a) {
-  const int n = blockIdx.x, qh = blockIdx.y * 4 + wave_id();
-  if (qh >= a.Hq) return;
-  int s = n, n0 = n, cnt = 1;
-  if (a.cu) {
-    s = find_sequence(a.cu, a.S, n);
-    if (s >= a.S || n < a.cu[s]) return;
-    n0 = a.cu[s];
-    cnt = (a.cu[s + 1] < a.N ? a.cu[s + 1] : a.N) - n0;
+struct RowsFp4 {
+  static constexpr int BM = 16, KT = 32, BN = 4 * KT;                            // as RowsLayout
+  static constexpr int PER_CU = (D == 128 ? 3 : 4) - (sizeof(E) == 4);
+  static constexpr int NI = D / 32;                                              // products per block of 16 keys
+  static constexpr int NQ = sizeof(E) == 2 ? 1 : 3, NP = sizeof(E) == 2 ? 2 : 3; // parts of q and of the weights
+  static constexpr int VLD = 2 * D + 32, OLD = D + 4;
+  static constexpr int v_bytes = 4 * KT * VLD, o_bytes = 4 * BM * OLD * 4;
+  static constexpr int bytes = v_bytes > o_bytes ? v_bytes : o_bytes;
+};
+
+// Three parts of 8 bits, cut off one after the other: their sum is x.
+__device__ __forceinline__ void cut_parts(const float (&x)[8], u32x4 (&part)[3]) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned a = __float_as_uint(r[2 * i]) & 0xffff0000u, b = __float_as_uint(r[2 * i + 1]) & 0xffff0000u;
+      part[p][i] = a >> 16 | b;
+      r[2 * i] -= __uint_as_float(a);
+      r[2 * i + 1] -= __uint_as_float(b);
+    }
+}
+
+__device__ __forceinline__ f32x4 mma_bits(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_kernel(Fp4Args a) {
+  using LY = RowsFp4<E, D>;
+  constexpr int NI = LY::NI, KT = LY::KT, NQ = LY::NQ;
+  using Codes = __attribute__((ext_vector_type(NI))) unsigned;
+  __shared__ __align__(16) char lds[LY::bytes];
+  __shared__ float ms[4][16], ls[4][16];
+  __shared__ int bad[16];
+  const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
+  const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
+  int* cut = a.cuts + blockIdx.x * kCutInts;
+  if (threadIdx.x == 0 && a.shares > 1) cut[2] = 0;
+  if ((int)blockIdx.x >= plan.shares) return;
+  int at_block = plan.start(blockIdx.x);
+  const int end_block = plan.start(blockIdx.x + 1);
+  const int in = 63 - __clzll(__ballot(plan.before <= at_block));
+  int s = in * plan.run;
+  int seq_block = __builtin_amdgcn_readlane(plan.before, in);
+  RowsWork w = plan.work(a, s, LY::BM, LY::BN);
+  while (at_block < end_block) {
+  while (at_block >= seq_block + w.blocks()) {
+    seq_block += w.blocks();
+    w = plan.work(a, ++s, LY::BM, LY::BN);
   }
-  const int h = qh / a.G;
-  const AttnTile x = tile_of_rows(a, s, n0, cnt, first_position(a, s, cnt), (n - n0) * a.G + qh % a.G, 1);
-  const RowOut<E, D> ro{a, h, true, 0, 0};
-  careful_row(ro, Fp4Entries<E, D>(a, h), x, 0, x.lo, x.hi);
+  const int item = (at_block - seq_block) / w.nb, blk = at_block - seq_block - item * w.nb;
+  const int take = w.nb - blk < end_block - at_block ? w.nb - blk : end_block - at_block;
+  const int last_block = at_block - blk + w.nb - 1;  // of the item
+  at_block += take;
+  const int h = item % a.Hk;
+  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
+  const int64_t k0_ = (int64_t)(x.lo / LY::BN + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
+  const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
+  const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
+  if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
+
+  // this lane's row and its queries
+  const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
+  const int p = x.pos0 + row / a.G;
+  const int p_min = x.pos0 + x.row0 / a.G, p_max = x.pos0 + (x.row0 + x.rows - 1) / a.G;
+  const int lo = first_seen(a, p, 0), lo_max = first_seen(a, p_max, 0);
+  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D + g * (D / 4);
+  u32x4 q[NI][NQ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    if constexpr (NQ == 1) {
+      q[i][0] = reinterpret_cast<const u32x4*>(qp)[i];
+    } else {
+      float y[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) y[u] = qp[8 * i + u];
+      cut_parts(y, q[i]);
+    }
+  }
+
+  const uint8_t* kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head + g * (D / 8);
+  const uint8_t* vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head + g * (D / 8);
+  const uint8_t* ksb = a.ks + h * a.k.head + g * (D / 4) / kFp4Block;
+  const uint8_t* vsb = a.vs + h * a.v.head + g * (D / 4) / kFp4Block;
+  const int pmask = (1 << a.page_shift) - 1;
+  char* vl = lds + wave * KT * LY::VLD;
+
+  f32x4 o[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i] = zero4();
+  float m = kNoMax, l = 0.f;
+
+  // As in paged_rows_kernel: a lane looks up the pages of its two keys a block ahead.
+  const int* trow = a.table + s * a.table_row;
+  auto lookup = [&](int j0, int (&id)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j = j0 + 16 * b + c;
+      id[b] = trow[(j < k1 ? j : k1 - 1) >> a.page_shift];
+    }
+  };
+  Codes kr[2], vr[2];
+  unsigned kf[2], vf[2];                            // scales
+  unsigned long long okn = 0;                       // which of the 32 keys exist (bit = key)
+  auto fetch = [&](int j0, const int (&id)[2]) {
+    bool ok[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int j = j0 + 16 * b + c;
+      ok[b] = j >= k0 && j < k1 && (unsigned)id[b] < (unsigned)a.pages;
+      const unsigned pg = ok[b] ? id[b] : 0, off = j & pmask;
+      auto at = [&](const uint8_t* base, int64_t page, int64_t tok) {
+        return base + (uint64_t)pg * (unsigned)page + (uint64_t)off * (unsigned)tok;
+      };
+      kr[b] = *reinterpret_cast<const Codes*>(at(kb, a.kc_page, a.kc_tok));
+      kf[b] = *at(ksb, a.k.page, a.k.tok);
+      vr[b] = *reinterpret_cast<const Codes*>(at(vb, a.vc_page, a.vc_tok));
+      vf[b] = *at(vsb, a.v.page, a.v.tok);
+    }
+    okn = (__ballot(ok[0]) & 0xffffu) | ((__ballot(ok[1]) & 0xffffu) << 16);
+  };
+  constexpr int STEP = 4 * KT;
+  int j0 = (k0 / LY::BN) * LY::BN + wave * KT;
+  int id[2];
+  if (j0 < k1) {
+    int id0[2];
+    lookup(j0, id0);
+    lookup(j0 + STEP, id);
+    fetch(j0, id0);
+  }
+  for (; j0 < k1; j0 += STEP) {
+    const unsigned ok = (unsigned)okn;
+    f32x4 sc[2] = {zero4(), zero4()};
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float f = fp4_factor(kf[b]);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const u32x4 k = fp4_open8(kr[b][i], f);
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) sc[b] = mma_bits(k, q[i][u], sc[b]);
+      }
+    }
+    // values to LDS; rows that do not exist as zeros
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bool z = ok != 0xffffffffu && !((ok >> (16 * b + c)) & 1u);
+      const float f = fp4_factor(z ? 127u : vf[b]);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        *reinterpret_cast<u32x4*>(vl + (16 * b + c) * LY::VLD + g * (D / 2) + 16 * i) = fp4_open8(z ? 0u : vr[b][i], f);
+    }
+    if (j0 + STEP < k1) {
+      int id2[2];
+      lookup(j0 + 2 * STEP, id2);
+      fetch(j0 + STEP, id);
+      id[0] = id2[0]; id[1] = id2[1];
+    }
+    // lane: row c, keys 16 b + 4 g + i
+    if (ok != 0xffffffffu || j0 + KT - 1 > p_min || j0 < lo_max) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 16 * b + 4 * g + i, j = j0 + kk;
+          const bool see = ((ok >> kk) & 1u) && j <= p && j >= lo;
+          sc[b][i] = see ? sc[b][i] : -__builtin_inff();
+        }
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[b][i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__ballot((top - m) * a.c > kSlack)) {
+      const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i] *= al;
+    }
+    const float mc = m * a.c;
+    float e[8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[4 * b + i] = fast_exp2(sc[b][i] * a.c - mc);
+        l += e[4 * b + i];
+      }
+    // The weights go in as bf16 parts: two (16 bits) where the output is bf16, which
+    // costs nothing beside the loads, three (24) where it is fp32.
+    u32x4 pw[LY::NP];
+    if constexpr (LY::NP == 3) {
+      cut_parts(e, pw);
+    } else {
+      bf16x8 hi, rest;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[i] = (bf16)e[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rest[i] = (bf16)(e[i] - (float)hi[i]);
+      pw[0] = __builtin_bit_cast(u32x4, hi);
+      pw[1] = __builtin_bit_cast(u32x4, rest);
+    }
+    const char* src = vl + (4 * g + (lane & 15) / 4) * LY::VLD + (lane & 3) * 8;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const u32x2 v0 = __builtin_bit_cast(u32x2, read_tr(src + 32 * d));
+      const u32x2 v1 = __builtin_bit_cast(u32x2, read_tr(src + 32 * d + 16 * LY::VLD));
+      const u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
+#pragma unroll
+      for (int u = 0; u < LY::NP; ++u) o[d] = mma_bits(v, pw[u], o[d]);
+    }
+  }
+
+  // join the four waves (the last item's readers are past the barrier that ended it)
+  l = sum_groups(l);
+  if (threadIdx.x < 16) bad[threadIdx.x] = 0;
+  if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }
+  __syncthreads();
+  float* ol = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+    *reinterpret_cast<f32x4*>(ol + (wave * 16 + c) * LY::OLD + 16 * d + 4 * g) = o[d];
+  __syncthreads();
+  const int r = threadIdx.x >> 4, t = threadIdx.x & 15;
+  if (r < x.rows) {
+    float M = ms[0][r], Lr = 0.f, acc[D / 16];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) M = fmaxf(M, ms[w][r]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = fast_exp2((ms[w][r] - M) * a.c);
+      Lr += ls[w][r] * f;
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(ol + (w * 16 + r) * LY::OLD + t * (D / 16) + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[i + u] += v[u] * f;
+      }
+    }
+    const int64_t at = ro.index(x, r);
+    bool nf = odd_sum(Lr) || (Lr == 0.f && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
+    if (nf) bad[r] = 1;
+    if (ro.whole) {
+      const float inv = Lr == 0.f ? 0.f : 1.f / Lr;
+      E* out = ro.out(at) + t * (D / 16);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) out[i] = from_f32<E>(acc[i] * inv);
+    } else {
+      f32x4* out = reinterpret_cast<f32x4*>(ro.part(at, r) + t * (D / 16));
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4) out[i / 4] = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+    }
+    if (t == 0) ro.stats(at, r, M, Lr);
+  }
+  __syncthreads();
+  for (int i = wave; i < x.rows; i += 4)
+    if (bad[i]) careful_row(ro, Fp4Entries<E, D>(a, h), x, i, k0, k1);
+  __syncthreads();                                  // the next item writes the same LDS
+  }
 }
 
 }  // namespace carve
