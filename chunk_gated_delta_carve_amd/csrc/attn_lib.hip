@@ -1,7 +1,6 @@
 // Host side of the attention layer's entry points: validation, plan, dispatch.
 // Every check runs before the first HIP call.
-#include "attn_host.h"
-#include "kernels/paged_attn.h"
+#include "attn_plan.h"
 
 namespace {
 
@@ -28,9 +27,6 @@ int check_rope(const carve_rope_config* c) {
     if (r > kMaxInt) return CARVE_EUNSUPPORTED;
   return CARVE_OK;
 }
-
-constexpr int64_t kManyRows = 16384;   // rows to join: eight to a wave are two waves per SIMD
-constexpr int kWideJoin = 32;          // shares per item from which a workgroup joins a row, not a wave
 
 // Blocks of the gradient: four per CU share the rows of q and k in proportion,
 // each tensor at least one where it has rows.
@@ -89,94 +85,15 @@ int check_paged(const carve_paged_config* c) {
   return CARVE_OK;
 }
 
-// Kernel and split of an attention call, from sizes alone. The row kernel takes
-// fp32 and, in bf16, batches whose sequences average at most 16 rows (tokens x
-// grouped heads, one tile of it), or 32 where their tables or the window hold fewer
-// than kLongKeys keys, which is too short to pay for the tile kernels' start. Row and
-// tile kernel, all launches, 4 heads: of 128, 16 sequences of 4096 keys with 16 rows
-// 35 and 37 us, 24 rows 44 and 37, 32 rows 45 and 41; 64 of 2048 with 32 rows 93 and
-// 78; 4 of 1000 with 32 rows 14 and 18; of 64, 16 of 4096 with 32 rows 35 and 27, 4 of
-// 1000 with 32 rows 11 and 15.
-// Tiles have 128 rows (four waves) at d = 64. At d = 128 they have 256 (eight) where
-// those occupy more than half of the CUs, and 128 otherwise, two workgroups to a CU:
-// twice as many parts to spread, fewer rows wasted in a sequence's last tile, a
-// shorter start. With 256 and 128 rows, all launches, heads of 128: 64 tokens of 16 on
-// 2 heads over 4096 keys 27 and 23 us, 8 times 128 tokens of 16 on 4 over 4096 keys 93
-// and 85, 256 tokens over 32768 keys 123 and 118; 22 times 100 tokens of 16 on 2 over
-// 3600 keys, 180 tiles of 256 rows, 134 and 144.
-constexpr int kRowsShort = 32, kRowsLong = 16, kLongKeys = 2048;
-constexpr int kTileSplits = 128;
-constexpr int kCUs = 256;
-struct Plan {
-  bool tile;
-  int waves;                 // tile kernels: of a workgroup
-  int64_t tiles, most;       // row kernel: blocks of keys at most, over all items
-  int splits, shares;
-  int64_t rows;              // partial results
-  int64_t bytes;
-};
-
+// Row or tile kernel. Row and tile kernel, all launches, 4 heads: of 128, 16 sequences
+// of 4096 keys with 16 rows 35 and 37 us, 24 rows 44 and 37, 32 rows 45 and 41; 64 of
+// 2048 with 32 rows 93 and 78; 4 of 1000 with 32 rows 14 and 18; of 64, 16 of 4096 with
+// 32 rows 35 and 27, 4 of 1000 with 32 rows 11 and 15.
 Plan plan_of(const carve_paged_config* c) {
-  Plan p{};
-  if (c->N == 0 || c->S == 0 || c->Hk == 0 || c->Hq == 0) return p;
-  const int64_t G = c->Hq / c->Hk;
-  const bool step = (c->flags & CARVE_PAGED_STEP) != 0;
-  int64_t keys = (int64_t)c->width * c->page_size;
-  const int64_t seen = c->window > 0 && c->window < keys ? c->window : keys;
-  p.tile = c->dtype == CARVE_BF16 && (int64_t)c->N * G > (int64_t)(seen < kLongKeys ? kRowsShort : kRowsLong) * c->S;
-  auto tiles = [&](int BM) { return step ? c->S * up(G, BM) : up((int64_t)c->N * G, BM) + c->S - 1; };
-  p.waves = c->d == 128 && 2 * tiles(256) * c->Hk > kCUs ? 8 : 4;
-  const int BM = p.tile ? 32 * p.waves : 16, BN = p.tile ? 64 : 128;
-  p.tiles = tiles(BM);
-  if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
-  if (p.tile) {
-    // four waves: as many workgroups as the CUs hold at once; eight fill them with a tile each
-    const int64_t most = up(keys, (int64_t)BN * 4);
-    int64_t s = p.waves == 8 ? 1 : kCUs * (c->d == 64 ? 4 : 2) / (p.tiles * c->Hk);
-    s = s < most ? s : most;
-    s = s < kTileSplits ? s : kTileSplits;
-    p.splits = s < 1 ? 1 : (int)s;
-    p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
-  } else {
-    // a workgroup per block of keys at most; no item has more blocks than this counts
-    const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1);
-    const bool f32 = c->dtype == CARVE_F32;
-    const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;
-    const int slim = f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU;
-    const int64_t want = kCUs * (c->d == 128 ? wide : slim);
-    p.most = blocks;
-    p.shares = (int)(blocks < want ? blocks : want);
-    p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
-  }
-  const int64_t cuts = p.rows == 0 ? 0 : p.tile ? p.tiles * c->Hk : p.shares;
-  p.bytes = (p.rows * (c->d + 2) + cuts * carve::kCutInts) * 4;
-  return p;
-}
-
-template <int D, int WAVES, bool WIDE>
-constexpr auto tile_kernel() {
-  if constexpr (WAVES == 8) return carve::paged_step_kernel<D, WIDE>;
-  else return carve::paged_tile_kernel<D, WIDE>;
-}
-
-template <int D, int WAVES, bool WIDE>
-hipError_t launch_tiles(const carve::PagedArgs& a, hipStream_t s) {
-  using LY = carve::TileLayout<D, WAVES>;
-  constexpr auto kern = tile_kernel<D, WAVES, WIDE>();
-  hipError_t e = set_lds<kern>(LY::bytes);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)a.tiles * a.splits * a.Hk)), dim3(LY::NT), LY::bytes, s, a);
-  e = hipGetLastError();
-  if constexpr (WAVES == 4) {
-    if (e != hipSuccess || a.splits == 1) return e;
-    const unsigned tiles = a.tiles * a.Hk;
-    if (a.splits > carve::kFewShares || (int64_t)a.N * a.Hq < kManyRows)
-      hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 1>), dim3(tiles, LY::BM / 4), dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((carve::paged_tile_combine_kernel<D, 8>), dim3(tiles, LY::BM / 32), dim3(256), 0, s, a);
-    e = hipGetLastError();
-  }
-  return e;
+  const bool f32 = c->dtype == CARVE_F32;
+  const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;
+  const int slim = f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU;
+  return plan_attention(c, {c->d == 128 ? wide : slim, 32, 16, 2048});
 }
 
 template <typename E, int D>
@@ -185,22 +102,13 @@ hipError_t dispatch_attention(const carve::PagedArgs& a, const Plan& plan, hipSt
   using LY = carve::TileLayout<D, 4>;
   const int64_t reach = (LY::WR - 1) * 2 * std::max(a.kc_tok, a.vc_tok) + LY::CPR * 16;
   const bool wide = a.page_shift >= 3 && reach <= 0xffffffffLL;
-  if constexpr (sizeof(E) == 2 && D == 128)
-    if (plan.tile && plan.waves == 8) return wide ? launch_tiles<D, 8, true>(a, s) : launch_tiles<D, 8, false>(a, s);
   if constexpr (sizeof(E) == 2)
-    if (plan.tile) return wide ? launch_tiles<D, 4, true>(a, s) : launch_tiles<D, 4, false>(a, s);
+    if (plan.tile)
+      return wide ? launch_tiles<carve::PlainTiles, D, true>(a, plan, s)
+                  : launch_tiles<carve::PlainTiles, D, false>(a, plan, s);
   hipLaunchKernelGGL((carve::paged_rows_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.shares == 1) return e;
-  constexpr int BM = carve::RowsLayout<E, D>::BM;
-  const int64_t most = (a.cu ? a.N : 1) * (int64_t)a.G;      // rows of an item
-  const int rows = (int)(most < BM ? most : BM);
-  const int64_t items = a.Hk * (up((int64_t)a.N * a.G, BM) > a.S ? up((int64_t)a.N * a.G, BM) : a.S);
-  if (a.shares >= kWideJoin * items)
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(a.shares, rows), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 1>), dim3(a.shares, up(rows, 4)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return e != hipSuccess || a.shares == 1 ? e : join_rows<E, D>(a, s);
 }
 
 }  // namespace
@@ -408,10 +316,7 @@ int check_attention(const carve_paged_config* c) {
   if (!(c->scale > 0.f)) return CARVE_EINVAL;
   if (!(c->scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c->Hq > 0 && (c->Hk == 0 || c->Hq % c->Hk)) return CARVE_EINVAL;
-  const Plan p = plan_of(c);
-  if (p.tile && p.tiles * p.splits * c->Hk > kMaxThreads / (64 * p.waves)) return CARVE_EUNSUPPORTED;
-  if (p.most > kMaxInt) return CARVE_EUNSUPPORTED;
-  return CARVE_OK;
+  return check_plan(c, plan_of(c));
 }
 }  // namespace
 

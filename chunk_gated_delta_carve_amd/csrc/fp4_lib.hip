@@ -1,6 +1,6 @@
 // Host side of the 4-bit paged cache's entry points and of the room in a paged
 // cache: validation, plan, dispatch. Every check runs before the first HIP call.
-#include "attn_host.h"
+#include "attn_plan.h"
 #include "kernels/assign.h"
 #include "kernels/fp4.h"
 #include "kernels/paged_fp4.h"
@@ -179,50 +179,25 @@ extern "C" int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* 
 }
 
 namespace {
-// Split of an attention call, from sizes alone (see plan_of of the bf16 and fp32 cache).
-constexpr int kCUs = 256, kWideJoin = 32;
-struct Plan {
-  int64_t most;              // blocks of keys at most, over all items
-  int shares;
-  int64_t rows;              // partial results
-  int64_t bytes;
-};
-
 Plan plan_of(const carve_paged_config* c) {
-  Plan p{};
-  if (c->N == 0 || c->S == 0 || c->Hk == 0 || c->Hq == 0) return p;
-  const int64_t G = c->Hq / c->Hk;
-  const bool step = (c->flags & CARVE_PAGED_STEP) != 0, f32 = c->dtype == CARVE_F32;
-  int64_t keys = (int64_t)c->width * c->page_size;
-  constexpr int BM = 16, BN = carve::RowsFp4<float, 64>::BN;
-  const int64_t tiles = step ? c->S * up(G, BM) : up((int64_t)c->N * G, BM) + c->S - 1;
-  if (c->window > 0 && keys > (int64_t)c->window + BM + BN) keys = (int64_t)c->window + BM + BN;
-  // a workgroup per block of keys at most; no item has more blocks than this counts
-  p.most = tiles * c->Hk * (up(keys, BN) + 1);
+  const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsFp4<float, 64>::PER_CU : carve::RowsFp4<carve::bf16, 64>::PER_CU;
-  const int64_t want = kCUs * (c->d == 128 ? wide : slim);
-  p.shares = (int)(p.most < want ? p.most : want);
-  p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
-  const int64_t cuts = p.rows == 0 ? 0 : p.shares;
-  p.bytes = (p.rows * (c->d + 2) + cuts * carve::kCutInts) * 4;
-  return p;
+  return plan_attention(c, {c->d == 128 ? wide : slim, 32, 16, 2048});
 }
 
 template <typename E, int D>
-hipError_t dispatch_attention(const carve::Fp4Args& a, hipStream_t s) {
+hipError_t dispatch_attention(const carve::Fp4Args& a, const Plan& plan, hipStream_t s) {
+  // rows of one load of a wave in one page, their offsets from its first within 32 bits
+  constexpr int WR = carve::Fp4Tiles<D, 4, true>::WR;
+  const bool wide = (1 << a.page_shift) >= WR && (WR - 1) * std::max(a.kc_tok, a.vc_tok) + D / 2 <= 0xffffffffLL &&
+                    (WR - 1) * std::max(a.k.tok, a.v.tok) + D / carve::kFp4Block <= 0xffffffffLL;
+  if constexpr (sizeof(E) == 2)
+    if (plan.tile)
+      return wide ? launch_tiles<carve::Fp4Tiles, D, true>(a, plan, s) : launch_tiles<carve::Fp4Tiles, D, false>(a, plan, s);
   hipLaunchKernelGGL((carve::paged_rows_fp4_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.shares == 1) return e;
-  constexpr int BM = carve::RowsFp4<E, D>::BM;
-  const int64_t most = (a.cu ? a.N : 1) * (int64_t)a.G;      // rows of an item
-  const int rows = (int)(most < BM ? most : BM);
-  const int64_t items = a.Hk * (up((int64_t)a.N * a.G, BM) > a.S ? up((int64_t)a.N * a.G, BM) : a.S);
-  if (a.shares >= kWideJoin * items)
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(a.shares, rows), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 1>), dim3(a.shares, up(rows, 4)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return e != hipSuccess || a.shares == 1 ? e : join_rows<E, D>(a, s);
 }
 
 int check_attention(const carve_fp4_config* f) {
@@ -232,8 +207,7 @@ int check_attention(const carve_fp4_config* f) {
   if (!(c.scale > 0.f)) return CARVE_EINVAL;
   if (!(c.scale <= 16.f)) return CARVE_EUNSUPPORTED;
   if (c.Hq > 0 && (c.Hk == 0 || c.Hq % c.Hk)) return CARVE_EINVAL;
-  if (plan_of(&c).most > kMaxInt) return CARVE_EUNSUPPORTED;
-  return CARVE_OK;
+  return check_plan(&c, plan_of(&c));
 }
 }  // namespace
 
@@ -304,9 +278,9 @@ extern "C" int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void
   a.po = static_cast<float*>(workspace);
   a.pml = need ? a.po + plan.rows * c.d : nullptr;
   a.cuts = need ? reinterpret_cast<int*>(a.pml + plan.rows * 2) : nullptr;
-  a.shares = plan.shares;
+  a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
-    return dispatch_attention<decltype(t), decltype(d)::value>(a, reinterpret_cast<hipStream_t>(stream));
+    return dispatch_attention<decltype(t), decltype(d)::value>(a, plan, reinterpret_cast<hipStream_t>(stream));
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);
 }

@@ -683,12 +683,16 @@ struct TileLayout {
   static constexpr int WR = 64 / CPR;                        // rows of one load of a wave
 };
 
-template <int D, int NW, bool WIDE>
-struct TileWork {
+// A workgroup's tile and blocks and a wave's rows. How a block of keys and values gets
+// from the cache to LDS is left to what derives from this.
+template <int D_, int NW, typename A>
+struct TileRows {
+  static constexpr int D = D_;
+  using Args = A;
   using LY = TileLayout<D, NW>;
   using E = bf16;
   static constexpr bool SPLIT = NW == 4;            // eight waves run where tiles fill the CUs: one workgroup each
-  const PagedArgs& a;
+  const A& a;
   AttnTile x;
   int h, sp, first_b, T;                            // key/value head, share, first block, blocks
   bool whole;
@@ -696,12 +700,10 @@ struct TileWork {
   int p, p_min, p_max;                              // position of the lane's row, of the wave's first and last
   int lo_min, lo_max;                               // first keys that the wave's first and last rows see
   bf16x8 q[D / 16];
-  const char *kb, *vb;
   const int* trow;
-  int pmask, sr, sc;
-  unsigned k_page, k_tok, v_page, v_tok, k_off, v_off;   // strides in bytes, below 2^32
+  int pmask;
 
-  __device__ __forceinline__ TileWork(const PagedArgs& a_) : a(a_) {
+  __device__ __forceinline__ TileRows(const A& a_) : a(a_) {
     h = blockIdx.x % a.Hk;
     const int rest = blockIdx.x / a.Hk;
     sp = SPLIT ? rest / a.tiles : 0;
@@ -739,16 +741,8 @@ struct TileWork {
     const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
-    kb = reinterpret_cast<const char*>(static_cast<const E*>(a.kc) + h * a.kc_head);
-    vb = reinterpret_cast<const char*>(static_cast<const E*>(a.vc) + h * a.vc_head);
     trow = a.table + x.s * a.table_row;
     pmask = (1 << a.page_shift) - 1;
-    sr = threadIdx.x / LY::CPR;
-    sc = threadIdx.x % LY::CPR;
-    k_page = (unsigned)a.kc_page * 2u; k_tok = (unsigned)a.kc_tok * 2u;
-    v_page = (unsigned)a.vc_page * 2u; v_tok = (unsigned)a.vc_tok * 2u;
-    k_off = (lane / LY::CPR) * k_tok + sc * 16;
-    v_off = (lane / LY::CPR) * v_tok + sc * 16;
   }
   // The queries are here before the loop: without this the waits for them stand in it.
   __device__ __forceinline__ void have_queries() {
@@ -766,40 +760,6 @@ struct TileWork {
   __device__ __forceinline__ unsigned long long valid(int t, int id) const {   // the block's keys that exist, a bit each
     const int j = (first_b + t) * LY::BN + lane;
     return __ballot((j >= x.lo) & (j < x.hi) & ((unsigned)id < (unsigned)a.pages));
-  }
-  // Byte offset of the lane's key of block t, on page `id` (page 0 where there is none).
-  __device__ __forceinline__ uint64_t place(int t, int id, unsigned page_bytes, unsigned tok_bytes) const {
-    const unsigned pg = (unsigned)id < (unsigned)a.pages ? id : 0;
-    const unsigned off = ((first_b + t) * LY::BN + lane) & pmask;
-    return (uint64_t)pg * page_bytes + (uint64_t)off * tok_bytes;
-  }
-  // The thread's chunk i of a block. The rows that one load of a wave covers (4, or
-  // 8 at d = 64) lie in one page of at least 8 tokens (WIDE): their first row's
-  // address is a scalar then, and a lane adds a constant of 32 bits. Token strides
-  // that would pass those take the other form.
-  __device__ __forceinline__ u32x4 load(const char* base, uint64_t at, unsigned lane_off, int i) const {
-    if constexpr (WIDE) {
-      const int r0 = wave * LY::WR + LY::RS * i;
-      const unsigned lo = __builtin_amdgcn_readlane((int)at, r0), hi = __builtin_amdgcn_readlane((int)(at >> 32), r0);
-      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + lane_off);
-    } else {
-      const int rr = sr + LY::RS * i;
-      const unsigned lo = __shfl((int)at, rr), hi = __shfl((int)(at >> 32), rr);
-      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + sc * 16);
-    }
-  }
-  __device__ __forceinline__ u32x4 load_k(uint64_t at, int i) const { return load(kb, at, k_off, i); }
-  __device__ __forceinline__ u32x4 load_v(uint64_t at, int i) const { return load(vb, at, v_off, i); }
-  // Zeros in the place of values whose key does not exist: a weight of 0 would not
-  // drop what an unused cache entry holds if that is not finite.
-  __device__ __forceinline__ void clear(unsigned long long ok, u32x4 (&vr)[LY::ST]) const {
-    if (ok != ~0ull) {
-#pragma unroll
-      for (int i = 0; i < LY::ST; ++i) {
-        const unsigned keep = (ok >> (sr + LY::RS * i)) & 1ull ? ~0u : 0u;
-        vr[i] &= u32x4{keep, keep, keep, keep};
-      }
-    }
   }
   // Scores of block t that a row does not see. Lane: row c, keys 32 kb2 + 8 (u / 4) + 4 hf + u % 4.
   __device__ __forceinline__ void mask(int t, unsigned long long ok, f32x16 (&s)[2]) const {
@@ -834,6 +794,8 @@ struct TileWork {
         for (int u = 0; u < 16; ++u) o[i][u] *= al;
     }
   }
+  // Cache: a key/value head, an entry at a time (as PlainEntries)
+  template <typename Cache>
   __device__ __forceinline__ void finish(const f32x16 (&o)[D / 32], float m, float l) const {
     l += __shfl_xor(l, 32);
     const RowOut<E, D> ro{a, h, !SPLIT || whole, (int64_t)sp * a.N * a.Hq, 0};
@@ -876,8 +838,85 @@ struct TileWork {
     while (again) {
       const int i = __ffsll((unsigned long long)again) - 1;
       again &= again - 1;
-      careful_row(ro, PlainEntries<E, D>(a, h), x, wave * 32 + i, k0, k1);
+      careful_row(ro, Cache(a, h), x, wave * 32 + i, k0, k1);
     }
+  }
+};
+
+// Blocks of a bf16 cache: 16-byte chunks by way of registers.
+template <int D, int NW, bool WIDE>
+struct PlainTiles : TileRows<D, NW, PagedArgs> {
+  using R = TileRows<D, NW, PagedArgs>;
+  using LY = typename R::LY;
+  using Cache = PlainEntries<bf16, D>;
+  using Chunks = u32x4[LY::ST];                     // a thread's part of a block
+  using Place = uint64_t;
+  using R::a; using R::lane; using R::wave; using R::h; using R::first_b; using R::pmask;
+  const char *kb, *vb;
+  int sr, sc;
+  unsigned k_page, k_tok, v_page, v_tok, k_off, v_off;   // strides in bytes, below 2^32
+
+  __device__ __forceinline__ PlainTiles(const PagedArgs& a_) : R(a_) {
+    kb = reinterpret_cast<const char*>(static_cast<const bf16*>(a.kc) + h * a.kc_head);
+    vb = reinterpret_cast<const char*>(static_cast<const bf16*>(a.vc) + h * a.vc_head);
+    sr = threadIdx.x / LY::CPR;
+    sc = threadIdx.x % LY::CPR;
+    k_page = (unsigned)a.kc_page * 2u; k_tok = (unsigned)a.kc_tok * 2u;
+    v_page = (unsigned)a.vc_page * 2u; v_tok = (unsigned)a.vc_tok * 2u;
+    k_off = (lane_id() / LY::CPR) * k_tok + sc * 16;
+    v_off = (lane_id() / LY::CPR) * v_tok + sc * 16;
+  }
+  // Byte offset of the lane's key of block t, on page `id` (page 0 where there is none).
+  __device__ __forceinline__ uint64_t place(int t, int id, unsigned page_bytes, unsigned tok_bytes) const {
+    const unsigned pg = (unsigned)id < (unsigned)a.pages ? id : 0;
+    const unsigned off = ((first_b + t) * LY::BN + lane) & pmask;
+    return (uint64_t)pg * page_bytes + (uint64_t)off * tok_bytes;
+  }
+  // The thread's chunk i of a block. The rows that one load of a wave covers (4, or
+  // 8 at d = 64) lie in one page of at least 8 tokens (WIDE): their first row's
+  // address is a scalar then, and a lane adds a constant of 32 bits. Token strides
+  // that would pass those take the other form.
+  __device__ __forceinline__ u32x4 load(const char* base, uint64_t at, unsigned lane_off, int i) const {
+    if constexpr (WIDE) {
+      const int r0 = wave * LY::WR + LY::RS * i;
+      const unsigned lo = __builtin_amdgcn_readlane((int)at, r0), hi = __builtin_amdgcn_readlane((int)(at >> 32), r0);
+      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + lane_off);
+    } else {
+      const int rr = sr + LY::RS * i;
+      const unsigned lo = __shfl((int)at, rr), hi = __shfl((int)(at >> 32), rr);
+      return *reinterpret_cast<const u32x4*>(base + ((uint64_t)hi << 32 | lo) + sc * 16);
+    }
+  }
+  __device__ __forceinline__ Place place_k(int t, int id) const { return place(t, id, k_page, k_tok); }
+  __device__ __forceinline__ Place place_v(int t, int id) const { return place(t, id, v_page, v_tok); }
+  __device__ __forceinline__ void load_k(Place at, Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) r[i] = load(kb, at, k_off, i);
+  }
+  __device__ __forceinline__ void load_v(Place at, Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i) r[i] = load(vb, at, v_off, i);
+  }
+  // Zeros in the place of values whose key does not exist: a weight of 0 would not
+  // drop what an unused cache entry holds if that is not finite.
+  __device__ __forceinline__ void clear(unsigned long long ok, Chunks& vr) const {
+    if (ok != ~0ull) {
+#pragma unroll
+      for (int i = 0; i < LY::ST; ++i) {
+        const unsigned keep = (ok >> (sr + LY::RS * i)) & 1ull ? ~0u : 0u;
+        vr[i] &= u32x4{keep, keep, keep, keep};
+      }
+    }
+  }
+  __device__ __forceinline__ void store_k(char* block, const Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i)
+      *reinterpret_cast<u32x4*>(block + sr * LY::KLD + sc * 16 + LY::RS * i * LY::KLD) = r[i];
+  }
+  __device__ __forceinline__ void store_v(char* block, const Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < LY::ST; ++i)
+      *reinterpret_cast<u32x4*>(block + sr * LY::VLD + sc * 16 + LY::RS * i * LY::VLD) = r[i];
   }
 };
 
@@ -890,9 +929,9 @@ struct TileWork {
 // TFLOP/s). In the loop the matrix units are busy 57% of the time; a workgroup of 18
 // blocks spends an eighth of its time on finding its tile and its first loads.
 // d = 128: two workgroups per CU, for calls of few tiles.
-template <int D, bool WIDE>
-__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedArgs a) {
-  using W = TileWork<D, 4, WIDE>;
+template <typename W>
+__global__ __launch_bounds__(256, W::D == 64 ? 4 : 2) void paged_tile_kernel(typename W::Args a) {
+  constexpr int D = W::D;
   using LY = typename W::LY;
   extern __shared__ __align__(16) char lds[];
   W w(a);
@@ -905,24 +944,16 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedA
     for (int u = 0; u < 16; ++u) o[i][u] = 0.f;
   float m = kNoMax, l = 0.f;
   constexpr int buf_bytes = LY::k_bytes + LY::v_bytes;
-  u32x4 kr[LY::ST], vr[LY::ST];
+  typename W::Chunks kr, vr;
   auto fetch = [&](int t, int id) {
-    const uint64_t k_at = w.place(t, id, w.k_page, w.k_tok), v_at = w.place(t, id, w.v_page, w.v_tok);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) {
-      kr[i] = w.load_k(k_at, i);
-      vr[i] = w.load_v(v_at, i);
-    }
+    const typename W::Place k_at = w.place_k(t, id), v_at = w.place_v(t, id);
+    w.load_k(k_at, kr);
+    w.load_v(v_at, vr);
   };
   auto store = [&](int buf, unsigned long long ok) {
-    char* kl = lds + buf * buf_bytes + w.sr * LY::KLD + w.sc * 16;
-    char* vl = lds + buf * buf_bytes + LY::k_bytes + w.sr * LY::VLD + w.sc * 16;
     w.clear(ok, vr);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) {
-      *reinterpret_cast<u32x4*>(kl + LY::RS * i * LY::KLD) = kr[i];
-      *reinterpret_cast<u32x4*>(vl + LY::RS * i * LY::VLD) = vr[i];
-    }
+    w.store_k(lds + buf * buf_bytes, kr);
+    w.store_v(lds + buf * buf_bytes + LY::k_bytes, vr);
   };
   unsigned long long ok = 0;
   int idn = 0;                                      // table entry of the block after the one in registers
@@ -989,7 +1020,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedA
     store(buf ^ 1, okn);
     ok = okn;
   }
-  w.finish(o, m, l);
+  w.template finish<typename W::Cache>(o, m, l);
 }
 
 // d = 128, many tiles: eight waves, two blocks under way in each. A wave issues an
@@ -1008,9 +1039,9 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void paged_tile_kernel(PagedA
 // 4096 tokens of 16 heads over 16384 keys (481 GFLOP): 495 to 527 us a call by card,
 // 913 to 970 TFLOP/s, where the kernel above takes 600 us. Those are 256 workgroups of
 // 192 to 256 blocks on 256 CUs: the longest decides, an eighth above the mean.
-template <int D, bool WIDE>
-__global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
-  using W = TileWork<D, 8, WIDE>;
+template <typename W>
+__global__ __launch_bounds__(512, 2) void paged_step_kernel(typename W::Args a) {
+  constexpr int D = W::D;
   using LY = typename W::LY;
   extern __shared__ __align__(16) char lds[];
   W w(a);
@@ -1023,51 +1054,39 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
     for (int u = 0; u < 16; ++u) o[i][u] = 0.f;
   float m = kNoMax, l = 0.f, top = 0.f;             // top: the row's maximum in the next block
 
-  u32x4 kr[LY::ST], vr[LY::ST];
+  typename W::Chunks kr, vr;
   int pair = 0;                                     // the pair in registers: keys pair + 1, values pair
   int id1 = 0, id2 = 0;                             // table entries of blocks pair + 1 and pair + 2
   unsigned long long ok_now = 0, ok_last = 0;       // keys of blocks pair and pair - 1
   char* vlds = lds + 2 * LY::k_bytes;
-  char* k_dst = lds + w.sr * LY::KLD + w.sc * 16;
-  char* v_dst = vlds + w.sr * LY::VLD + w.sc * 16;
   // Pair to LDS, the one after it under way. Nothing here depends on how many
   // blocks are left (blocks past the end are not used), so the counts of loads in
   // flight are known and each wait is for its own.
   auto next_pair = [&]() {
     w.clear(ok_now, vr);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i)
-      *reinterpret_cast<u32x4*>(k_dst + ((pair + 1) & 1) * LY::k_bytes + LY::RS * i * LY::KLD) = kr[i];
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i)
-      *reinterpret_cast<u32x4*>(v_dst + (pair & 1) * LY::v_bytes + LY::RS * i * LY::VLD) = vr[i];
+    w.store_k(lds + ((pair + 1) & 1) * LY::k_bytes, kr);
+    w.store_v(vlds + (pair & 1) * LY::v_bytes, vr);
     ok_last = ok_now;
     ok_now = w.valid(pair + 1, id1);
     ++pair;
-    const uint64_t k_at = w.place(pair + 1, id2, w.k_page, w.k_tok), v_at = w.place(pair, id1, w.v_page, w.v_tok);
+    const typename W::Place k_at = w.place_k(pair + 1, id2), v_at = w.place_v(pair, id1);
     id1 = id2;
     id2 = w.lookup(pair + 2);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) vr[i] = w.load_v(v_at, i);
+    w.load_k(k_at, kr);
+    w.load_v(v_at, vr);
   };
   if (T > 0) {
     const int id0 = w.lookup(0);
     id1 = w.lookup(1);
     id2 = w.lookup(2);
     ok_now = w.valid(0, id0);
-    uint64_t k_at = w.place(0, id0, w.k_page, w.k_tok);
-    const uint64_t v_at = w.place(0, id0, w.v_page, w.v_tok);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) *reinterpret_cast<u32x4*>(k_dst + LY::RS * i * LY::KLD) = kr[i];
-    k_at = w.place(1, id1, w.k_page, w.k_tok);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) kr[i] = w.load_k(k_at, i);
-#pragma unroll
-    for (int i = 0; i < LY::ST; ++i) vr[i] = w.load_v(v_at, i);
+    typename W::Place k_at = w.place_k(0, id0);
+    const typename W::Place v_at = w.place_v(0, id0);
+    w.load_k(k_at, kr);
+    w.store_k(lds, kr);
+    k_at = w.place_k(1, id1);
+    w.load_k(k_at, kr);
+    w.load_v(v_at, vr);
   }
   w.have_queries();
 
@@ -1188,7 +1207,7 @@ __global__ __launch_bounds__(512, 2) void paged_step_kernel(PagedArgs a) {
       step(t, s0, s1);
       if (t + 1 < T) step(t + 1, s1, s0);
     }
-  w.finish(o, m, l);
+  w.template finish<typename W::Cache>(o, m, l);
 }
 
 // ---------------------------------------------------------------------------

@@ -39,7 +39,7 @@ struct Fp4Entries {
     return s;
   }
   __device__ __forceinline__ void add(int id, int64_t off, float w, float (&o)[PER]) const {
-    // lane l has channels l PER on: half a byte at d = 64
+    // lane l has the channels from l PER on: half a byte at d = 64
     const int at = lane_id() * PER;
     const unsigned c = vc[id * a.vc_page + off * a.vc_tok + at / 2];
     const float s = fp4_factor(vs[id * a.v.page + off * a.v.tok + at / kFp4Block]);
@@ -331,5 +331,86 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   __syncthreads();                                  // the next item writes the same LDS
   }
 }
+
+// ---------------------------------------------------------------------------
+// Many rows (bf16): the kernels of paged_attn.h over blocks that are opened to bf16 on
+// their way from registers to LDS. A thread has 16 channels of a key, 8 bytes and a
+// scale: 64 keys of 128 channels are one such piece for each of 512 threads, keys and
+// values alike, 16 conversions and four 16-byte stores a step.
+template <int D, int NW, bool WIDE>
+struct Fp4Tiles : TileRows<D, NW, Fp4Args> {
+  using R = TileRows<D, NW, Fp4Args>;
+  using LY = typename R::LY;
+  using Cache = Fp4Entries<bf16, D>;
+  static constexpr int GPR = D / 16;                // pieces per key
+  static constexpr int ST = LY::BN * GPR / LY::NT, RS = LY::NT / GPR, WR = 64 / GPR;   // as TileLayout has them
+  struct Chunks { u32x2 codes[ST]; unsigned scale[ST]; };
+  struct Place { unsigned page, off; };
+  using R::a; using R::h; using R::first_b; using R::pmask;
+  const uint8_t *kb, *vb, *ksb, *vsb;
+  int sr, sc;
+
+  __device__ __forceinline__ Fp4Tiles(const Fp4Args& a_) : R(a_) {
+    kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head;
+    vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head;
+    ksb = a.ks + h * a.k.head;
+    vsb = a.vs + h * a.v.head;
+    sr = threadIdx.x / GPR;
+    sc = threadIdx.x % GPR;
+  }
+  // Page (0 where there is none) and offset in it of the lane's key of block t.
+  __device__ __forceinline__ Place place(int t, int id) const {
+    return {(unsigned)id < (unsigned)a.pages ? (unsigned)id : 0u, (unsigned)((first_b + t) * LY::BN + lane_id()) & pmask};
+  }
+  __device__ __forceinline__ Place place_k(int t, int id) const { return place(t, id); }
+  __device__ __forceinline__ Place place_v(int t, int id) const { return place(t, id); }
+  // As PlainTiles::load: one load of a wave covers 8 keys (16 at d = 64), and in pages
+  // that hold so many the first one's address is a scalar.
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t page, int64_t tok,
+                                       const Fp4Strides& s, Place at, Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      if constexpr (WIDE) {
+        const int r0 = wave_id() * WR + RS * i;
+        const unsigned pg = __builtin_amdgcn_readlane((int)at.page, r0), off = __builtin_amdgcn_readlane((int)at.off, r0);
+        const unsigned row = lane_id() / GPR;
+        const uint8_t* c = codes + (uint64_t)pg * (unsigned)page + (uint64_t)off * (unsigned)tok;
+        const uint8_t* e = scales + (uint64_t)pg * (unsigned)s.page + (uint64_t)off * (unsigned)s.tok;
+        r.codes[i] = *reinterpret_cast<const u32x2*>(c + (row * (unsigned)tok + sc * 8));
+        r.scale[i] = e[row * (unsigned)s.tok + sc / 2];
+      } else {
+        const int rr = sr + RS * i;
+        const unsigned pg = __shfl((int)at.page, rr), off = __shfl((int)at.off, rr);
+        r.codes[i] = *reinterpret_cast<const u32x2*>(codes + ((uint64_t)pg * (unsigned)page +
+                                                              (uint64_t)off * (unsigned)tok + sc * 8));
+        r.scale[i] = scales[(uint64_t)pg * (unsigned)s.page + (uint64_t)off * (unsigned)s.tok + sc / 2];
+      }
+    }
+  }
+  __device__ __forceinline__ void load_k(Place at, Chunks& r) const { load(kb, ksb, a.kc_page, a.kc_tok, a.k, at, r); }
+  __device__ __forceinline__ void load_v(Place at, Chunks& r) const { load(vb, vsb, a.vc_page, a.vc_tok, a.v, at, r); }
+  // Zeros in the place of values whose key does not exist.
+  __device__ __forceinline__ void clear(unsigned long long ok, Chunks& r) const {
+    if (ok != ~0ull) {
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+        if (!((ok >> (sr + RS * i)) & 1ull)) {
+          r.codes[i] = u32x2{0, 0};
+          r.scale[i] = 127;
+        }
+    }
+  }
+  __device__ __forceinline__ void store(char* block, int ld, const Chunks& r) const {
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      char* at = block + (sr + RS * i) * ld + sc * 32;
+      const float f = fp4_factor(r.scale[i]);
+      *reinterpret_cast<u32x4*>(at) = fp4_open8(r.codes[i][0], f);
+      *reinterpret_cast<u32x4*>(at + 16) = fp4_open8(r.codes[i][1], f);
+    }
+  }
+  __device__ __forceinline__ void store_k(char* block, const Chunks& r) const { store(block, LY::KLD, r); }
+  __device__ __forceinline__ void store_v(char* block, const Chunks& r) const { store(block, LY::VLD, r); }
+};
 
 }  // namespace carve
