@@ -93,7 +93,7 @@ Plan plan_of(const carve_paged_config* c) {
   const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU;
-  return plan_attention(c, {c->d == 128 ? wide : slim, 32, 16, 2048});
+  return plan_attention(c, {c->d == 128 ? wide : slim, 0, 32, 16, 2048});
 }
 
 template <typename E, int D>
@@ -380,6 +380,8 @@ extern "C" int carve_paged_attention(const carve_paged_config* cfg, const void* 
   a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
   a.window = c.window;
   a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
+  a.by_g = carve::Divisor(a.G); a.by_hk = carve::Divisor(a.Hk); a.by_hq = carve::Divisor(a.Hq);
+  a.by_shares = carve::Divisor(a.shares);
   a.scale = c.scale; a.c = c.scale * carve::kLog2e;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
     return dispatch_attention<decltype(t), decltype(d)::value>(a, plan, reinterpret_cast<hipStream_t>(stream));

@@ -23,6 +23,7 @@ constexpr int64_t kManyRows = 16384;   // rows to join: eight to a wave are two 
 constexpr int kWideJoin = 32;          // shares per item from which a workgroup joins a row, not a wave
 struct Choice {
   int per_cu;                // row kernel: workgroups that a CU holds
+  int more;                  // and blocks that an item counts for beside its own
   int rows_short, rows_long, long_keys;
 };
 struct Plan {
@@ -57,7 +58,7 @@ inline Plan plan_attention(const carve_paged_config* c, const Choice& ch) {
     p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
   } else {
     // a workgroup per block of keys at most; no item has more blocks than this counts
-    const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1);
+    const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1 + ch.more);
     const int64_t want = (int64_t)kCUs * ch.per_cu;
     p.most = blocks;
     p.shares = (int)(blocks < want ? blocks : want);

@@ -183,7 +183,7 @@ Plan plan_of(const carve_paged_config* c) {
   const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsFp4<float, 64>::PER_CU : carve::RowsFp4<carve::bf16, 64>::PER_CU;
-  return plan_attention(c, {c->d == 128 ? wide : slim, 32, 16, 2048});
+  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, 32, 16, 2048});
 }
 
 template <typename E, int D>
@@ -195,7 +195,12 @@ hipError_t dispatch_attention(const carve::Fp4Args& a, const Plan& plan, hipStre
   if constexpr (sizeof(E) == 2)
     if (plan.tile)
       return wide ? launch_tiles<carve::Fp4Tiles, D, true>(a, plan, s) : launch_tiles<carve::Fp4Tiles, D, false>(a, plan, s);
-  hipLaunchKernelGGL((carve::paged_rows_fp4_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
+  const bool runs = a.page_shift >= 4 && 15 * std::max(a.kc_tok, a.vc_tok) + D / 2 <= 0xffffffffLL &&
+                    15 * std::max(a.k.tok, a.v.tok) + D / carve::kFp4Block <= 0xffffffffLL;
+  if (runs)
+    hipLaunchKernelGGL((carve::paged_rows_fp4_kernel<E, D, true>), dim3(a.shares), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((carve::paged_rows_fp4_kernel<E, D, false>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess || a.shares == 1 ? e : join_rows<E, D>(a, s);
 }
@@ -279,6 +284,8 @@ extern "C" int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void
   a.pml = need ? a.po + plan.rows * c.d : nullptr;
   a.cuts = need ? reinterpret_cast<int*>(a.pml + plan.rows * 2) : nullptr;
   a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
+  a.by_g = carve::Divisor(a.G); a.by_hk = carve::Divisor(a.Hk); a.by_hq = carve::Divisor(a.Hq);
+  a.by_shares = carve::Divisor(a.shares);
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
     return dispatch_attention<decltype(t), decltype(d)::value>(a, plan, reinterpret_cast<hipStream_t>(stream));
   });

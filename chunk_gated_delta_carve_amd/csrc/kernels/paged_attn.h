@@ -37,6 +37,19 @@ namespace carve {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Division of n < 2^31 by a number that the host knows: floor(n mul / 2^(32 + shift)),
+// mul = ceil(2^(32 + shift) / d) with 2^shift < d <= 2^(shift + 1), is exact there.
+struct Divisor {
+  unsigned mul = 0, shift = 0;         // mul 0: d = 1
+  Divisor() = default;
+  explicit Divisor(unsigned d) {
+    if (d < 2) return;
+    while ((2ull << shift) < d) ++shift;
+    mul = (unsigned)(((1ull << (32 + shift)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int div(int n) const { return mul ? (int)(__umulhi((unsigned)n, mul) >> shift) : n; }
+};
+
 struct PagedArgs {
   const void *q, *kc, *vc;
   const int *cu, *kv_lens, *table;
@@ -50,6 +63,7 @@ struct PagedArgs {
   int tiles, splits;                                // tile kernel: tiles, workgroups per tile at most
   int shares;                                       // row kernel: workgroups that the work is dealt to
   float scale, c;                                   // c = scale log2 e
+  Divisor by_g, by_hk, by_hq, by_shares;            // by G, Hk, Hq and the most shares
 };
 
 // The reference m of a row follows its maximum only when that has grown by more
@@ -89,12 +103,13 @@ __device__ __forceinline__ AttnTile tile_of_rows(const PagedArgs& a, int s, int 
   x.s = s; x.n0 = n0; x.row0 = row0; x.pos0 = pos0;
   const int all = cnt * a.G;
   x.rows = all - row0 < BM ? all - row0 : BM;
-  const int64_t cap = (int64_t)a.width << a.page_shift;
-  const int64_t first = (int64_t)x.pos0 + row0 / a.G, last = (int64_t)x.pos0 + (row0 + x.rows - 1) / a.G;
-  const int64_t hi = last + 1 < cap ? last + 1 : cap;
-  const int64_t lo = a.window > 0 && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
-  x.hi = hi > 0 ? (int)hi : 0;
-  x.lo = lo < x.hi ? (int)lo : x.hi;
+  // positions lie in [-N, 2^31 - 2]
+  const int cap = a.width << a.page_shift;
+  const int first = x.pos0 + a.by_g.div(row0), last = x.pos0 + a.by_g.div(row0 + x.rows - 1);
+  const int hi = last + 1 < cap ? last + 1 : cap;
+  const int lo = a.window > 0 && first >= a.window ? first - a.window + 1 : 0;
+  x.hi = hi > 0 ? hi : 0;
+  x.lo = lo < x.hi ? lo : x.hi;
   return x;
 }
 
@@ -211,12 +226,13 @@ struct RowOut {
   bool whole;
   int64_t part0, part_row;                          // partial index of row r: part0 + (part_row ? r : index(r))
   __device__ __forceinline__ int64_t index(const AttnTile& x, int r) const {     // n Hq + query head
-    const int row = x.row0 + r;
-    return (int64_t)(x.n0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+    const int row = x.row0 + r, i = a.by_g.div(row);
+    return (int64_t)(x.n0 + i) * a.Hq + h * a.G + (row - i * a.G);
   }
   __device__ __forceinline__ int64_t slot(int64_t at, int r) const { return part0 + (part_row ? r : at); }
   __device__ __forceinline__ E* out(int64_t at) const {
-    return static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D;
+    const int n = a.by_hq.div((int)at);
+    return static_cast<E*>(a.o) + n * a.o_row + ((int)at - n * a.Hq) * D;
   }
   __device__ __forceinline__ float* part(int64_t at, int r) const { return a.po + slot(at, r) * D; }
   __device__ __forceinline__ void stats(int64_t at, int r, float m, float l) const {    // one lane per row
@@ -267,8 +283,8 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const C& cac
   const PagedArgs& a = ro.a;
   const int h = ro.h;
   const int64_t at = ro.index(x, r);
-  const int p = x.pos0 + (x.row0 + r) / a.G, lane = lane_id();
-  const E* q = static_cast<const E*>(a.q) + at / a.Hq * a.q_row + at % a.Hq * D;
+  const int i = a.by_g.div(x.row0 + r), p = x.pos0 + i, lane = lane_id();
+  const E* q = static_cast<const E*>(a.q) + (x.n0 + i) * a.q_row + (h * a.G + x.row0 + r - i * a.G) * D;
   const int first = first_seen(a, p, k0), end = p + 1 < k1 ? p + 1 : k1;
   float m = kLeast, l = 0.f, o[PER];
 #pragma unroll
@@ -370,6 +386,7 @@ struct RowsWork {
   int n0, cnt, pos0, items, nb;
   __device__ __forceinline__ int blocks() const { return items * nb; }
 };
+template <int MORE>                                 // blocks that an item counts for beside its own
 __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM, int BN) {
   RowsWork w;
   w.n0 = s; w.cnt = 1;
@@ -387,7 +404,17 @@ __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM,
     const int most = (int)(((unsigned)a.window + BM + BN - 3) / BN) + 1;
     w.nb = w.nb < most ? w.nb : most;
   }
+  w.nb += MORE;
   return w;
+}
+
+// n / d for n >= 0, d > 0, neither near 2^31: the quotient of floats is off by one at most
+// where it is below 2^20, and larger ones are left to the exact division.
+__device__ __forceinline__ int quotient(int n, int d) {
+  int q = (int)((float)n * __builtin_amdgcn_rcpf((float)d));
+  if (q > 0xfffff) return n / d;
+  const int r = n - q * d;
+  return r < 0 ? q - 1 : r >= d ? q + 1 : q;
 }
 
 // Prefix sums of the sequences' blocks, a lane per run of sequences; with one
@@ -403,12 +430,14 @@ struct RowsPlan {
     const int big = more * (base + 1);
     return b < big ? b / (base + 1) : more + (b - big) / base;
   }
+  template <int MORE = 0>
   __device__ __forceinline__ RowsWork work(const PagedArgs& a, int s, int BM, int BN) const {
-    if (run > 1) return rows_work(a, s, BM, BN);
+    if (run > 1) return rows_work<MORE>(a, s, BM, BN);
     auto at = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
     return RowsWork{at(own.n0), at(own.cnt), at(own.pos0), at(own.items), at(own.nb)};
   }
 };
+template <int MORE = 0>
 __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN) {
   RowsPlan p;
   p.run = (a.S + 63) >> 6;
@@ -417,7 +446,7 @@ __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN
 #pragma unroll 4
   for (int i = 0; i < p.run; ++i) {
     const int s = lane_id() * p.run + i;
-    const RowsWork w = rows_work(a, s < a.S ? s : a.S - 1, BM, BN);
+    const RowsWork w = rows_work<MORE>(a, s < a.S ? s : a.S - 1, BM, BN);
     if (s < a.S) { p.own = w; sum += w.blocks(); }
   }
   int incl = sum;
@@ -429,7 +458,7 @@ __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN
   p.before = incl - sum;
   p.total = __builtin_amdgcn_readlane(incl, 63);
   p.shares = p.total < a.shares ? p.total : a.shares;
-  p.base = p.total / (p.shares > 0 ? p.shares : 1);
+  p.base = p.shares < a.shares ? 1 : a.by_shares.div(p.total);
   p.more = p.total - p.base * p.shares;
   return p;
 }
@@ -462,8 +491,8 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   const int take = w.nb - blk < end_block - at_block ? w.nb - blk : end_block - at_block;
   const int last_block = at_block - blk + w.nb - 1;  // of the item
   at_block += take;
-  const int h = item % a.Hk;
-  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
+  const int tile = a.by_hk.div(item), h = item - tile * a.Hk;
+  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, tile * LY::BM, LY::BM);
   const int64_t k0_ = (int64_t)(x.lo / LY::BN + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
   const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
@@ -471,10 +500,10 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
 
   // this lane's row and its queries, in the pieces the keys come in
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
-  const int p = x.pos0 + row / a.G;
-  const int p_min = x.pos0 + x.row0 / a.G, p_max = x.pos0 + (x.row0 + x.rows - 1) / a.G;
+  const int tok = a.by_g.div(row), p = x.pos0 + tok;
+  const int p_min = x.pos0 + a.by_g.div(x.row0), p_max = x.pos0 + a.by_g.div(x.row0 + x.rows - 1);
   const int lo = first_seen(a, p, 0), lo_max = first_seen(a, p_max, 0);
-  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
+  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + tok) * a.q_row + (h * a.G + row - tok * a.G) * D;
   u32x4 q[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) q[i] = reinterpret_cast<const u32x4*>(qp)[4 * i + g];
@@ -644,7 +673,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
       }
     }
     const int64_t at = ro.index(x, r);
-    bool nf = odd_sum(L) || (L == 0.f && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
+    bool nf = odd_sum(L) || (L == 0.f && sees_any(a, x.pos0 + a.by_g.div(x.row0 + r), k0, k1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
@@ -704,8 +733,8 @@ struct TileRows {
   int pmask;
 
   __device__ __forceinline__ TileRows(const A& a_) : a(a_) {
-    h = blockIdx.x % a.Hk;
-    const int rest = blockIdx.x / a.Hk;
+    const int rest = a.by_hk.div(blockIdx.x);
+    h = blockIdx.x - rest * a.Hk;
     sp = SPLIT ? rest / a.tiles : 0;
     // the last tiles of a sequence see the most keys: start with them
     x = find_tile(a, a.tiles - 1 - (SPLIT ? rest % a.tiles : rest), LY::BM);
@@ -733,12 +762,13 @@ struct TileRows {
     const int wr0 = wave * 32 < x.rows ? wave * 32 : x.rows - 1;
     const int wr1 = wave * 32 + 31 < x.rows ? wave * 32 + 31 : x.rows - 1;
     const int row = x.row0 + (wave * 32 + c < x.rows ? wave * 32 + c : x.rows - 1);
-    p = x.pos0 + row / a.G;
-    p_min = x.pos0 + (x.row0 + wr0) / a.G;
-    p_max = x.pos0 + (x.row0 + wr1) / a.G;
+    const int tok = a.by_g.div(row);
+    p = x.pos0 + tok;
+    p_min = x.pos0 + a.by_g.div(x.row0 + wr0);
+    p_max = x.pos0 + a.by_g.div(x.row0 + wr1);
     lo_min = first_seen(a, p_min, 0);
     lo_max = first_seen(a, p_max, 0);
-    const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D;
+    const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + tok) * a.q_row + (h * a.G + row - tok * a.G) * D;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) q[i] = *reinterpret_cast<const bf16x8*>(qp + 16 * i + 8 * hf);
     trow = a.table + x.s * a.table_row;
@@ -833,7 +863,7 @@ struct TileRows {
     const int64_t k1_ = (int64_t)(first_b + T) * LY::BN;
     const int k1 = k1_ < x.hi ? (int)k1_ : x.hi;
     unsigned long long again = __ballot(nf);
-    if (__ballot(none)) again |= __ballot(none && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
+    if (__ballot(none)) again |= __ballot(none && sees_any(a, x.pos0 + a.by_g.div(x.row0 + r), k0, k1));
     again = (again | again >> 32) & 0xffffffffull;
     while (again) {
       const int i = __ffsll((unsigned long long)again) - 1;
@@ -1280,7 +1310,8 @@ __device__ __forceinline__ void join_shares(const PagedArgs& a, int64_t at, int6
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  E* out = static_cast<E*>(a.o) + at / a.Hq * a.o_row + at % a.Hq * D + lane * PER;
+  const int n = a.by_hq.div((int)at);
+  E* out = static_cast<E*>(a.o) + n * a.o_row + ((int)at - n * a.Hq) * D + lane * PER;
 #pragma unroll
   for (int k = 0; k < PER; ++k) out[k] = from_f32<E>(o[k] * inv);
   if (lane == 0 && a.lse)
@@ -1299,8 +1330,8 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
   const int n0 = cut[0], row0 = cut[1], rows = cut[2], h = cut[3], count = cut[4];
   const int64_t stride = (int64_t)a.N * a.Hq;
   auto index = [&](int r) {
-    const int row = row0 + r;
-    return (int64_t)(n0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+    const int row = row0 + r, i = a.by_g.div(row);
+    return (int64_t)(n0 + i) * a.Hq + h * a.G + (row - i * a.G);
   };
   const int first = (blockIdx.y * 4 + wave_id()) * ROWS;
   if (first >= rows) return;
@@ -1345,7 +1376,8 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (r0 + r < rows) {
-          bf16* out = static_cast<bf16*>(a.o) + at[r] / a.Hq * a.o_row + at[r] % a.Hq * D + lane * PER;
+          const int n = a.by_hq.div((int)at[r]);
+          bf16* out = static_cast<bf16*>(a.o) + n * a.o_row + ((int)at[r] - n * a.Hq) * D + lane * PER;
 #pragma unroll
           for (int k = 0; k < PER; ++k) out[k] = (bf16)o[r][k];
         }
@@ -1367,8 +1399,8 @@ __global__ __launch_bounds__(256) void paged_rows_combine_kernel(PagedArgs a) {
   const int* cut = a.cuts + w * kCutInts;
   const int r = WAVES > 1 ? blockIdx.y : blockIdx.y * 4 + wave_id();
   if (r >= cut[2]) return;
-  const int row = cut[1] + r;
-  const int64_t at = (int64_t)(cut[0] + row / a.G) * a.Hq + cut[3] * a.G + row % a.G;
+  const int row = cut[1] + r, i = a.by_g.div(row);
+  const int64_t at = (int64_t)(cut[0] + i) * a.Hq + cut[3] * a.G + (row - i * a.G);
   join_shares<E, D, WAVES>(a, at, (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r, 2 * LY::BM, cut[4]);
 }
 

@@ -89,7 +89,26 @@ __device__ __forceinline__ f32x4 mma_bits(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-template <typename E, int D>
+// Maximum over the four row groups of a C tile column, without a trip to LDS.
+__device__ __forceinline__ float max_groups(float x) {
+  auto u = __float_as_uint(x);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  u = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// An item costs a workgroup about as much before and after its blocks as three of them
+// (finding it, three dependent loads, joining the waves), so that much is added to its
+// blocks where the work is dealt out: short sequences, several to a workgroup, would
+// otherwise make the slowest ones. 64 sequences of 200 to 8192 keys, 4 heads of 128:
+// 37.5 us, without 44.
+constexpr int kStart = 3;
+
+// WIDE: pages of 16 tokens and more, so that 16 aligned keys lie in one. A lane looks
+// up the page of one of the wave's next 64 runs of 16 keys, and a run's address is a
+// scalar to which a lane adds a constant. Otherwise every lane looks up its own keys'.
+template <typename E, int D, bool WIDE>
 __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_kernel(Fp4Args a) {
   using LY = RowsFp4<E, D>;
   constexpr int NI = LY::NI, KT = LY::KT, NQ = LY::NQ;
@@ -98,38 +117,114 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   __shared__ float ms[4][16], ls[4][16];
   __shared__ int bad[16];
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
-  const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
+  const RowsPlan plan = rows_plan<kStart>(a, LY::BM, LY::BN);
   int* cut = a.cuts + blockIdx.x * kCutInts;
   if (threadIdx.x == 0 && a.shares > 1) cut[2] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
-  int at_block = plan.start(blockIdx.x);
+  int at_block = plan.start(blockIdx.x);            // in blocks of the plan, kStart more per item than it has
   const int end_block = plan.start(blockIdx.x + 1);
   const int in = 63 - __clzll(__ballot(plan.before <= at_block));
   int s = in * plan.run;
   int seq_block = __builtin_amdgcn_readlane(plan.before, in);
-  RowsWork w = plan.work(a, s, LY::BM, LY::BN);
+  RowsWork w = plan.work<kStart>(a, s, LY::BM, LY::BN);
   while (at_block < end_block) {
   while (at_block >= seq_block + w.blocks()) {
     seq_block += w.blocks();
-    w = plan.work(a, ++s, LY::BM, LY::BN);
+    w = plan.work<kStart>(a, ++s, LY::BM, LY::BN);
   }
-  const int item = (at_block - seq_block) / w.nb, blk = at_block - seq_block - item * w.nb;
-  const int take = w.nb - blk < end_block - at_block ? w.nb - blk : end_block - at_block;
-  const int last_block = at_block - blk + w.nb - 1;  // of the item
-  at_block += take;
-  const int h = item % a.Hk;
-  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, item / a.Hk * LY::BM, LY::BM);
-  const int64_t k0_ = (int64_t)(x.lo / LY::BN + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
-  const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
-  const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
-  if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
+  const int item = quotient(at_block - seq_block, w.nb), b0 = at_block - seq_block - item * w.nb;
+  const int b1 = w.nb - b0 < end_block - at_block ? w.nb : b0 + (end_block - at_block);
+  const int last_block = at_block - b0 + w.nb - 1;  // of the item
+  at_block += b1 - b0;
+  if (b1 <= kStart) continue;                       // the blocks that stand for the start alone: the next workgroup's
+  const int blk = b0 > kStart ? b0 - kStart : 0, take = b1 - kStart - blk;
+  const bool whole = take == w.nb - kStart;
+  const int tile = a.by_hk.div(item), h = item - tile * a.Hk;
+  const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, tile * LY::BM, LY::BM);
+  const int first_key = (x.lo / LY::BN + blk) * LY::BN;
+  const int k0 = __builtin_amdgcn_readfirstlane(first_key > x.lo ? first_key : x.lo);
+  const int k1 = __builtin_amdgcn_readfirstlane((x.hi - first_key) / LY::BN < take ? x.hi : first_key + take * LY::BN);
+  const RowOut<E, D> ro{a, h, whole, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
+
+  const uint8_t* kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head;
+  const uint8_t* vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head;
+  const uint8_t* ksb = a.ks + h * a.k.head;
+  const uint8_t* vsb = a.vs + h * a.v.head;
+  const int pmask = (1 << a.page_shift) - 1;
+  char* vl = lds + wave * KT * LY::VLD;
+
+  const int* trow = a.table + s * a.table_row;
+  constexpr int STEP = 4 * KT;
+  int j0 = (k0 / LY::BN) * LY::BN + wave * KT;
+  Codes kr[2], vr[2];
+  unsigned kf[2], vf[2];                            // scales
+  unsigned okn = 0;                                 // which of the 32 keys exist (bit = key)
+  const unsigned gc = g * (D / 8), gs = g * (D / 4) / kFp4Block;
+  int ids = 0, left = 0;                            // WIDE: page of a lane's run, iterations until the next lookup
+  int id[2];                                        // else: pages of the lane's keys, looked up a block ahead, since
+                                                    // looking at them sooner would wait for the loads under way
+  auto lookup = [&](int j) {
+    if constexpr (WIDE) {
+      const int mine = j + (lane >> 1) * STEP + 16 * (lane & 1);
+      ids = trow[(mine < k1 ? mine : k1 - 1) >> a.page_shift];
+      left = 32;
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int mine = j + 16 * b + c;
+        id[b] = trow[(mine < k1 ? mine : k1 - 1) >> a.page_shift];
+      }
+    }
+  };
+  auto fetch = [&](int j) {
+    if constexpr (WIDE) {
+      if (left == 0) lookup(j);
+      const int at_id = 64 - 2 * left--;
+      okn = 0;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int page = __builtin_amdgcn_readlane(ids, at_id + b), first = j + 16 * b;
+        const bool there = (unsigned)page < (unsigned)a.pages;
+        const int lo16 = k0 - first > 0 ? k0 - first : 0, hi16 = k1 - first < 16 ? k1 - first : 16;
+        if (there && hi16 > lo16) okn |= ((1u << hi16) - (1u << lo16)) << (16 * b);
+        const unsigned pg = there ? page : 0, off = first & pmask;
+        auto from = [&](const uint8_t* base, int64_t page_bytes, int64_t tok, unsigned part) {
+          const uint8_t* run = base + ((uint64_t)pg * (unsigned)page_bytes + (uint64_t)off * (unsigned)tok);
+          return run + ((unsigned)c * (unsigned)tok + part);
+        };
+        kr[b] = *reinterpret_cast<const Codes*>(from(kb, a.kc_page, a.kc_tok, gc));
+        kf[b] = *from(ksb, a.k.page, a.k.tok, gs);
+        vr[b] = *reinterpret_cast<const Codes*>(from(vb, a.vc_page, a.vc_tok, gc));
+        vf[b] = *from(vsb, a.v.page, a.v.tok, gs);
+      }
+    } else {
+      bool ok[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int mine = j + 16 * b + c;
+        ok[b] = mine >= k0 && mine < k1 && (unsigned)id[b] < (unsigned)a.pages;
+        const unsigned pg = ok[b] ? id[b] : 0, off = mine & pmask;
+        auto from = [&](const uint8_t* base, int64_t page_bytes, int64_t tok, unsigned part) {
+          return base + ((uint64_t)pg * (unsigned)page_bytes + (uint64_t)off * (unsigned)tok + part);
+        };
+        kr[b] = *reinterpret_cast<const Codes*>(from(kb, a.kc_page, a.kc_tok, gc));
+        kf[b] = *from(ksb, a.k.page, a.k.tok, gs);
+        vr[b] = *reinterpret_cast<const Codes*>(from(vb, a.vc_page, a.vc_tok, gc));
+        vf[b] = *from(vsb, a.v.page, a.v.tok, gs);
+      }
+      okn = (unsigned)(__ballot(ok[0]) & 0xffffu) | (unsigned)(__ballot(ok[1]) & 0xffffu) << 16;
+      lookup(j + STEP);
+    }
+  };
+  if (j0 < k1) lookup(j0);
 
   // this lane's row and its queries
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
-  const int p = x.pos0 + row / a.G;
-  const int p_min = x.pos0 + x.row0 / a.G, p_max = x.pos0 + (x.row0 + x.rows - 1) / a.G;
+  const int tok = a.by_g.div(row), p = x.pos0 + tok;
+  const int p_min = x.pos0 + a.by_g.div(x.row0), p_max = x.pos0 + a.by_g.div(x.row0 + x.rows - 1);
   const int lo = first_seen(a, p, 0), lo_max = first_seen(a, p_max, 0);
-  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + row / a.G) * a.q_row + (h * a.G + row % a.G) * D + g * (D / 4);
+  const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + tok) * a.q_row + (h * a.G + row - tok * a.G) * D +
+                g * (D / 4);
   u32x4 q[NI][NQ];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -143,58 +238,13 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
     }
   }
 
-  const uint8_t* kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head + g * (D / 8);
-  const uint8_t* vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head + g * (D / 8);
-  const uint8_t* ksb = a.ks + h * a.k.head + g * (D / 4) / kFp4Block;
-  const uint8_t* vsb = a.vs + h * a.v.head + g * (D / 4) / kFp4Block;
-  const int pmask = (1 << a.page_shift) - 1;
-  char* vl = lds + wave * KT * LY::VLD;
-
   f32x4 o[D / 16];
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) o[i] = zero4();
   float m = kNoMax, l = 0.f;
-
-  // As in paged_rows_kernel: a lane looks up the pages of its two keys a block ahead.
-  const int* trow = a.table + s * a.table_row;
-  auto lookup = [&](int j0, int (&id)[2]) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int j = j0 + 16 * b + c;
-      id[b] = trow[(j < k1 ? j : k1 - 1) >> a.page_shift];
-    }
-  };
-  Codes kr[2], vr[2];
-  unsigned kf[2], vf[2];                            // scales
-  unsigned long long okn = 0;                       // which of the 32 keys exist (bit = key)
-  auto fetch = [&](int j0, const int (&id)[2]) {
-    bool ok[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int j = j0 + 16 * b + c;
-      ok[b] = j >= k0 && j < k1 && (unsigned)id[b] < (unsigned)a.pages;
-      const unsigned pg = ok[b] ? id[b] : 0, off = j & pmask;
-      auto at = [&](const uint8_t* base, int64_t page, int64_t tok) {
-        return base + (uint64_t)pg * (unsigned)page + (uint64_t)off * (unsigned)tok;
-      };
-      kr[b] = *reinterpret_cast<const Codes*>(at(kb, a.kc_page, a.kc_tok));
-      kf[b] = *at(ksb, a.k.page, a.k.tok);
-      vr[b] = *reinterpret_cast<const Codes*>(at(vb, a.vc_page, a.vc_tok));
-      vf[b] = *at(vsb, a.v.page, a.v.tok);
-    }
-    okn = (__ballot(ok[0]) & 0xffffu) | ((__ballot(ok[1]) & 0xffffu) << 16);
-  };
-  constexpr int STEP = 4 * KT;
-  int j0 = (k0 / LY::BN) * LY::BN + wave * KT;
-  int id[2];
-  if (j0 < k1) {
-    int id0[2];
-    lookup(j0, id0);
-    lookup(j0 + STEP, id);
-    fetch(j0, id0);
-  }
+  if (j0 < k1) fetch(j0);
   for (; j0 < k1; j0 += STEP) {
-    const unsigned ok = (unsigned)okn;
+    const unsigned ok = okn;
     f32x4 sc[2] = {zero4(), zero4()};
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -215,12 +265,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
       for (int i = 0; i < NI; ++i)
         *reinterpret_cast<u32x4*>(vl + (16 * b + c) * LY::VLD + g * (D / 2) + 16 * i) = fp4_open8(z ? 0u : vr[b][i], f);
     }
-    if (j0 + STEP < k1) {
-      int id2[2];
-      lookup(j0 + 2 * STEP, id2);
-      fetch(j0 + STEP, id);
-      id[0] = id2[0]; id[1] = id2[1];
-    }
+    if (j0 + STEP < k1) fetch(j0 + STEP);
     // lane: row c, keys 16 b + 4 g + i
     if (ok != 0xffffffffu || j0 + KT - 1 > p_min || j0 < lo_max) {
 #pragma unroll
@@ -237,8 +282,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[b][i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_groups(top);
     if (__ballot((top - m) * a.c > kSlack)) {
       const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
       m = mn;
@@ -281,6 +325,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   }
 
   // join the four waves (the last item's readers are past the barrier that ended it)
+  if (threadIdx.x == 0 && blk == 0 && !whole) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
   l = sum_groups(l);
   if (threadIdx.x < 16) bad[threadIdx.x] = 0;
   if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }
@@ -309,7 +354,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
       }
     }
     const int64_t at = ro.index(x, r);
-    bool nf = odd_sum(Lr) || (Lr == 0.f && sees_any(a, x.pos0 + (x.row0 + r) / a.G, k0, k1));
+    bool nf = odd_sum(Lr) || (Lr == 0.f && sees_any(a, x.pos0 + a.by_g.div(x.row0 + r), k0, k1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
