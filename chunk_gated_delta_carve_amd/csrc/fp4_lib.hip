@@ -165,15 +165,12 @@ extern "C" int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* 
   a.k_row = c.k_row; a.v_row = c.v_row;
   a.entries = (int64_t)c.pages * c.page_size;
   a.N = c.N; a.Hk = c.Hk; a.heads = (int)heads; a.page_shift = shift_of(c.page_size);
-  const TokenWaves w = token_waves(c.N, heads, c.d, c.dtype);
-  if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
+  const int64_t blocks = up(c.N * heads * (c.d * (int64_t)es / 16), carve::kReadThreads * carve::kReadPieces);
+  if (blocks > kMaxThreads / carve::kReadThreads) return CARVE_EUNSUPPORTED;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
-    return by_pieces(w.per_lane, [&](auto u) {
-      hipLaunchKernelGGL((carve::paged_read_fp4_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
-                         dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                         a);
-      return hipGetLastError();
-    });
+    hipLaunchKernelGGL((carve::paged_read_fp4_kernel<decltype(t), decltype(d)::value>), dim3((unsigned)blocks),
+                       dim3(carve::kReadThreads), 0, reinterpret_cast<hipStream_t>(stream), a);
+    return hipGetLastError();
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);
 }
@@ -302,7 +299,7 @@ extern "C" int carve_paged_assign(const carve_assign_config* cfg, const int32_t*
       (c.S > 1 && c.table_row < c.width))
     return CARVE_EINVAL;
   if ((c.page_size & (c.page_size - 1)) || (int64_t)c.width * c.page_size > (1 << 30)) return CARVE_EUNSUPPORTED;
-  if (c.table_row > kMaxInt || c.capacity > kMaxInt) return CARVE_EUNSUPPORTED;
+  if (c.table_row > kMaxInt || c.capacity > kMaxInt || (int64_t)c.S * c.width > kMaxInt) return CARVE_EUNSUPPORTED;
   if (!free_count || !cu || !free_count_out) return CARVE_EINVAL;
   if (c.S > 0 && (!kv_lens || !new_lens || !kv_lens_out || (c.width > 0 && !table))) return CARVE_EINVAL;
   if (c.capacity > 0 && !free_pages) return CARVE_EINVAL;

@@ -26,18 +26,24 @@ struct AssignArgs {
 
 constexpr int kAssignThreads = 1024;
 constexpr int kAssignTokens = 4096;                 // up to here the first kernel does the tokens too
-constexpr int64_t kMostInt = 0x7fffffff;
+constexpr int kAssignLds = 4096;                    // requests whose offsets the second one keeps in LDS
+constexpr unsigned kMostInt = 0x7fffffff;
 
-// Exclusive prefix sums over the workgroup of two numbers; their totals in `all`.
-struct Two { int64_t a, b; };
+// Lengths and offsets stop at 2^31 - 1 (and pages in between cannot pass it: there are
+// at most that many table entries).
+__device__ __forceinline__ unsigned sum_to_most(unsigned a, unsigned b) { return a + b < kMostInt ? a + b : kMostInt; }
+
+// Exclusive prefix sums over the workgroup of two numbers below 2^31; their totals in `all`.
+struct Two { unsigned a, b; };
 __device__ __forceinline__ Two scan_two(Two x, Two& all) {
-  __shared__ int64_t sum[kAssignThreads / 64][2];
+  constexpr int W = kAssignThreads / 64;
+  __shared__ unsigned sum[W][2];
   const int lane = lane_id(), wave = wave_id();
   Two y = x;
 #pragma unroll
   for (int w = 1; w < 64; w <<= 1) {
-    const int64_t a = __shfl_up(y.a, w), b = __shfl_up(y.b, w);
-    if (lane >= w) { y.a += a; y.b += b; }
+    const unsigned a = __shfl_up(y.a, w), b = __shfl_up(y.b, w);
+    if (lane >= w) { y.a = sum_to_most(y.a, a); y.b = sum_to_most(y.b, b); }
   }
   __syncthreads();                                  // the last call's readers are done
   if (lane == 63) { sum[wave][0] = y.a; sum[wave][1] = y.b; }
@@ -45,136 +51,169 @@ __device__ __forceinline__ Two scan_two(Two x, Two& all) {
   all = Two{0, 0};
   Two before{0, 0};
 #pragma unroll
-  for (int w = 0; w < kAssignThreads / 64; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w == wave) before = all;
-    all.a += sum[w][0];
-    all.b += sum[w][1];
+    all.a = sum_to_most(all.a, sum[w][0]);
+    all.b = sum_to_most(all.b, sum[w][1]);
   }
-  return Two{before.a + y.a - x.a, before.b + y.b - x.b};
+  const unsigned ua = __shfl_up(y.a, 1), ub = __shfl_up(y.b, 1);
+  return Two{sum_to_most(before.a, lane ? ua : 0), sum_to_most(before.b, lane ? ub : 0)};
 }
 
 // Last i in [0, n) with first[i] <= at (first ascends, first[0] <= at).
 template <typename T>
-__device__ __forceinline__ int last_at(const T* first, int n, int64_t at) {
+__device__ __forceinline__ int last_at(const T* first, int n, unsigned at) {
   int lo = 0;
   while (n > 1) {
     const int half = n >> 1;
-    if (first[lo + half] <= at) { lo += half; n -= half; } else n = half;
+    if ((unsigned)first[lo + half] <= at) { lo += half; n -= half; } else n = half;
   }
   return lo;
 }
 
-__device__ __forceinline__ int64_t pages_of(const AssignArgs& a, int64_t tokens) {
-  const int64_t n = (tokens + (1 << a.page_shift) - 1) >> a.page_shift;
-  return n < a.width ? n : a.width;
+__device__ __forceinline__ unsigned pages_of(const AssignArgs& a, unsigned tokens) {
+  const unsigned n = (tokens + ((1u << a.page_shift) - 1)) >> a.page_shift;
+  return n < (unsigned)a.width ? n : a.width;
 }
 
-__device__ __forceinline__ int64_t at_least_0(int x) { return x > 0 ? x : 0; }
+__device__ __forceinline__ unsigned at_least_0(int x) { return x > 0 ? x : 0; }
 
-// Position and slot of token t, `s` its request, `c0` and `c1` the request's offsets.
-__device__ __forceinline__ void put_token(const AssignArgs& a, int64_t t, int s, int64_t c0, int64_t c1, int64_t kv) {
-  int64_t pos = 0, slot = -1;
+// Position and slot of token t of request s, whose tokens end before c1 at length kv;
+// t >= c1 for a token behind the last request.
+__device__ __forceinline__ void put_token(const AssignArgs& a, int t, int s, int c1, int kv) {
+  int pos = 0;
+  int64_t slot = -1;
   if (t < c1) {
     pos = kv - c1 + t;
     if (pos < 0) pos = 0;                           // lengths that stopped at 2^31 - 1
-    const int64_t i = pos >> a.page_shift;
+    const int i = pos >> a.page_shift;
     if (a.slots && i < a.width) {
-      const int64_t page = a.table[s * a.table_row + i];
-      if (page >= 0) slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+      const int page = a.table[s * a.table_row + i];
+      if (page >= 0) slot = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
     }
   }
-  if (a.positions) a.positions[t] = (int)pos;
+  if (a.positions) a.positions[t] = pos;
   if (a.slots) a.slots[t] = slot;
 }
 
+// Where few requests have many pages each, a thread takes this many of them: their loads
+// overlap, and one prefix sum does for all.
+constexpr int kAssignRun = 8;
+
 __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs a) {
-  __shared__ int64_t first[kAssignThreads];         // a request's first page among the chunk's
-  __shared__ int64_t offset[kAssignThreads + 1];    // and its first token
-  __shared__ int have[kAssignThreads];              // pages it holds already
+  __shared__ unsigned first[kAssignThreads];        // a request's first page among the chunk's
+  __shared__ unsigned offset[kAssignThreads + 1];   // and its first token
+  __shared__ unsigned have[kAssignThreads];         // pages it holds already
   const int tid = threadIdx.x;
-  int64_t top = a.free_count[0];
-  int64_t lacking = a.free_count[1];
-  top = top < 0 ? 0 : top < a.capacity ? top : a.capacity;
+  const unsigned capacity = (unsigned)a.capacity, lacking = a.free_count[1];
+  unsigned top = at_least_0(a.free_count[0]);
+  top = top < capacity ? top : capacity;
   Two all;
   // what ended requests give back
   if (a.done)
     for (int s0 = 0; s0 < a.S; s0 += kAssignThreads) {
       const int s = s0 + tid, n = a.S - s0 < kAssignThreads ? a.S - s0 : kAssignThreads;
-      const int64_t held = s < a.S && a.done[s] != 0 ? pages_of(a, at_least_0(a.kv_lens[s])) : 0;
-      first[tid] = scan_two(Two{held, 0}, all).a;
+      const unsigned held = s < a.S && a.done[s] != 0 ? pages_of(a, at_least_0(a.kv_lens[s])) : 0;
+      const unsigned mine = scan_two(Two{held, 0}, all).a;
+      first[tid] = mine;
       __syncthreads();
-      const int64_t entries = all.a;
-      for (int64_t i0 = 0; i0 < entries; i0 += kAssignThreads) {
-        const int64_t i = i0 + tid;
-        int page = -1;
-        if (i < entries) {
-          const int r = last_at(first, n, i);
-          page = a.table[(s0 + r) * a.table_row + (i - first[r])];
+      const unsigned entries = all.a;
+      for (unsigned i0 = 0; i0 < entries; i0 += kAssignThreads * kAssignRun) {
+        const unsigned i = i0 + tid * kAssignRun;
+        int page[kAssignRun];
+        unsigned good = 0;
+        int r = i < entries ? last_at(first, n, i) : 0;
+#pragma unroll
+        for (int u = 0; u < kAssignRun; ++u) {
+          page[u] = -1;
+          if (i + u < entries) {
+            while (r + 1 < n && first[r + 1] <= i + u) ++r;
+            page[u] = a.table[(s0 + r) * a.table_row + (i + u - first[r])];
+          }
         }
-        const int64_t at = top + scan_two(Two{page >= 0, 0}, all).a;
-        if (page >= 0 && at < a.capacity) a.free_pages[at] = page;
-        top = top + all.a < a.capacity ? top + all.a : a.capacity;
+#pragma unroll
+        for (int u = 0; u < kAssignRun; ++u) good += page[u] >= 0;
+        unsigned at = sum_to_most(top, scan_two(Two{good, 0}, all).a);
+#pragma unroll
+        for (int u = 0; u < kAssignRun; ++u)
+          if (page[u] >= 0 && at < capacity) a.free_pages[at++] = page[u];
+        top = sum_to_most(top, all.a) < capacity ? top + all.a : capacity;
       }
       __syncthreads();
     }
   // what the others take
-  int64_t used = 0, tokens = 0;
+  unsigned used = 0, tokens = 0;
   for (int s0 = 0; s0 < a.S; s0 += kAssignThreads) {
     const int s = s0 + tid, n = a.S - s0 < kAssignThreads ? a.S - s0 : kAssignThreads;
-    int64_t fresh = 0, need = 0;
+    unsigned fresh = 0, need = 0;
     if (s < a.S) {
-      const int64_t old = a.done && a.done[s] != 0 ? 0 : at_least_0(a.kv_lens[s]);
+      const unsigned old = a.done && a.done[s] != 0 ? 0 : at_least_0(a.kv_lens[s]);
       fresh = at_least_0(a.new_lens[s]);
-      const int64_t len = old + fresh < kMostInt ? old + fresh : kMostInt, holds = pages_of(a, old);
+      const unsigned len = sum_to_most(old, fresh), holds = pages_of(a, old);
       need = pages_of(a, len) - holds;
-      have[tid] = (int)holds;
+      have[tid] = holds;
       a.kv_out[s] = (int)len;
     }
     const Two at = scan_two(Two{need, fresh}, all);
     first[tid] = at.a;
-    auto offset_of = [&](int64_t x) { return tokens + x < kMostInt ? tokens + x : kMostInt; };
-    offset[tid] = offset_of(at.b);
+    offset[tid] = sum_to_most(tokens, at.b);
     if (s < a.S) a.cu[s] = (int)offset[tid];
     __syncthreads();
-    for (int64_t i = tid; i < all.a; i += kAssignThreads) {
-      const int r = last_at(first, n, i);
-      const int64_t from = top - 1 - used - i;
-      a.table[(s0 + r) * a.table_row + have[r] + (i - first[r])] = from >= 0 ? a.free_pages[from] : -1;
+    for (unsigned i0 = tid; i0 < all.a; i0 += kAssignThreads * 4) {
+      int page[4];
+      int64_t to[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {                 // four loads in flight
+        const unsigned i = i0 + u * kAssignThreads, from = sum_to_most(used, i);
+        page[u] = -1;
+        if (i >= all.a) continue;
+        const int r = last_at(first, n, i);
+        to[u] = (s0 + r) * a.table_row + have[r] + (i - first[r]);
+        if (from < top) page[u] = a.free_pages[top - 1 - from];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kAssignThreads < all.a) a.table[to[u]] = page[u];
     }
-    used += all.a;
-    tokens += all.b;
+    used = sum_to_most(used, all.a);
+    tokens = sum_to_most(tokens, all.b);
     __syncthreads();
   }
-  const int64_t total = tokens < kMostInt ? tokens : kMostInt;
   if (tid == 0) {
-    a.cu[a.S] = (int)total;
-    const int64_t lack = lacking + (used > top ? used - top : 0);
+    a.cu[a.S] = (int)tokens;
     a.count_out[0] = (int)(used < top ? top - used : 0);
-    a.count_out[1] = (int)(lack < kMostInt ? lack : kMostInt);
+    a.count_out[1] = (int)sum_to_most(lacking, used > top ? used - top : 0);
   }
   if (a.N > kAssignTokens || a.S > kAssignThreads || (!a.positions && !a.slots)) return;
   // the tokens of one chunk of requests, whose offsets are still here
-  const int s = tid < a.S ? tid : 0;
-  if (tid < a.S) first[tid] = a.kv_out[s];
-  if (tid == 0) offset[a.S] = total;
+  if (tid < a.S) first[tid] = a.kv_out[tid];
+  if (tid == 0) offset[a.S] = tokens;
   __syncthreads();
-  for (int64_t t = tid; t < a.N; t += kAssignThreads) {
-    if (a.S == 0 || t >= total) { put_token(a, t, 0, 0, 0, 0); continue; }
+  for (int t = tid; t < a.N; t += kAssignThreads) {
+    if ((unsigned)t >= tokens) { put_token(a, t, 0, 0, 0); continue; }
     const int r = last_at(offset, a.S, t);
-    put_token(a, t, r, offset[r], offset[r + 1], first[r]);
+    put_token(a, t, r, offset[r + 1], first[r]);
   }
 }
 
 // The tokens of a large call, 1024 to a workgroup.
 __global__ __launch_bounds__(256) void paged_assign_tokens_kernel(AssignArgs a) {
-  const int64_t total = a.cu[a.S];
+  __shared__ int offset[kAssignLds + 1];
+  const bool here = a.S <= kAssignLds;
+  if (here) {
+    for (int s = threadIdx.x; s <= a.S; s += 256) offset[s] = a.cu[s];
+    __syncthreads();
+  }
+  const int tokens = here ? offset[a.S] : a.cu[a.S];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int64_t t = (int64_t)blockIdx.x * 1024 + u * 256 + threadIdx.x;
     if (t >= a.N) return;
-    if (a.S == 0 || t >= total) { put_token(a, t, 0, 0, 0, 0); continue; }
-    const int s = last_at(a.cu, a.S, t);
-    put_token(a, t, s, a.cu[s], a.cu[s + 1], a.kv_out[s]);
+    if (t >= tokens) { put_token(a, (int)t, 0, 0, 0); continue; }
+    int s, end;
+    if (here) { s = last_at(offset, a.S, (unsigned)t); end = offset[s + 1]; }
+    else { s = last_at(a.cu, a.S, (unsigned)t); end = a.cu[s + 1]; }
+    put_token(a, (int)t, s, end, a.kv_out[s]);
   }
 }
 

@@ -150,41 +150,52 @@ struct Fp4ReadArgs {
   int N, Hk, heads, page_shift;        // heads: of k and v, those that are asked for
 };
 
-// One wave per row n and 64 U pieces of its heads (k's, then v's), 16 bytes of output
-// each.
-template <typename E, int D, int U>
-__global__ __launch_bounds__(256) void paged_read_fp4_kernel(Fp4ReadArgs a) {
-  constexpr int V = Piece<E>::V, LPR = D / V;
-  const int n = blockIdx.x * 4 + wave_id();
-  if (n >= a.N) return;
-  const int64_t slot = a.slots[n];
-  const bool there = slot >= 0 && slot < a.entries;
-  const int64_t page = there ? slot >> a.page_shift : 0, off = there ? slot & ((1 << a.page_shift) - 1) : 0;
-  const int c = lane_id() % LPR;
-  unsigned codes[U], byte[U];
-  int hh[U];
+// A piece is 16 bytes of output; the pieces of all slots and heads (a slot's k heads,
+// then its v heads) are laid end to end over the workgroups, kReadPieces of them in
+// flight to a lane, and the tokens of a workgroup's use the lines they read together.
+// Bound by memory: READ_NUMBERS
+constexpr int kReadPieces = 4, kReadThreads = 256;
+template <typename E, int D>
+__global__ __launch_bounds__(kReadThreads) void paged_read_fp4_kernel(Fp4ReadArgs a) {
+  constexpr int V = Piece<E>::V, LPR = D / V, U = kReadPieces;
+  const unsigned per = a.heads * LPR;               // pieces of a slot
+  const int64_t first = (int64_t)blockIdx.x * (kReadThreads * U), n0 = first / per;
+  const unsigned rest = (unsigned)(first - n0 * per);
+  const unsigned mask = (1u << a.page_shift) - 1;
+  int64_t n[U], slot[U];
+  unsigned piece[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    hh[u] = ((blockIdx.y * U + u) * 64 + lane_id()) / LPR;
-    const int h0 = hh[u] < a.heads ? hh[u] : a.heads - 1;
-    const bool isk = a.k && h0 < a.Hk;
-    const int h = isk || !a.k ? h0 : h0 - a.Hk;
-    const Fp4Strides &cs = isk ? a.kcs : a.vcs, &ss = isk ? a.kss : a.vss;
-    const uint8_t* pc = (isk ? a.kc : a.vc) + page * cs.page + off * cs.tok + h * cs.head;
-    const uint8_t* ps = (isk ? a.ks : a.vs) + page * ss.page + off * ss.tok + h * ss.head;
+    const unsigned i = rest + u * kReadThreads + threadIdx.x, k = i / per;
+    n[u] = n0 + k;
+    piece[u] = i - k * per;
+    slot[u] = n[u] < a.N ? a.slots[n[u]] : -1;
+  }
+  unsigned codes[U], byte[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const unsigned hh = piece[u] / LPR, c = piece[u] % LPR;
+    const bool isk = a.k && hh < (unsigned)a.Hk;
+    const unsigned h = isk || !a.k ? hh : hh - a.Hk;
     codes[u] = byte[u] = 0;
-    if (there) {
+    if (slot[u] >= 0 && slot[u] < a.entries) {
+      const unsigned page = (unsigned)(slot[u] >> a.page_shift), off = (unsigned)slot[u] & mask;
+      auto entry = [&](const uint8_t* base, const Fp4Strides& s) {
+        return base + ((uint64_t)page * (unsigned)s.page + (uint64_t)off * (unsigned)s.tok + (uint64_t)h * (unsigned)s.head);
+      };
+      const uint8_t* pc = entry(isk ? a.kc : a.vc, isk ? a.kcs : a.vcs);
       if constexpr (V == 8) codes[u] = reinterpret_cast<const unsigned*>(pc)[c];
       else codes[u] = reinterpret_cast<const uint16_t*>(pc)[c];
-      byte[u] = ps[c / (kFp4Block / V)];
+      byte[u] = entry(isk ? a.ks : a.vs, isk ? a.kss : a.vss)[c / (kFp4Block / V)];
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    if (hh[u] >= a.heads) continue;
-    const bool isk = a.k && hh[u] < a.Hk;
-    const int h = isk || !a.k ? hh[u] : hh[u] - a.Hk;
-    E* dst = isk ? static_cast<E*>(a.k) + n * a.k_row + h * D : static_cast<E*>(a.v) + n * a.v_row + h * D;
+    if (n[u] >= a.N) continue;
+    const unsigned hh = piece[u] / LPR, c = piece[u] % LPR;
+    const bool isk = a.k && hh < (unsigned)a.Hk;
+    const unsigned h = isk || !a.k ? hh : hh - a.Hk;
+    E* dst = isk ? static_cast<E*>(a.k) + n[u] * a.k_row + h * D : static_cast<E*>(a.v) + n[u] * a.v_row + h * D;
     u32x4 y;
     if constexpr (V == 8) {
       y = fp4_open8(codes[u], fp4_factor(byte[u]));

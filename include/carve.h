@@ -456,7 +456,7 @@ int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void* q, const 
  * free_count; no other output overlaps anything. */
 typedef struct {
   int32_t S, N;
-  int32_t page_size, width;          /* page_size a power of two; width * page_size <= 2^30 */
+  int32_t page_size, width;          /* page_size a power of two; width * page_size <= 2^30, S * width < 2^31 */
   int64_t table_row;                 /* entries from one request's table row to the next's */
   int64_t capacity;                  /* of free_pages, below 2^31 */
 } carve_assign_config;
