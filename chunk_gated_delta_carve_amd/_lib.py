@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 # CARVE_LIB_PATH may name another build of the same library (the host
 # sanitizer build, build.py --sanitize); by default the in-tree libcarve.so.
@@ -52,6 +53,10 @@ class CarveFp4Config(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("ks_page", "ks_tok", "ks_head", "vs_page", "vs_tok", "vs_head")])
 
 
+# The same as bytes, made in a quarter of the time: the fields of CarvePagedConfig, then those above.
+pack_fp4 = struct.Struct("@13i2f11q6q").pack
+
+
 class CarveAssignConfig(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("S", "N", "page_size", "width")]
                 + [(n, ctypes.c_int64) for n in ("table_row", "capacity")])
@@ -94,7 +99,7 @@ def lib() -> ctypes.CDLL:
         L.carve_paged_append.argtypes = [paged] + [vp] * 14
         L.carve_paged_workspace.argtypes = [paged, bytes_out]
         L.carve_paged_attention.argtypes = [paged] + [vp] * 9 + [size, vp]
-        fp4 = ctypes.POINTER(CarveFp4Config)
+        fp4 = vp                             # a CarveFp4Config by reference, or what pack_fp4 gives
         L.carve_paged_append_fp4.argtypes = [fp4] + [vp] * 16
         L.carve_paged_read_fp4.argtypes = [fp4] + [vp] * 8
         L.carve_paged_workspace_fp4.argtypes = [fp4, bytes_out]

@@ -93,7 +93,7 @@ Plan plan_of(const carve_paged_config* c) {
   const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsLayout<float, 128>::PER_CU : carve::RowsLayout<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsLayout<float, 64>::PER_CU : carve::RowsLayout<carve::bf16, 64>::PER_CU;
-  return plan_attention(c, {c->d == 128 ? wide : slim, 0, 32, 16, 2048});
+  return plan_attention(c, {c->d == 128 ? wide : slim, 0, 0, 32, 16, 2048});
 }
 
 template <typename E, int D>

@@ -24,10 +24,11 @@ constexpr int kWideJoin = 32;          // shares per item from which a workgroup
 struct Choice {
   int per_cu;                // row kernel: workgroups that a CU holds
   int more;                  // and blocks that an item counts for beside its own
+  int whole;                 // and blocks up to which items are dealt undivided
   int rows_short, rows_long, long_keys;
 };
 struct Plan {
-  bool tile;
+  bool tile, whole;
   int waves;                 // tile kernels: of a workgroup
   int64_t tiles, most;       // row kernel: blocks of keys at most, over all items
   int splits, shares;
@@ -58,11 +59,11 @@ inline Plan plan_attention(const carve_paged_config* c, const Choice& ch) {
     p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
   } else {
     // a workgroup per block of keys at most; no item has more blocks than this counts
-    const int64_t blocks = p.tiles * c->Hk * (up(keys, BN) + 1 + ch.more);
-    const int64_t want = (int64_t)kCUs * ch.per_cu;
-    p.most = blocks;
-    p.shares = (int)(blocks < want ? blocks : want);
-    p.rows = p.shares > 1 ? 2 * (int64_t)p.shares * BM : 0;
+    const int64_t items = p.tiles * c->Hk, nb = up(keys, BN) + 1, want = (int64_t)kCUs * ch.per_cu;
+    p.whole = nb - 1 <= ch.whole;
+    p.most = items * (p.whole ? 1 : nb + ch.more);
+    p.shares = (int)(p.most < want ? p.most : want);
+    p.rows = p.shares > 1 && !p.whole ? 2 * (int64_t)p.shares * BM : 0;
   }
   const int64_t cuts = p.rows == 0 ? 0 : p.tile ? p.tiles * c->Hk : p.shares;
   p.bytes = (p.rows * (c->d + 2) + cuts * carve::kCutInts) * 4;

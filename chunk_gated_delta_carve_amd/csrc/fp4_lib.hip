@@ -176,11 +176,16 @@ extern "C" int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* 
 }
 
 namespace {
+// Blocks of 128 keys up to which an item is left to one workgroup: splitting it needs a
+// second launch to join the parts, which takes as long as about six blocks.
+// WHOLE_NUMBERS
+constexpr int kWhole = 8;
+
 Plan plan_of(const carve_paged_config* c) {
   const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsFp4<float, 64>::PER_CU : carve::RowsFp4<carve::bf16, 64>::PER_CU;
-  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, 32, 16, 2048});
+  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, kWhole, 32, 16, 2048});
 }
 
 template <typename E, int D>
@@ -199,7 +204,7 @@ hipError_t dispatch_attention(const carve::Fp4Args& a, const Plan& plan, hipStre
   else
     hipLaunchKernelGGL((carve::paged_rows_fp4_kernel<E, D, false>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess || a.shares == 1 ? e : join_rows<E, D>(a, s);
+  return e != hipSuccess || !a.po ? e : join_rows<E, D>(a, s);
 }
 
 int check_attention(const carve_fp4_config* f) {
@@ -277,10 +282,10 @@ extern "C" int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void
   a.width = c.width; a.pages = c.pages; a.page_shift = shift_of(c.page_size);
   a.window = c.window;
   a.scale = c.scale; a.c = c.scale * carve::kLog2e;
-  a.po = static_cast<float*>(workspace);
+  a.po = need ? static_cast<float*>(workspace) : nullptr;
   a.pml = need ? a.po + plan.rows * c.d : nullptr;
   a.cuts = need ? reinterpret_cast<int*>(a.pml + plan.rows * 2) : nullptr;
-  a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares;
+  a.splits = plan.splits; a.tiles = (int)plan.tiles; a.shares = plan.shares; a.whole = plan.whole;
   a.by_g = carve::Divisor(a.G); a.by_hk = carve::Divisor(a.Hk); a.by_hq = carve::Divisor(a.Hq);
   a.by_shares = carve::Divisor(a.shares);
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {

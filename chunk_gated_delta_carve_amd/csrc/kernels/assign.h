@@ -60,15 +60,23 @@ __device__ __forceinline__ Two scan_two(Two x, Two& all) {
   return Two{sum_to_most(before.a, lane ? ua : 0), sum_to_most(before.b, lane ? ub : 0)};
 }
 
-// Last i in [0, n) with first[i] <= at (first ascends, first[0] <= at).
-template <typename T>
-__device__ __forceinline__ int last_at(const T* first, int n, unsigned at) {
-  int lo = 0;
+// Last i in [0, n) with first[i] <= at, for U numbers at a time (first ascends, first[0] <= at).
+template <int U, typename T>
+__device__ __forceinline__ void last_at(const T* first, int n, const unsigned (&at)[U], int (&lo)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) lo[u] = 0;
   while (n > 1) {
     const int half = n >> 1;
-    if ((unsigned)first[lo + half] <= at) { lo += half; n -= half; } else n = half;
+#pragma unroll
+    for (int u = 0; u < U; ++u) lo[u] = (unsigned)first[lo[u] + half] <= at[u] ? lo[u] + half : lo[u];
+    n -= half;
   }
-  return lo;
+}
+template <typename T>
+__device__ __forceinline__ int last_at(const T* first, int n, unsigned at) {
+  int lo[1];
+  last_at<1>(first, n, {at}, lo);
+  return lo[0];
 }
 
 __device__ __forceinline__ unsigned pages_of(const AssignArgs& a, unsigned tokens) {
@@ -159,21 +167,22 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
     offset[tid] = sum_to_most(tokens, at.b);
     if (s < a.S) a.cu[s] = (int)offset[tid];
     __syncthreads();
-    for (unsigned i0 = tid; i0 < all.a; i0 += kAssignThreads * 4) {
-      int page[4];
-      int64_t to[4];
+    for (unsigned i0 = tid; i0 < all.a; i0 += kAssignThreads * kAssignRun) {
+      unsigned i[kAssignRun];
+      int r[kAssignRun], page[kAssignRun];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {                 // four loads in flight
-        const unsigned i = i0 + u * kAssignThreads, from = sum_to_most(used, i);
-        page[u] = -1;
-        if (i >= all.a) continue;
-        const int r = last_at(first, n, i);
-        to[u] = (s0 + r) * a.table_row + have[r] + (i - first[r]);
-        if (from < top) page[u] = a.free_pages[top - 1 - from];
+      for (int u = 0; u < kAssignRun; ++u) {
+        i[u] = i0 + u * kAssignThreads;
+        i[u] = i[u] < all.a ? i[u] : all.a - 1;     // past the end, the last one again: the same entry and page
+      }
+      last_at<kAssignRun>(first, n, i, r);
+#pragma unroll
+      for (int u = 0; u < kAssignRun; ++u) {
+        const unsigned from = sum_to_most(used, i[u]);
+        page[u] = from < top ? a.free_pages[top - 1 - from] : -1;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + u * kAssignThreads < all.a) a.table[to[u]] = page[u];
+      for (int u = 0; u < kAssignRun; ++u) a.table[(s0 + r[u]) * a.table_row + have[r[u]] + (i[u] - first[r[u]])] = page[u];
     }
     used = sum_to_most(used, all.a);
     tokens = sum_to_most(tokens, all.b);
@@ -210,10 +219,8 @@ __global__ __launch_bounds__(256) void paged_assign_tokens_kernel(AssignArgs a) 
     const int64_t t = (int64_t)blockIdx.x * 1024 + u * 256 + threadIdx.x;
     if (t >= a.N) return;
     if (t >= tokens) { put_token(a, (int)t, 0, 0, 0); continue; }
-    int s, end;
-    if (here) { s = last_at(offset, a.S, (unsigned)t); end = offset[s + 1]; }
-    else { s = last_at(a.cu, a.S, (unsigned)t); end = a.cu[s + 1]; }
-    put_token(a, (int)t, s, end, a.kv_out[s]);
+    const int s = here ? last_at(offset, a.S, (unsigned)t) : last_at(a.cu, a.S, (unsigned)t);
+    put_token(a, (int)t, s, here ? offset[s + 1] : a.cu[s + 1], a.kv_out[s]);
   }
 }
 

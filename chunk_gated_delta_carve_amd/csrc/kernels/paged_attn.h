@@ -62,6 +62,7 @@ struct PagedArgs {
   int N, S, Hq, Hk, G, width, pages, page_shift, window;
   int tiles, splits;                                // tile kernel: tiles, workgroups per tile at most
   int shares;                                       // row kernel: workgroups that the work is dealt to
+  int whole;                                        // row kernel, 4 bits: items are dealt undivided
   float scale, c;                                   // c = scale log2 e
   Divisor by_g, by_hk, by_hq, by_shares;            // by G, Hk, Hq and the most shares
 };
@@ -383,7 +384,7 @@ __device__ __forceinline__ s16x4 read_tr(const char* p) {
 // A sequence's part of the work: `items` times `nb` blocks, each item's from the
 // block of its first key on.
 struct RowsWork {
-  int n0, cnt, pos0, items, nb;
+  int n0, cnt, pos0, items, nb;                     // nb: what an item counts for (its blocks, in most cases)
   __device__ __forceinline__ int blocks() const { return items * nb; }
 };
 template <int MORE>                                 // blocks that an item counts for beside its own
@@ -404,7 +405,7 @@ __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM,
     const int most = (int)(((unsigned)a.window + BM + BN - 3) / BN) + 1;
     w.nb = w.nb < most ? w.nb : most;
   }
-  w.nb += MORE;
+  if constexpr (MORE > 0) w.nb = a.whole ? 1 : w.nb + MORE;
   return w;
 }
 

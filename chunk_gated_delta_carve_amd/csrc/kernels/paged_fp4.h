@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan<kStart>(a, LY::BM, LY::BN);
   int* cut = a.cuts + blockIdx.x * kCutInts;
-  if (threadIdx.x == 0 && a.shares > 1) cut[2] = 0;
+  if (threadIdx.x == 0 && a.po) cut[2] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);            // in blocks of the plan, kStart more per item than it has
   const int end_block = plan.start(blockIdx.x + 1);
@@ -136,14 +136,15 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const int b1 = w.nb - b0 < end_block - at_block ? w.nb : b0 + (end_block - at_block);
   const int last_block = at_block - b0 + w.nb - 1;  // of the item
   at_block += b1 - b0;
-  if (b1 <= kStart) continue;                       // the blocks that stand for the start alone: the next workgroup's
-  const int blk = b0 > kStart ? b0 - kStart : 0, take = b1 - kStart - blk;
-  const bool whole = take == w.nb - kStart;
+  if (b1 <= kStart && !a.whole) continue;           // the blocks that stand for the start alone: the next workgroup's
+  const int blk = b0 > kStart ? b0 - kStart : 0;
+  const bool whole = a.whole || (blk == 0 && b1 == w.nb);
   const int tile = a.by_hk.div(item), h = item - tile * a.Hk;
   const AttnTile x = tile_of_rows(a, s, w.n0, w.cnt, w.pos0, tile * LY::BM, LY::BM);
-  const int first_key = (x.lo / LY::BN + blk) * LY::BN;
+  const int first_key = (x.lo / LY::BN + blk) * LY::BN, take = b1 - kStart - blk;
   const int k0 = __builtin_amdgcn_readfirstlane(first_key > x.lo ? first_key : x.lo);
-  const int k1 = __builtin_amdgcn_readfirstlane((x.hi - first_key) / LY::BN < take ? x.hi : first_key + take * LY::BN);
+  const int k1 = __builtin_amdgcn_readfirstlane(whole || (x.hi - first_key) / LY::BN < take ? x.hi
+                                                                                          : first_key + take * LY::BN);
   const RowOut<E, D> ro{a, h, whole, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
 
   const uint8_t* kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head;

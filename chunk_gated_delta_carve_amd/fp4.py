@@ -24,6 +24,7 @@ from .attention import (_I32, _MOST, _angles, _dense, _first, _flags, _flat, _li
                         _workspace)
 
 _U8 = torch.uint8
+_pack = _lib.pack_fp4
 
 
 def paged_fp4_cache(pages, page_size, heads, d, device="cuda"):
@@ -38,29 +39,32 @@ def paged_fp4_cache(pages, page_size, heads, d, device="cuda"):
                  for n in (d // 2, d // 32) * 2)
 
 
-def _fp4_part(t, name, shape, dev):
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not _U8 or t.device != dev:
-        _like(t, name, _U8, dev)
-    stride = t.stride()
-    if stride[3] != 1:
-        raise ValueError(f"{name}: the bytes of a head must be contiguous")
-    return stride
-
-
 def _fp4_cache(k_cache, k_scale, v_cache, v_scale, Hk, d, dev):
     """(pages, page size, strides of the codes as a paged config has them, strides of the scales)."""
-    shape = k_cache.shape
+    shape, small = k_cache.shape, k_scale.shape
     if len(shape) != 4 or shape[2] != Hk or 2 * shape[3] != d:
         raise ValueError(f"k_cache: expected [pages, page_size, {Hk}, {d // 2}], got {tuple(shape)}")
-    if shape[0] > _MOST or shape[1] > _MOST:
+    pages, page_size = shape[0], shape[1]
+    if pages > _MOST or page_size > _MOST:
         raise ValueError(f"k_cache: sizes past 32 bits: {tuple(shape)}")
-    lead = shape[:3]
-    kc, vc = _fp4_part(k_cache, "k_cache", shape, dev), _fp4_part(v_cache, "v_cache", shape, dev)
-    small = (*lead, d // 32)
-    ks, vs = _fp4_part(k_scale, "k_scale", small, dev), _fp4_part(v_scale, "v_scale", small, dev)
-    return lead[0], lead[1], (*kc[:3], *vc[:3]), (*ks[:3], *vs[:3])
+    want = (pages, page_size, Hk, d // 32)
+    at = dev.index
+    if not (v_cache.shape == shape and small == want and v_scale.shape == small
+            and k_cache.dtype is _U8 and k_scale.dtype is _U8 and v_cache.dtype is _U8 and v_scale.dtype is _U8
+            and k_cache.get_device() == at and k_scale.get_device() == at and v_cache.get_device() == at
+            and v_scale.get_device() == at):
+        for t, name, s in ((k_cache, "k_cache", shape), (k_scale, "k_scale", want), (v_cache, "v_cache", shape),
+                           (v_scale, "v_scale", want)):
+            if t.shape != s:
+                raise ValueError(f"{name}: expected shape {tuple(s)}, got {tuple(t.shape)}")
+            _like(t, name, _U8, dev)
+    kp, kt, kh, k1 = k_cache.stride()
+    sp, st, sh, s1 = k_scale.stride()
+    vp, vt, vh, v1 = v_cache.stride()
+    tp, tt, th, t1 = v_scale.stride()
+    if k1 != 1 or s1 != 1 or v1 != 1 or t1 != 1:
+        raise ValueError("the bytes of a head must be contiguous in codes and scales")
+    return pages, page_size, (kp, kt, kh, vp, vt, vh), (sp, st, sh, tp, tt, th)
 
 
 def _parts(*cache):
@@ -96,10 +100,8 @@ def paged_append_fp4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, kv_l
             o_row, po = _rows(q_out, "q_out", sq, dt, dev), q_out.data_ptr()
         elif q_weight is not None or q_out is not None:
             raise ValueError("q_weight and q_out belong to q")
-        c = _lib.CarveFp4Config(
-            _lib.CarvePagedConfig(N, S, Hq, Hk, d, page_size, pages, width, rot, table_len, 0, _DTYPES[dt], flags, eps,
-                                  1.0, q_row, _rows(k, "k", sk, dt, dev), _rows(v, "v", sk, dt, dev), o_row, table_row,
-                                  *codes), *scales)
+        c = _pack(N, S, Hq, Hk, d, page_size, pages, width, rot, table_len, 0, _DTYPES[dt], flags, eps, 1.0, q_row,
+                  _rows(k, "k", sk, dt, dev), _rows(v, "v", sk, dt, dev), o_row, table_row, *codes, *scales)
         code = _lib.lib().carve_paged_append_fp4(c, k.data_ptr(), v.data_ptr(), pq, wq, wk, pc, ps, cu, lens, table,
                                                  *_parts(k_cache, k_scale, v_cache, v_scale), po,
                                                  torch._C._cuda_getCurrentRawStream(dev.index))
@@ -129,12 +131,8 @@ def paged_read_fp4(k_cache, k_scale, v_cache, v_scale, slots, dtype=torch.bfloat
     with _on(dev, stream):
         k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
         v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-        c = _lib.CarveFp4Config()
-        p = c.paged
-        p.N, p.Hk, p.d, p.page_size, p.pages, p.dtype = N, Hk, d, page_size, pages, _DTYPES[dtype]
-        p.k_row, p.v_row = _rows(k_out, "k_out", shape, dtype, dev), _rows(v_out, "v_out", shape, dtype, dev)
-        p.kc_page, p.kc_tok, p.kc_head, p.vc_page, p.vc_tok, p.vc_head = codes
-        c.ks_page, c.ks_tok, c.ks_head, c.vs_page, c.vs_tok, c.vs_head = scales
+        c = _pack(N, 0, 0, Hk, d, page_size, pages, 0, 0, 0, 0, _DTYPES[dtype], 0, 0.0, 0.0, 0,
+                  _rows(k_out, "k_out", shape, dtype, dev), _rows(v_out, "v_out", shape, dtype, dev), 0, 0, *codes, *scales)
         code = _lib.lib().carve_paged_read_fp4(c, *_parts(k_cache, k_scale, v_cache, v_scale), at, k_out.data_ptr(),
                                                v_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
     if code:
@@ -158,10 +156,9 @@ def paged_attention_fp4(q, k_cache, k_scale, v_cache, v_scale, block_table, kv_l
     lse = pl = None
     with _on(dev, stream):
         out = _dense(q) if out is None else out
-        c = _lib.CarveFp4Config(
-            _lib.CarvePagedConfig(N, S, Hq, Hk, d, page_size, pages, width, 0, 0, _window(window), _DTYPES[dt], step,
-                                  0.0, d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0,
-                                  _rows(out, "out", sq, dt, dev), table_row, *codes), *scales)
+        c = _pack(N, S, Hq, Hk, d, page_size, pages, width, 0, 0, _window(window), _DTYPES[dt], step, 0.0,
+                  d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0, _rows(out, "out", sq, dt, dev),
+                  table_row, *codes, *scales)
         if return_lse:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
             pl = lse.data_ptr()
@@ -184,14 +181,9 @@ def paged_fp4_workspace_bytes(N, S, Hq, Hk, d, page_size, width, dtype=torch.bfl
     for name, n in (("N", N), ("S", S), ("Hq", Hq), ("Hk", Hk), ("d", d), ("page_size", page_size), ("width", width)):
         if not 0 <= n <= _MOST:
             raise ValueError(f"{name}: expected a size of 32 bits, got {n}")
-    c = _lib.CarveFp4Config()
-    p = c.paged
-    p.N, p.S, p.Hq, p.Hk, p.d, p.page_size, p.pages, p.width = N, S, Hq, Hk, d, page_size, 1, width
-    p.window, p.dtype, p.scale = _window(window), _DTYPES[dtype], 1.0
-    p.flags = _lib.CARVE_PAGED_STEP if step else 0
-    p.table_row = width
-    p.kc_page = p.kc_tok = p.kc_head = p.vc_page = p.vc_tok = p.vc_head = d // 2
-    c.ks_page = c.ks_tok = c.ks_head = c.vs_page = c.vs_tok = c.vs_head = d // 32
+    half, small = d // 2, d // 32
+    c = _pack(N, S, Hq, Hk, d, page_size, 1, width, 0, 0, _window(window), _DTYPES[dtype],
+              _lib.CARVE_PAGED_STEP if step else 0, 0.0, 1.0, 0, 0, 0, 0, width, *(half,) * 6, *(small,) * 6)
     need = ctypes.c_int64()
     _lib.check(_lib.lib().carve_paged_workspace_fp4(c, need))
     return need.value
@@ -232,10 +224,11 @@ def paged_assign(block_table, kv_lens, new_lens, free_pages, free_count, page_si
             _flat(done, "done", (S,), _I32, dev), block_table.data_ptr(),
             _flat(free_pages, "free_pages", free_pages.shape, _I32, dev), _flat(free_count, "free_count", (2,), _I32, dev)]
     with _on(dev, stream):
-        kv_lens_out = torch.empty_like(kv_lens) if kv_lens_out is None else kv_lens_out
-        free_count_out = torch.empty_like(free_count) if free_count_out is None else free_count_out
-        cu = torch.empty(S + 1, dtype=_I32, device=dev)
-        positions = torch.empty(tokens, dtype=_I32, device=dev)
+        # one allocation for what has 32 bits
+        cu, positions, lens, count = torch.empty(2 * S + tokens + 3, dtype=_I32, device=dev).split_with_sizes(
+            (S + 1, tokens, S, 2))
+        kv_lens_out = lens if kv_lens_out is None else kv_lens_out
+        free_count_out = count if free_count_out is None else free_count_out
         slots = torch.empty(tokens, dtype=torch.int64, device=dev)
         c = _lib.CarveAssignConfig(S, tokens, page_size, width, row if S > 1 else width, free_pages.numel())
         code = _lib.lib().carve_paged_assign(
