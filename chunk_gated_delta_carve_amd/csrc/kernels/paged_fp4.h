@@ -127,6 +127,16 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   int s = in * plan.run;
   int seq_block = __builtin_amdgcn_readlane(plan.before, in);
   RowsWork w = plan.work<kStart>(a, s, LY::BM, LY::BN);
+  // Strides as registers of their own: the compiler keeps kernel arguments in the groups it
+  // loads them in, and parks whole groups in vector registers for want of scalar ones.
+  unsigned kpage = a.kc_page, ktok = a.kc_tok, vpage = a.vc_page, vtok = a.vc_tok;
+  unsigned kspage = a.k.page, kstok = a.k.tok, vspage = a.v.page, vstok = a.v.tok, pages = a.pages, shift = a.page_shift;
+  asm volatile("" : "+s"(kpage), "+s"(ktok), "+s"(vpage), "+s"(vtok), "+s"(kspage), "+s"(kstok), "+s"(vspage),
+               "+s"(vstok), "+s"(pages), "+s"(shift));
+  const unsigned mask = (1u << shift) - 1;
+  const unsigned gc = g * (D / 8), gs = g * (D / 4) / kFp4Block;   // the lane's part of an entry
+  // a lane's offset in a run of 16 keys
+  const unsigned k_off = c * ktok + gc, ks_off = c * kstok + gs, v_off = c * vtok + gc, vs_off = c * vstok + gs;
   while (at_block < end_block) {
   while (at_block >= seq_block + w.blocks()) {
     seq_block += w.blocks();
@@ -151,7 +161,6 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const uint8_t* vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head;
   const uint8_t* ksb = a.ks + h * a.k.head;
   const uint8_t* vsb = a.vs + h * a.v.head;
-  const int pmask = (1 << a.page_shift) - 1;
   char* vl = lds + wave * KT * LY::VLD;
 
   const int* trow = a.table + s * a.table_row;
@@ -160,23 +169,24 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   Codes kr[2], vr[2];
   unsigned kf[2], vf[2];                            // scales
   unsigned okn = 0;                                 // which of the 32 keys exist (bit = key)
-  const unsigned gc = g * (D / 8), gs = g * (D / 4) / kFp4Block;
   int ids = 0, left = 0;                            // WIDE: page of a lane's run, iterations until the next lookup
   int id[2];                                        // else: pages of the lane's keys, looked up a block ahead, since
                                                     // looking at them sooner would wait for the loads under way
   auto lookup = [&](int j) {
     if constexpr (WIDE) {
       const int mine = j + (lane >> 1) * STEP + 16 * (lane & 1);
-      ids = trow[(mine < k1 ? mine : k1 - 1) >> a.page_shift];
+      ids = trow[(mine < k1 ? mine : k1 - 1) >> shift];
       left = 32;
     } else {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int mine = j + 16 * b + c;
-        id[b] = trow[(mine < k1 ? mine : k1 - 1) >> a.page_shift];
+        id[b] = trow[(mine < k1 ? mine : k1 - 1) >> shift];
       }
     }
   };
+  // No branch between a load and the block's end: a scale would be widened behind it, and
+  // waited for.
   auto fetch = [&](int j) {
     if constexpr (WIDE) {
       if (left == 0) lookup(j);
@@ -184,34 +194,36 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
       okn = 0;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int page = __builtin_amdgcn_readlane(ids, at_id + b), first = j + 16 * b;
-        const bool there = (unsigned)page < (unsigned)a.pages;
-        const int lo16 = k0 - first > 0 ? k0 - first : 0, hi16 = k1 - first < 16 ? k1 - first : 16;
-        if (there && hi16 > lo16) okn |= ((1u << hi16) - (1u << lo16)) << (16 * b);
-        const unsigned pg = there ? page : 0, off = first & pmask;
-        auto from = [&](const uint8_t* base, int64_t page_bytes, int64_t tok, unsigned part) {
-          const uint8_t* run = base + ((uint64_t)pg * (unsigned)page_bytes + (uint64_t)off * (unsigned)tok);
-          return run + ((unsigned)c * (unsigned)tok + part);
+        const unsigned page = __builtin_amdgcn_readlane(ids, at_id + b);
+        const int first = j + 16 * b;
+        const int from = k0 - first < 0 ? 0 : k0 - first < 16 ? k0 - first : 16;
+        const int to = k1 - first < from ? from : k1 - first < 16 ? k1 - first : 16;
+        okn |= (page < pages ? (1u << to) - (1u << from) : 0u) << (16 * b);
+        const unsigned pg = page < pages ? page : 0, off = first & mask;
+        // a scalar base and 32 bits of a lane's own, which has to be seen here for the load to take them so
+        auto run = [&](const uint8_t* base, unsigned page_bytes, unsigned tok_bytes, unsigned mine) {
+          asm volatile("" : "+v"(mine));
+          return base + ((uint64_t)pg * page_bytes + (uint64_t)off * tok_bytes) + mine;
         };
-        kr[b] = *reinterpret_cast<const Codes*>(from(kb, a.kc_page, a.kc_tok, gc));
-        kf[b] = *from(ksb, a.k.page, a.k.tok, gs);
-        vr[b] = *reinterpret_cast<const Codes*>(from(vb, a.vc_page, a.vc_tok, gc));
-        vf[b] = *from(vsb, a.v.page, a.v.tok, gs);
+        kr[b] = *reinterpret_cast<const Codes*>(run(kb, kpage, ktok, k_off));
+        kf[b] = *run(ksb, kspage, kstok, ks_off);
+        vr[b] = *reinterpret_cast<const Codes*>(run(vb, vpage, vtok, v_off));
+        vf[b] = *run(vsb, vspage, vstok, vs_off);
       }
     } else {
       bool ok[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int mine = j + 16 * b + c;
-        ok[b] = mine >= k0 && mine < k1 && (unsigned)id[b] < (unsigned)a.pages;
-        const unsigned pg = ok[b] ? id[b] : 0, off = mine & pmask;
-        auto from = [&](const uint8_t* base, int64_t page_bytes, int64_t tok, unsigned part) {
-          return base + ((uint64_t)pg * (unsigned)page_bytes + (uint64_t)off * (unsigned)tok + part);
+        ok[b] = mine >= k0 && mine < k1 && (unsigned)id[b] < pages;
+        const unsigned pg = ok[b] ? id[b] : 0, off = mine & mask;
+        auto key = [&](const uint8_t* base, unsigned page_bytes, unsigned tok_bytes, unsigned part) {
+          return base + ((uint64_t)pg * page_bytes + (uint64_t)off * tok_bytes + part);
         };
-        kr[b] = *reinterpret_cast<const Codes*>(from(kb, a.kc_page, a.kc_tok, gc));
-        kf[b] = *from(ksb, a.k.page, a.k.tok, gs);
-        vr[b] = *reinterpret_cast<const Codes*>(from(vb, a.vc_page, a.vc_tok, gc));
-        vf[b] = *from(vsb, a.v.page, a.v.tok, gs);
+        kr[b] = *reinterpret_cast<const Codes*>(key(kb, kpage, ktok, gc));
+        kf[b] = *key(ksb, kspage, kstok, gs);
+        vr[b] = *reinterpret_cast<const Codes*>(key(vb, vpage, vtok, gc));
+        vf[b] = *key(vsb, vspage, vstok, gs);
       }
       okn = (unsigned)(__ballot(ok[0]) & 0xffffu) | (unsigned)(__ballot(ok[1]) & 0xffffu) << 16;
       lookup(j + STEP);
@@ -248,24 +260,25 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
     const unsigned ok = okn;
     f32x4 sc[2] = {zero4(), zero4()};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const float f = fp4_factor(kf[b]);
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const u32x4 k = fp4_open8(kr[b][i], f);
+      for (int b = 0; b < 2; ++b) {
+        const u32x4 k = fp4_open8(kr[b][i], fp4_factor(kf[b]));
 #pragma unroll
         for (int u = 0; u < NQ; ++u) sc[b] = mma_bits(k, q[i][u], sc[b]);
       }
-    }
     // values to LDS; rows that do not exist as zeros
+    if (ok != 0xffffffffu) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bool z = ok != 0xffffffffu && !((ok >> (16 * b + c)) & 1u);
-      const float f = fp4_factor(z ? 127u : vf[b]);
+      for (int b = 0; b < 2; ++b)
+        if (!((ok >> (16 * b + c)) & 1u)) { vr[b] = Codes(0u); vf[b] = 127; }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        *reinterpret_cast<u32x4*>(vl + (16 * b + c) * LY::VLD + g * (D / 2) + 16 * i) = fp4_open8(z ? 0u : vr[b][i], f);
-    }
+        *reinterpret_cast<u32x4*>(vl + (16 * b + c) * LY::VLD + g * (D / 2) + 16 * i) =
+            fp4_open8(vr[b][i], fp4_factor(vf[b]));
     if (j0 + STEP < k1) fetch(j0 + STEP);
     // lane: row c, keys 16 b + 4 g + i
     if (ok != 0xffffffffu || j0 + KT - 1 > p_min || j0 < lo_max) {
@@ -309,19 +322,28 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
       bf16x8 hi, rest;
 #pragma unroll
       for (int i = 0; i < 8; ++i) hi[i] = (bf16)e[i];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) rest[i] = (bf16)(e[i] - (float)hi[i]);
       pw[0] = __builtin_bit_cast(u32x4, hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rest[2 * i] = (bf16)(e[2 * i] - __uint_as_float(pw[0][i] << 16));
+        rest[2 * i + 1] = (bf16)(e[2 * i + 1] - __uint_as_float(pw[0][i] & 0xffff0000u));
+      }
       pw[1] = __builtin_bit_cast(u32x4, rest);
     }
     const char* src = vl + (4 * g + (lane & 15) / 4) * LY::VLD + (lane & 3) * 8;
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) {
-      const u32x2 v0 = __builtin_bit_cast(u32x2, read_tr(src + 32 * d));
-      const u32x2 v1 = __builtin_bit_cast(u32x2, read_tr(src + 32 * d + 16 * LY::VLD));
-      const u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
+    for (int d = 0; d < D / 16; d += 2) {           // two at a time: a product does not wait for the one before it
+      u32x4 v[2];
 #pragma unroll
-      for (int u = 0; u < LY::NP; ++u) o[d] = mma_bits(v, pw[u], o[d]);
+      for (int t = 0; t < 2; ++t) {
+        const u32x2 v0 = __builtin_bit_cast(u32x2, read_tr(src + 32 * (d + t)));
+        const u32x2 v1 = __builtin_bit_cast(u32x2, read_tr(src + 32 * (d + t) + 16 * LY::VLD));
+        v[t] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+      }
+#pragma unroll
+      for (int u = 0; u < LY::NP; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) o[d + t] = mma_bits(v[t], pw[u], o[d + t]);
     }
   }
 
