@@ -53,8 +53,9 @@ class CarveFp4Config(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("ks_page", "ks_tok", "ks_head", "vs_page", "vs_tok", "vs_head")])
 
 
-# The same as bytes, made in a quarter of the time: the fields of CarvePagedConfig, then those above.
+# The same as bytes, made in a quarter of the time: the fields of CarvePagedConfig, then those above. And CarveAssignConfig.
 pack_fp4 = struct.Struct("@13i2f11q6q").pack
+pack_assign = struct.Struct("@4i2q").pack
 
 
 class CarveAssignConfig(ctypes.Structure):
@@ -104,7 +105,7 @@ def lib() -> ctypes.CDLL:
         L.carve_paged_read_fp4.argtypes = [fp4] + [vp] * 8
         L.carve_paged_workspace_fp4.argtypes = [fp4, bytes_out]
         L.carve_paged_attention_fp4.argtypes = [fp4] + [vp] * 11 + [size, vp]
-        L.carve_paged_assign.argtypes = [ctypes.POINTER(CarveAssignConfig)] + [vp] * 12
+        L.carve_paged_assign.argtypes = [vp] * 13
         for name in EXPORTED[5:-1]:
             getattr(L, name).restype = ctypes.c_int
         L.carve_error_string.argtypes = [ctypes.c_int]

@@ -101,13 +101,9 @@ __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) 
   constexpr int V = Piece<E>::V, LPR = D / V;
   const int n = blockIdx.x * 4 + wave_id();
   if (n >= a.N) return;
-  const TokenPlace at = token_place(a, n);
-  if (at.pos == kNoToken) return;                   // behind the last sequence
+  // the rows leave before the token's place is looked for, three loads that wait for each other
   const Turn<E, D> t(a.rot, a.interleaved);
   const int heads = a.Hq + 2 * a.Hk;
-  float cs[V], sn[V];
-  t.angles(a.cos, a.sin, a.rot, a.table_len, at.pos, false, cs, sn);
-  const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
   u32x4 raw[U];
   int hh[U];
 #pragma unroll
@@ -119,6 +115,11 @@ __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) 
                                      : static_cast<const E*>(a.v) + n * a.v_row + (h - a.Hq - a.Hk) * D;
     raw[u] = *reinterpret_cast<const u32x4*>(src + t.c * V);
   }
+  const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
+  const TokenPlace at = token_place(a, n);
+  if (at.pos == kNoToken) return;                   // behind the last sequence
+  float cs[V], sn[V];
+  t.angles(a.cos, a.sin, a.rot, a.table_len, at.pos, false, cs, sn);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = hh[u];

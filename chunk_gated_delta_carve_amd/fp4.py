@@ -14,7 +14,6 @@ free.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -123,16 +122,22 @@ def paged_read_fp4(k_cache, k_scale, v_cache, v_scale, slots, dtype=torch.bfloat
     Hk, d = k_cache.shape[2], 2 * k_cache.shape[3]
     pages, page_size, codes, scales = _fp4_cache(k_cache, k_scale, v_cache, v_scale, Hk, d, dev)
     lead = slots.shape
-    N = math.prod(lead)
+    N = slots.numel()
     if N > _MOST or Hk > _MOST:
         raise ValueError(f"sizes past 32 bits: {N} slots of {Hk} heads")
     at = _flat(slots, "slots", lead, torch.int64, dev)
-    shape = torch.Size((*lead, Hk, d))
+    shape = (*lead, Hk, d)
+    k_row = v_row = Hk * d
     with _on(dev, stream):
-        k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-        c = _pack(N, 0, 0, Hk, d, page_size, pages, 0, 0, 0, 0, _DTYPES[dtype], 0, 0.0, 0.0, 0,
-                  _rows(k_out, "k_out", shape, dtype, dev), _rows(v_out, "v_out", shape, dtype, dev), 0, 0, *codes, *scales)
+        if k_out is None and v_out is None:
+            k_out, v_out = torch.empty((2, *shape), dtype=dtype, device=dev).unbind()    # one allocation
+        else:
+            shape = torch.Size(shape)
+            k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
+            k_row, v_row = _rows(k_out, "k_out", shape, dtype, dev), _rows(v_out, "v_out", shape, dtype, dev)
+        c = _pack(N, 0, 0, Hk, d, page_size, pages, 0, 0, 0, 0, _DTYPES[dtype], 0, 0.0, 0.0, 0, k_row, v_row, 0, 0,
+                  *codes, *scales)
         code = _lib.lib().carve_paged_read_fp4(c, *_parts(k_cache, k_scale, v_cache, v_scale), at, k_out.data_ptr(),
                                                v_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
     if code:
@@ -230,7 +235,7 @@ def paged_assign(block_table, kv_lens, new_lens, free_pages, free_count, page_si
         kv_lens_out = lens if kv_lens_out is None else kv_lens_out
         free_count_out = count if free_count_out is None else free_count_out
         slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-        c = _lib.CarveAssignConfig(S, tokens, page_size, width, row if S > 1 else width, free_pages.numel())
+        c = _lib.pack_assign(S, tokens, page_size, width, row if S > 1 else width, free_pages.numel())
         code = _lib.lib().carve_paged_assign(
             c, *args, _flat(kv_lens_out, "kv_lens_out", (S,), _I32, dev), cu.data_ptr(), positions.data_ptr(),
             slots.data_ptr(), _flat(free_count_out, "free_count_out", (2,), _I32, dev),
