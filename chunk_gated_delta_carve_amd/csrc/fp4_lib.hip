@@ -117,11 +117,18 @@ extern "C" int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k
   f.k = strides(parts.ks); f.v = strides(parts.vs);
   const TokenWaves w = token_waves(c.N, (int64_t)c.Hq + 2 * (int64_t)c.Hk, c.d, c.dtype);
   if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
+  // several tokens to a wave where there are more waves than the GPU holds at once, eight pieces to a lane at most
+  const bool run = (int64_t)c.N * w.per_token > kFewWaves;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
     return by_pieces(w.per_lane, [&](auto u) {
-      hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, decltype(u)::value>),
-                         dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                         f);
+      constexpr int U = decltype(u)::value, TOK = U <= 2 ? 4 : 2;
+      const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+      if (run)
+        hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, U, TOK>),
+                           dim3((unsigned)up(c.N, 4 * TOK), w.per_token), dim3(256), 0, s, f);
+      else
+        hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, U, 1>),
+                           dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, s, f);
       return hipGetLastError();
     });
   });

@@ -10,6 +10,7 @@
 // k - 1. It is kept in [-125, 125], so that every value is a normal number or 0,
 // and finite. gfx950 converts two values an instruction, either way.
 #pragma once
+#include "assign.h"
 #include "common.h"
 #include "rope.h"
 
@@ -51,19 +52,28 @@ __device__ __forceinline__ unsigned block_max(unsigned x) {
 template <typename E>
 __device__ __forceinline__ unsigned fp4_close(u32x4 raw, unsigned& byte) {
   constexpr int V = Piece<E>::V;
-  float x[V];
-  Piece<E>::open(raw, x);
-  unsigned top = 0;
+  unsigned top = 0, c = 0;
+  if constexpr (V == 8) {                           // bf16: two maxima at a time, and converted as they are
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    auto size = [](unsigned x) { return __builtin_bit_cast(u16x2, x & 0x7fff7fffu); };
+    const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(size(raw[0]), size(raw[1])),
+                                              __builtin_elementwise_max(size(raw[2]), size(raw[3])));
+    top = (unsigned)(m[0] > m[1] ? m[0] : m[1]) << 16;
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) top = dpp_max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < V; ++i) top = dpp_max(top, raw[i] & 0x7fffffffu);
+  }
   byte = fp4_scale(block_max<kFp4Block / V>(top));
   const float s = fp4_factor(byte);
-  unsigned c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], s, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
   if constexpr (V == 8) {
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], s, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], s, 3);
+    auto two = [](unsigned x) { return __builtin_bit_cast(bf16x2, x); };
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(raw[0]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(raw[1]), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(raw[2]), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, two(raw[3]), s, 3);
+  } else {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(raw[0]), __uint_as_float(raw[1]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(raw[2]), __uint_as_float(raw[3]), s, 1);
   }
   return byte == kFp4Bad ? 0u : c;
 }
@@ -92,52 +102,100 @@ struct Fp4AppendArgs {
   Fp4Strides k, v;                     // of the scales
 };
 
-// As paged_append_kernel: one wave per token and 64 U pieces of its rows. A block's
-// lanes (4, or 8 in fp32) find its largest value by lane exchanges; each stores its
-// own codes, the first the scale.
-template <typename E, int D, int U>
+// As token_place, every lane for a token of its own.
+__device__ __forceinline__ TokenPlace lane_place(const AppendArgs& a, int n) {
+  TokenPlace x{kNoToken, -1, 0};
+  if (n >= a.N || a.S == 0) return x;
+  int s = n, i = 0, cnt = 1;
+  if (a.cu) {
+    s = last_at(a.cu, a.S, (unsigned)n);
+    const int c0 = a.cu[s], c1 = a.cu[s + 1];
+    if (n < c0 || n >= c1) return x;                // behind the last sequence
+    i = n - c0;
+    cnt = c1 - c0;
+  } else if (s >= a.S) {
+    return x;
+  }
+  x.pos = (int64_t)a.kv_lens[s] - cnt + i;
+  const int64_t slot = x.pos >> a.page_shift;
+  if (x.pos >= 0 && slot < a.width) x.page = a.table[s * a.table_row + slot];
+  if (x.page >= a.pages) x.page = -1;
+  x.off = x.pos & ((1 << a.page_shift) - 1);
+  return x;
+}
+
+// A wave has 64 U pieces of each of TOK neighbouring tokens (q's, k's and v's heads): all
+// of the rows are under way while lanes look for the tokens' places, three loads that wait
+// for each other. A block's lanes (4, or 8 in fp32) find its largest value by lane
+// exchanges; each stores its own codes, the first the scale. Bound by its addresses at
+// first: 21.4k tokens of 8 heads of 128 in bf16 (55 MB read and written) took 28 us with a
+// 64-bit product for every stride and piece, and take 17 with a token's part as scalars
+// and a head's found once for all tokens.
+template <typename E, int D, int U, int TOK>
 __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) {
   const AppendArgs& a = f.a;
   constexpr int V = Piece<E>::V, LPR = D / V;
-  const int n = blockIdx.x * 4 + wave_id();
-  if (n >= a.N) return;
-  // the rows leave before the token's place is looked for, three loads that wait for each other
+  const int n0 = (blockIdx.x * 4 + wave_id()) * TOK;
+  if (n0 >= a.N) return;
   const Turn<E, D> t(a.rot, a.interleaved);
   const int heads = a.Hq + 2 * a.Hk;
-  u32x4 raw[U];
+  u32x4 raw[TOK][U];
   int hh[U];
+  // a head's place within an entry's page and token, found once for all tokens
+  uint64_t code_at[U], scale_at[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     hh[u] = ((blockIdx.y * U + u) * 64 + lane_id()) / LPR;
     const int h = hh[u] < heads ? hh[u] : heads - 1;
-    const E* src = h < a.Hq ? static_cast<const E*>(a.q) + n * a.q_row + h * D
-                   : h < a.Hq + a.Hk ? static_cast<const E*>(a.k) + n * a.k_row + (h - a.Hq) * D
-                                     : static_cast<const E*>(a.v) + n * a.v_row + (h - a.Hq - a.Hk) * D;
-    raw[u] = *reinterpret_cast<const u32x4*>(src + t.c * V);
+    const bool isq = h < a.Hq, isk = h < a.Hq + a.Hk;
+    const E* src = isq ? static_cast<const E*>(a.q) : static_cast<const E*>(isk ? a.k : a.v);
+    const unsigned hk = isq ? h : h - a.Hq - (isk ? 0 : a.Hk), row = isq ? a.q_row : isk ? a.k_row : a.v_row;
+    src += hk * D + t.c * V;
+#pragma unroll
+    for (int k = 0; k < TOK; ++k) {
+      const unsigned n = n0 + k < a.N ? n0 + k : a.N - 1;
+      raw[k][u] = *reinterpret_cast<const u32x4*>(src + (uint64_t)n * row);
+    }
+    code_at[u] = (uint64_t)hk * (unsigned)(isk ? a.kc_head : a.vc_head) + t.c * (V / 2);
+    scale_at[u] = (uint64_t)hk * (unsigned)(isk ? f.k.head : f.v.head) + t.c / (kFp4Block / V);
   }
   const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
-  const TokenPlace at = token_place(a, n);
-  if (at.pos == kNoToken) return;                   // behind the last sequence
-  float cs[V], sn[V];
-  t.angles(a.cos, a.sin, a.rot, a.table_len, at.pos, false, cs, sn);
+  const TokenPlace mine = lane_place(a, n0 + lane_id() % TOK);
+  const bool turns = a.rot > 0 || a.norm;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = hh[u];
-    const u32x4 y = norm_rope_piece<E, D>(raw[u], t, h < a.Hq ? wq : wk, cs, sn, a.norm, a.eps);
-    const bool isk = h < a.Hq + a.Hk;
-    unsigned byte;
-    const unsigned codes = fp4_close<E>(isk ? y : raw[u], byte);
-    if (h < a.Hq) {
-      *reinterpret_cast<u32x4*>(static_cast<E*>(a.qo) + n * a.qo_row + h * D + t.c * V) = y;
-    } else if (h < heads && at.page >= 0) {
-      const int hk = h - a.Hq - (isk ? 0 : a.Hk);
-      uint8_t* c = isk ? static_cast<uint8_t*>(a.kc) + at.page * a.kc_page + at.off * a.kc_tok + hk * a.kc_head
-                       : static_cast<uint8_t*>(a.vc) + at.page * a.vc_page + at.off * a.vc_tok + hk * a.vc_head;
-      uint8_t* s = isk ? f.ks + at.page * f.k.page + at.off * f.k.tok + hk * f.k.head
-                       : f.vs + at.page * f.v.page + at.off * f.v.tok + hk * f.v.head;
-      if constexpr (V == 8) reinterpret_cast<unsigned*>(c)[t.c] = codes;
-      else reinterpret_cast<uint16_t*>(c)[t.c] = (uint16_t)codes;
-      if (t.c % (kFp4Block / V) == 0) s[t.c / (kFp4Block / V)] = (uint8_t)byte;
+  for (int k = 0; k < TOK; ++k) {
+    const int64_t n = n0 + k;
+    // the token's place is the wave's: scalars
+    const int pos_hi = __builtin_amdgcn_readlane((int)(mine.pos >> 32), k);
+    const int64_t pos = (int64_t)pos_hi << 32 | (unsigned)__builtin_amdgcn_readlane((int)mine.pos, k);
+    if (pos == kNoToken) continue;                  // behind the last sequence
+    const int page = __builtin_amdgcn_readlane((int)mine.page, k);
+    const unsigned off = __builtin_amdgcn_readlane((int)mine.off, k), pg = page >= 0 ? page : 0;
+    auto token = [&](void* base, int64_t page_bytes, int64_t tok_bytes) {
+      return static_cast<uint8_t*>(base) + (uint64_t)pg * (unsigned)page_bytes + (uint64_t)off * (unsigned)tok_bytes;
+    };
+    uint8_t *kc = token(a.kc, a.kc_page, a.kc_tok), *vc = token(a.vc, a.vc_page, a.vc_tok);
+    uint8_t *ks = token(f.ks, f.k.page, f.k.tok), *vs = token(f.vs, f.v.page, f.v.tok);
+    float cs[V], sn[V];
+    t.angles(a.cos, a.sin, a.rot, a.table_len, pos, false, cs, sn);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hh[u];
+      const bool isq = h < a.Hq, isk = h < a.Hq + a.Hk;
+      u32x4 y = raw[k][u];
+      if (turns && __ballot(isk)) {
+        const u32x4 z = norm_rope_piece<E, D>(y, t, isq ? wq : wk, cs, sn, a.norm, a.eps);
+        y = isk ? z : y;
+      }
+      if (isq) *reinterpret_cast<u32x4*>(static_cast<E*>(a.qo) + n * a.qo_row + h * D + t.c * V) = y;
+      if (page < 0 || !__ballot(!isq)) continue;
+      unsigned byte;
+      const unsigned codes = fp4_close<E>(y, byte);
+      if (isq || h >= heads) continue;
+      uint8_t *c = (isk ? kc : vc) + code_at[u], *s = (isk ? ks : vs) + scale_at[u];
+      if constexpr (V == 8) *reinterpret_cast<unsigned*>(c) = codes;
+      else *reinterpret_cast<uint16_t*>(c) = (uint16_t)codes;
+      if (t.c % (kFp4Block / V) == 0) *s = (uint8_t)byte;
     }
   }
 }
@@ -154,7 +212,8 @@ struct Fp4ReadArgs {
 // A piece is 16 bytes of output; the pieces of all slots and heads (a slot's k heads,
 // then its v heads) are laid end to end over the workgroups, kReadPieces of them in
 // flight to a lane, and the tokens of a workgroup's use the lines they read together.
-// Bound by memory: READ_NUMBERS
+// Bound by memory: 228k slots of 2 heads of 128 (307 MB) 60 us, 5.1 TB/s; a wave to a slot,
+// which leaves one load under way, took 105.
 constexpr int kReadPieces = 4, kReadThreads = 256;
 template <typename E, int D>
 __global__ __launch_bounds__(kReadThreads) void paged_read_fp4_kernel(Fp4ReadArgs a) {
