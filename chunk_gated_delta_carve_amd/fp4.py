@@ -14,6 +14,7 @@ free.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -23,7 +24,13 @@ from .attention import (_I32, _MOST, _angles, _dense, _first, _flags, _flat, _li
                         _workspace)
 
 _U8 = torch.uint8
-_pack = _lib.pack_fp4
+
+
+def _pack(*values):
+    try:
+        return _lib.pack_fp4(*values)
+    except struct.error as e:
+        raise ValueError(f"a size past 32 bits: {e}") from None
 
 
 def paged_fp4_cache(pages, page_size, heads, d, device="cuda"):
@@ -66,10 +73,6 @@ def _fp4_cache(k_cache, k_scale, v_cache, v_scale, Hk, d, dev):
     return pages, page_size, (kp, kt, kh, vp, vt, vh), (sp, st, sh, tp, tt, th)
 
 
-def _parts(*cache):
-    return [t.data_ptr() for t in cache]
-
-
 def paged_append_fp4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, kv_lens, cu_seqlens=None, cos=None,
                      sin=None, q=None, q_weight=None, k_weight=None, norm=False, eps=1e-6, interleaved=False, q_out=None,
                      stream=None):
@@ -102,8 +105,8 @@ def paged_append_fp4(k, v, k_cache, k_scale, v_cache, v_scale, block_table, kv_l
         c = _pack(N, S, Hq, Hk, d, page_size, pages, width, rot, table_len, 0, _DTYPES[dt], flags, eps, 1.0, q_row,
                   _rows(k, "k", sk, dt, dev), _rows(v, "v", sk, dt, dev), o_row, table_row, *codes, *scales)
         code = _lib.lib().carve_paged_append_fp4(c, k.data_ptr(), v.data_ptr(), pq, wq, wk, pc, ps, cu, lens, table,
-                                                 *_parts(k_cache, k_scale, v_cache, v_scale), po,
-                                                 torch._C._cuda_getCurrentRawStream(dev.index))
+                                                 k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                                                 v_scale.data_ptr(), po, torch._C._cuda_getCurrentRawStream(dev.index))
     if code:
         _lib.check(code)
     return q_out
@@ -138,8 +141,9 @@ def paged_read_fp4(k_cache, k_scale, v_cache, v_scale, slots, dtype=torch.bfloat
             k_row, v_row = _rows(k_out, "k_out", shape, dtype, dev), _rows(v_out, "v_out", shape, dtype, dev)
         c = _pack(N, 0, 0, Hk, d, page_size, pages, 0, 0, 0, 0, _DTYPES[dtype], 0, 0.0, 0.0, 0, k_row, v_row, 0, 0,
                   *codes, *scales)
-        code = _lib.lib().carve_paged_read_fp4(c, *_parts(k_cache, k_scale, v_cache, v_scale), at, k_out.data_ptr(),
-                                               v_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
+        code = _lib.lib().carve_paged_read_fp4(c, k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                                               v_scale.data_ptr(), at, k_out.data_ptr(), v_out.data_ptr(),
+                                               torch._C._cuda_getCurrentRawStream(dev.index))
     if code:
         _lib.check(code)
     return k_out, v_out
@@ -160,10 +164,13 @@ def paged_attention_fp4(q, k_cache, k_scale, v_cache, v_scale, block_table, kv_l
     L = _lib.lib()
     lse = pl = None
     with _on(dev, stream):
-        out = _dense(q) if out is None else out
+        if out is None:
+            out, o_row = _dense(q), Hq * d
+        else:
+            o_row = _rows(out, "out", sq, dt, dev)
         c = _pack(N, S, Hq, Hk, d, page_size, pages, width, 0, 0, _window(window), _DTYPES[dt], step, 0.0,
-                  d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0, _rows(out, "out", sq, dt, dev),
-                  table_row, *codes, *scales)
+                  d ** -0.5 if scale is None else scale, _rows(q, "q", sq, dt, dev), 0, 0, o_row, table_row, *codes,
+                  *scales)
         if return_lse:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
             pl = lse.data_ptr()
@@ -172,8 +179,8 @@ def paged_attention_fp4(q, k_cache, k_scale, v_cache, v_scale, block_table, kv_l
         if code:
             _lib.check(code)
         workspace, ws = _workspace(workspace, need.value, dev)
-        code = L.carve_paged_attention_fp4(c, q.data_ptr(), *_parts(k_cache, k_scale, v_cache, v_scale), cu, lens, table,
-                                           out.data_ptr(), pl, ws, need.value,
+        code = L.carve_paged_attention_fp4(c, q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                                           v_scale.data_ptr(), cu, lens, table, out.data_ptr(), pl, ws, need.value,
                                            torch._C._cuda_getCurrentRawStream(dev.index))
     if code:
         _lib.check(code)

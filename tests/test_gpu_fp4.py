@@ -178,16 +178,20 @@ def test_append_drops_what_has_no_place(torch):  # noqa: F811
     assert torch.equal(out[:31], q[:31]) and (out[31:] == 7.0).all()
 
 
-@pytest.mark.parametrize("dtype,Hk,d", [("bf16", 16, 128), ("bf16", 1, 64), ("f32", 5, 64), ("bf16", 3, 128)])
-def test_append_and_read_many_tokens(torch, dtype, Hk, d):  # noqa: F811
-    """Enough tokens for several pieces to a lane: what is read back is what one token at a time stores."""
+@pytest.mark.parametrize("dtype,Hk,d,N", [("bf16", 16, 128, 3001), ("bf16", 1, 64, 9003), ("f32", 5, 64, 9003),
+                                          ("bf16", 3, 128, 9003), ("f32", 1, 128, 5003), ("bf16", 3, 128, 3001)])
+def test_append_and_read_many_tokens(torch, dtype, Hk, d, N):  # noqa: F811
+    """Enough tokens for several pieces to a lane and several tokens to a wave, sequences that end inside of one's:
+    what is read back is what one token at a time stores."""
     from chunk_gated_delta_carve_amd import paged_append_fp4, paged_read_fp4
-    N, page = 3001, 16
-    cu, lens, table, pages = ragged(torch, 8, 2, [2000, 1001], [2100, 1001], page)
+    page = 16
+    n = [1999, 1, 0, 2, N - 2002]
+    cu, lens, table, pages = ragged(torch, 8, 5, n, [2100, 1, 0, 33, N - 2002], page)
     parts = cache4(torch, "heads", pages, page, Hk, d, 90)
     k, v = inputs(torch, 91, N, Hk, d, dtype), inputs(torch, 93, N, Hk, d, dtype)
     paged_append_fp4(k, v, *parts, ints(torch, table), ints(torch, lens), ints(torch, cu))
-    slots = np.array([table[s, p // page] * page + p % page for s, p in att.token_places(cu, lens, N)])
+    at = [(s, int(lens[s]) - n[s] + i) for s in range(5) for i in range(n[s])]
+    slots = np.array([table[s, p // page] * page + p % page for s, p in at])
     got = paged_read_fp4(*parts, tensor(torch, slots), dtype=dt(torch, dtype))
     rows = np.r_[0:40, 1990:2010, N - 20:N]
     for a, x in zip(got, (k, v)):
@@ -197,6 +201,27 @@ def test_append_and_read_many_tokens(torch, dtype, Hk, d):  # noqa: F811
         top = x.float().abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True)
         off = (a.float() - x.float()).abs().unflatten(-1, (-1, 32))
         assert (off <= top * (2 / 7)).all()
+
+
+@pytest.mark.parametrize("dtype,Hq,Hk,d,N", [("bf16", 4, 2, 64, 9001), ("f32", 12, 4, 64, 2501), ("bf16", 16, 16, 128, 3001)])
+def test_append_in_one_call_or_two(torch, dtype, Hq, Hk, d, N):  # noqa: F811
+    """Norm and rotation on the way of many tokens, some of them behind the last sequence."""
+    from chunk_gated_delta_carve_amd import paged_append_fp4, qk_norm_rope_fwd, rope_tables
+    live, page = N - 7, 32
+    n = [5, live - 5]
+    cu, lens, table, pages = ragged(torch, 15, 2, n, [70, live - 5], page)
+    q, k, v = (rand(torch, 95 + i, (N, h, d), dtype, 1.5) for i, h in enumerate((Hq, Hk, Hk)))
+    pos = np.r_[65:70, 0:live - 5, [0] * 7]
+    cos, sin = rope_tables(int(pos.max()) + 1, d)
+    q2, k2 = qk_norm_rope_fwd(q, k, cos, sin, ints(torch, pos))
+    args = ints(torch, table), ints(torch, lens), ints(torch, cu)
+    one, two = (cache4(torch, "heads", pages, page, Hk, d, 98) for _ in range(2))
+    out = torch.full_like(q, 3.0)
+    paged_append_fp4(k, v, *one, *args, cos, sin, q=q, q_out=out, norm=True)
+    paged_append_fp4(k2, v, *two, *args)
+    for a, b in zip(one, two):
+        assert torch.equal(a, b)
+    assert torch.equal(out[:live], q2[:live]) and (out[live:] == 3.0).all()
 
 
 # read
@@ -285,6 +310,55 @@ def test_attention_over_long_contexts(torch, case):  # noqa: F811
         bo, bl = attention_bounds(dtype, d, d ** -0.5, *ref)
         close(f"o {r}", out[r:r + 1], ref[0], bo)
         close(f"lse {r}", lse[r:r + 1], ref[1], bl)
+
+
+RAGGED = [
+    # dtype, Hq, Hk, d, page, sequences, most new tokens, longest context, window
+    ("bf16", 4, 2, 128, 16, 150, 1, 4000, 0), ("bf16", 3, 3, 64, 64, 90, 1, 3000, 0), ("f32", 4, 2, 64, 16, 70, 1, 3000, 0),
+    ("bf16", 4, 1, 128, 4, 40, 1, 3000, 0), ("bf16", 4, 2, 64, 32, 60, 4, 3000, 0), ("bf16", 2, 2, 64, 16, 100, 1, 4000, 1500),
+    ("f32", 2, 1, 128, 2, 30, 9, 2500, 900),
+]
+
+
+@pytest.mark.parametrize("case", RAGGED, ids=[str(i) for i in range(len(RAGGED))])
+def test_ragged_contexts_dealt_to_workgroups(torch, case):  # noqa: F811
+    """Many sequences from one key on, under a table that is far wider: several items to a workgroup, and items that
+    several share."""
+    from chunk_gated_delta_carve_amd import paged_attention_fp4
+    dtype, Hq, Hk, d, page, S, most, top, window = case
+    say("case", case)
+    rng = np.random.default_rng(31)
+    n = rng.integers(1, most + 1, S)
+    kv = [int(max(x, round(np.exp(rng.uniform(0, np.log(top)))))) for x in n]
+    cu, lens, table, pages = ragged(torch, 32, S, list(n), kv, page, width=20000 // page)
+    parts = cache4(torch, "heads", pages, page, Hk, d, 135)
+    N = int(n.sum())
+    q = rand(torch, 136, (N, Hq, d), dtype)
+    step = most == 1
+    out, lse = paged_attention_fp4(q, *parts, ints(torch, table), ints(torch, lens), None if step else ints(torch, cu),
+                                   window=window, return_lse=True)
+    kf, vf = (tensor(torch, x) for x in values(parts))
+    check_attention(torch, out, lse, q, kf, vf, table, lens, cu, d ** -0.5, window, dtype)
+
+
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("bf16", 64, 64), ("f32", 64, 16)])
+def test_long_stretches(torch, dtype, d, page):  # noqa: F811
+    """More blocks to a workgroup than a lane's pages last for: each sequence has the bits of its first keys alone only
+    if all are seen, so a few are checked against the definition."""
+    from chunk_gated_delta_carve_amd import paged_attention_fp4
+    S, Hk, kv = 48, 16, 6000
+    cu, lens, table, pages = ragged(torch, 33, S, [1] * S, [kv - 7 * s for s in range(S)], page)
+    parts = cache4(torch, "heads", pages, page, Hk, d, 137)
+    q = rand(torch, 138, (S, Hk, d), dtype)
+    out, lse = paged_attention_fp4(q, *parts, ints(torch, table), ints(torch, lens), return_lse=True)
+    for s in (0, 23, 47):
+        need = -(-int(lens[s]) // page)
+        own = [t[torch.tensor(table[s, :need], device="cuda")] for t in parts]
+        k, v = values(own)
+        ref = att.paged_attention(f64(q[s:s + 1]), k, v, np.arange(need)[None], [lens[s]], [0, 1], d ** -0.5, 0)
+        bo, bl = attention_bounds(dtype, d, d ** -0.5, *ref)
+        close(f"o {s}", out[s:s + 1], ref[0], bo)
+        close(f"lse {s}", lse[s:s + 1], ref[1], bl)
 
 
 @pytest.mark.parametrize("dtype,n,kv,d", [("bf16", 1, 40, 64), ("bf16", 100, 100, 128), ("f32", 9, 20, 64),
@@ -545,6 +619,7 @@ ASSIGN = [
     (1, 40, 1, 16, 0.0, 3, 0), (5, 100, 30, 16, 0.4, 3, 7), (64, 500, 1, 16, 0.0, 9, 0), (200, 300, 50, 4, 0.3, -90, 11),
     (1024, 60, 5, 8, 0.2, 0, 100), (1025, 60, 3, 8, 0.2, 5, 1), (2500, 30, 2, 1, 0.5, -300, 0), (3, 20000, 9000, 16, 0.0, 0, 5),
     (30, 2000, 700, 256, 0.1, 2, 0), (7, 0, 20, 16, 0.0, 4, 0), (4000, 10, 0, 16, 0.9, 0, 3),
+    (5000, 20, 3, 4, 0.25, -100, 9), (4096, 9, 4, 2, 0.0, 0, 1), (2, 100, 60000, 64, 0.0, 0, 0),
 ]
 
 
@@ -742,6 +817,8 @@ def test_refusals(torch):  # noqa: F811
         (ValueError, lambda: att_(q, *parts, table, lens, cu, out=q[:2])),
         (CarveError, lambda: att_(q, *parts, table, lens, cu, out=q)),
         (CarveError, lambda: att_(q, *parts, table, lens, cu, scale=0.0)),
+        (CarveError, lambda: att_(q, *parts, table, lens, cu, scale=1e39)),
+        (CarveError, lambda: att_(q, *parts, table, lens, cu, scale=float("inf"))),
         (CarveError, lambda: att_(q, *parts, table, lens, cu, window=-1)),
         (CarveError, lambda: att_(q[:, :3], *parts, table, lens, cu)),              # 3 heads over 2
         (CarveError, lambda: att_(q, *(t[:, :12] for t in parts), table, lens, cu)),     # 12 tokens a page
