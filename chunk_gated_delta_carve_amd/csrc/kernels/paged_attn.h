@@ -303,9 +303,7 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const C& cac
       break;
     }
     if (s == -__builtin_inff()) id = -1;            // not seen: its value stays out
-    float top = s;
-#pragma unroll
-    for (int w = 1; w < 64; w <<= 1) top = fmaxf(top, __shfl_xor(top, w));
+    const float top = wave_max(s);
     if (top == -__builtin_inff()) continue;
     const float mn = fmaxf(m, top), al = fast_exp2((m - mn) * a.c);
     const float e = fast_exp2((s - mn) * a.c);      // +inf - +inf: NaN, as the formula has it
@@ -314,9 +312,9 @@ __device__ __forceinline__ void careful_row(const RowOut<E, D>& ro, const C& cac
 #pragma unroll
     for (int i = 0; i < PER; ++i) o[i] *= al;
     for (int u = 0; u < 64; ++u) {
-      const int uid = __shfl(id, u);
+      const int uid = __builtin_amdgcn_readlane(id, u);
       if (uid < 0) continue;
-      const float w = __shfl(e, u);
+      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(e), u));
       cache.add(uid, (j0 + u) & ((1 << a.page_shift) - 1), w, o);
     }
   }
@@ -428,8 +426,10 @@ struct RowsPlan {
   int base, more;                                   // blocks per workgroup, one more for the first `more`
   __device__ __forceinline__ int start(int w) const { return w * base + (w < more ? w : more); }
   __device__ __forceinline__ int share(int b) const {      // the workgroup that holds block b
-    const int big = more * (base + 1);
-    return b < big ? b / (base + 1) : more + (b - big) / base;
+    int per = base;                                        // (its reciprocal is formed here, not ahead of all else)
+    asm volatile("" : "+s"(per));
+    const int big = more * (per + 1);
+    return b < big ? quotient(b, per + 1) : more + quotient(b - big, per);
   }
   template <int MORE = 0>
   __device__ __forceinline__ RowsWork work(const PagedArgs& a, int s, int BM, int BN) const {

@@ -89,15 +89,6 @@ __device__ __forceinline__ f32x4 mma_bits(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Maximum over the four row groups of a C tile column, without a trip to LDS.
-__device__ __forceinline__ float max_groups(float x) {
-  auto u = __float_as_uint(x);
-  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  u = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
-  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-}
-
 // An item costs a workgroup about as much before and after its blocks as three of them
 // (finding it, three dependent loads, joining the waves), so that much is added to its
 // blocks where the work is dealt out: short sequences, several to a workgroup, would
@@ -118,8 +109,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   __shared__ int bad[16];
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan<kStart>(a, LY::BM, LY::BN);
-  int* cut = a.cuts + blockIdx.x * kCutInts;
-  if (threadIdx.x == 0 && a.po) cut[2] = 0;
+  if (threadIdx.x == 0 && a.po) a.cuts[blockIdx.x * kCutInts + 2] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);            // in blocks of the plan, kStart more per item than it has
   const int end_block = plan.start(blockIdx.x + 1);
@@ -155,8 +145,6 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const int k0 = __builtin_amdgcn_readfirstlane(first_key > x.lo ? first_key : x.lo);
   const int k1 = __builtin_amdgcn_readfirstlane(whole || (x.hi - first_key) / LY::BN < take ? x.hi
                                                                                           : first_key + take * LY::BN);
-  const RowOut<E, D> ro{a, h, whole, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
-
   const uint8_t* kb = static_cast<const uint8_t*>(a.kc) + h * a.kc_head;
   const uint8_t* vb = static_cast<const uint8_t*>(a.vc) + h * a.vc_head;
   const uint8_t* ksb = a.ks + h * a.k.head;
@@ -236,6 +224,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const int tok = a.by_g.div(row), p = x.pos0 + tok;
   const int p_min = x.pos0 + a.by_g.div(x.row0), p_max = x.pos0 + a.by_g.div(x.row0 + x.rows - 1);
   const int lo = first_seen(a, p, 0), lo_max = first_seen(a, p_max, 0);
+  const unsigned seen = p >= lo ? p - lo + 1 : 0;   // keys the row sees, the last of them p
   const E* qp = static_cast<const E*>(a.q) + (int64_t)(x.n0 + tok) * a.q_row + (h * a.G + row - tok * a.G) * D +
                 g * (D / 4);
   u32x4 q[NI][NQ];
@@ -282,12 +271,13 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
     if (j0 + STEP < k1) fetch(j0 + STEP);
     // lane: row c, keys 16 b + 4 g + i
     if (ok != 0xffffffffu || j0 + KT - 1 > p_min || j0 < lo_max) {
+      const unsigned mine = ok >> (4 * g);
+      const int far = p - j0 - 4 * g;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int kk = 16 * b + 4 * g + i, j = j0 + kk;
-          const bool see = ((ok >> kk) & 1u) && j <= p && j >= lo;
+          const bool see = (mine >> (16 * b + i)) & 1u && (unsigned)(far - (16 * b + i)) < seen;
           sc[b][i] = see ? sc[b][i] : -__builtin_inff();
         }
     }
@@ -348,8 +338,11 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   }
 
   // join the four waves (the last item's readers are past the barrier that ended it)
-  if (threadIdx.x == 0 && blk == 0 && !whole) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
-  l = sum_groups(l);
+  const Fp4Args& z = args_again<Fp4Args>();
+  const RowOut<E, D> ro{z, h, whole, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
+  if (threadIdx.x == 0 && blk == 0 && !whole)
+    note_cut(z.cuts + blockIdx.x * kCutInts, x, h, plan.share(last_block) - blockIdx.x + 1);
+  l = sum_halves(sum_row_pairs(l));
   if (threadIdx.x < 16) bad[threadIdx.x] = 0;
   if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }
   __syncthreads();
@@ -367,7 +360,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
     for (int i = 0; i < D / 16; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float f = fast_exp2((ms[w][r] - M) * a.c);
+      const float f = fast_exp2((ms[w][r] - M) * z.c);
       Lr += ls[w][r] * f;
 #pragma unroll
       for (int i = 0; i < D / 16; i += 4) {
@@ -377,7 +370,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
       }
     }
     const int64_t at = ro.index(x, r);
-    bool nf = odd_sum(Lr) || (Lr == 0.f && sees_any(a, x.pos0 + a.by_g.div(x.row0 + r), k0, k1));
+    bool nf = odd_sum(Lr) || (Lr == 0.f && sees_any(z, x.pos0 + z.by_g.div(x.row0 + r), k0, k1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) nf = nf || not_finite(acc[i]);
     if (nf) bad[r] = 1;
@@ -395,7 +388,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   }
   __syncthreads();
   for (int i = wave; i < x.rows; i += 4)
-    if (bad[i]) careful_row(ro, Fp4Entries<E, D>(a, h), x, i, k0, k1);
+    if (bad[i]) careful_row(ro, Fp4Entries<E, D>(z, h), x, i, k0, k1);
   __syncthreads();                                  // the next item writes the same LDS
   }
 }
