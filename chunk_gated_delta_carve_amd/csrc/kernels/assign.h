@@ -10,8 +10,14 @@
 // slots need no second pass over them but a load.
 //
 // Few tokens (a decode step) are done by the same workgroup; many by a second
-// kernel over all CUs. Bound by latency: about four dependent trips to memory.
+// kernel over all CUs. Bound by latency (a step of 64 requests: lengths, page, entry and
+// token wait for each other, 4.3 us) and by the scattered loads that one CU can make:
+// 333 requests of which 57 end with 7,700 pages, 8,800 given out and 141,000 tokens 14.3
+// and 6.3 us. Pages given back pass LDS, so that they are stored as they lie and taken
+// again from there (18.7 us before that).
 #pragma once
+#include <type_traits>
+
 #include "common.h"
 
 namespace carve {
@@ -33,18 +39,28 @@ constexpr unsigned kMostInt = 0x7fffffff;
 // at most that many table entries).
 __device__ __forceinline__ unsigned sum_to_most(unsigned a, unsigned b) { return a + b < kMostInt ? a + b : kMostInt; }
 
+// Inclusive prefix sums over a wave: in rows of 16 lanes, then the last lane of a row to the next
+// one and of the first half to the second.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned plus_dpp(unsigned x) {
+  return sum_to_most(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ unsigned scan_wave(unsigned x) {
+  x = plus_dpp<0x111, 0xf>(x);
+  x = plus_dpp<0x112, 0xf>(x);
+  x = plus_dpp<0x114, 0xf>(x);
+  x = plus_dpp<0x118, 0xf>(x);
+  x = plus_dpp<0x142, 0xa>(x);
+  return plus_dpp<0x143, 0xc>(x);
+}
+
 // Exclusive prefix sums over the workgroup of two numbers below 2^31; their totals in `all`.
 struct Two { unsigned a, b; };
 __device__ __forceinline__ Two scan_two(Two x, Two& all) {
   constexpr int W = kAssignThreads / 64;
   __shared__ unsigned sum[W][2];
   const int lane = lane_id(), wave = wave_id();
-  Two y = x;
-#pragma unroll
-  for (int w = 1; w < 64; w <<= 1) {
-    const unsigned a = __shfl_up(y.a, w), b = __shfl_up(y.b, w);
-    if (lane >= w) { y.a = sum_to_most(y.a, a); y.b = sum_to_most(y.b, b); }
-  }
+  const Two y{scan_wave(x.a), scan_wave(x.b)};
   __syncthreads();                                  // the last call's readers are done
   if (lane == 63) { sum[wave][0] = y.a; sum[wave][1] = y.b; }
   __syncthreads();
@@ -112,16 +128,24 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
   __shared__ unsigned first[kAssignThreads];        // a request's first page among the chunk's
   __shared__ unsigned offset[kAssignThreads + 1];   // and its first token
   __shared__ unsigned have[kAssignThreads];         // pages it holds already
+  // pages given back last, those from moved_from on; a word in 32 is left out against bank conflicts
+  __shared__ int moved[kAssignThreads * kAssignRun * 33 / 32];
+  auto pad = [](unsigned i) { return i + i / 32; };
   const int tid = threadIdx.x;
   const unsigned capacity = (unsigned)a.capacity, lacking = a.free_count[1];
   unsigned top = at_least_0(a.free_count[0]);
   top = top < capacity ? top : capacity;
+  unsigned moved_from = kMostInt;
+  // the first chunk of requests, on its way while nothing waits for it
+  const bool there = tid < a.S;
+  const int kv0 = there ? a.kv_lens[tid] : 0, new0 = there ? a.new_lens[tid] : 0, done0 = there && a.done ? a.done[tid] : 0;
   Two all;
   // what ended requests give back
   if (a.done)
     for (int s0 = 0; s0 < a.S; s0 += kAssignThreads) {
       const int s = s0 + tid, n = a.S - s0 < kAssignThreads ? a.S - s0 : kAssignThreads;
-      const unsigned held = s < a.S && a.done[s] != 0 ? pages_of(a, at_least_0(a.kv_lens[s])) : 0;
+      const int over = s0 == 0 ? done0 : s < a.S ? a.done[s] : 0;
+      const unsigned held = over ? pages_of(a, at_least_0(s0 == 0 ? kv0 : a.kv_lens[s])) : 0;
       const unsigned mine = scan_two(Two{held, 0}, all).a;
       first[tid] = mine;
       __syncthreads();
@@ -141,11 +165,15 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
         }
 #pragma unroll
         for (int u = 0; u < kAssignRun; ++u) good += page[u] >= 0;
-        unsigned at = sum_to_most(top, scan_two(Two{good, 0}, all).a);
+        unsigned at = scan_two(Two{good, 0}, all).a;
 #pragma unroll
         for (int u = 0; u < kAssignRun; ++u)
-          if (page[u] >= 0 && at < capacity) a.free_pages[at++] = page[u];
-        top = sum_to_most(top, all.a) < capacity ? top + all.a : capacity;
+          if (page[u] >= 0) moved[pad(at++)] = page[u];
+        __syncthreads();
+        const unsigned fit = all.a < capacity - top ? all.a : capacity - top;
+        for (unsigned k = tid; k < fit; k += kAssignThreads) a.free_pages[top + k] = moved[pad(k)];
+        moved_from = top;
+        top += fit;
       }
       __syncthreads();
     }
@@ -155,8 +183,9 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
     const int s = s0 + tid, n = a.S - s0 < kAssignThreads ? a.S - s0 : kAssignThreads;
     unsigned fresh = 0, need = 0;
     if (s < a.S) {
-      const unsigned old = a.done && a.done[s] != 0 ? 0 : at_least_0(a.kv_lens[s]);
-      fresh = at_least_0(a.new_lens[s]);
+      const int over = s0 == 0 ? done0 : a.done ? a.done[s] : 0;
+      const unsigned old = over ? 0 : at_least_0(s0 == 0 ? kv0 : a.kv_lens[s]);
+      fresh = at_least_0(s0 == 0 ? new0 : a.new_lens[s]);
       const unsigned len = sum_to_most(old, fresh), holds = pages_of(a, old);
       need = pages_of(a, len) - holds;
       have[tid] = holds;
@@ -167,22 +196,32 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
     offset[tid] = sum_to_most(tokens, at.b);
     if (s < a.S) a.cu[s] = (int)offset[tid];
     __syncthreads();
-    for (unsigned i0 = tid; i0 < all.a; i0 += kAssignThreads * kAssignRun) {
-      unsigned i[kAssignRun];
-      int r[kAssignRun], page[kAssignRun];
+    auto deal = [&](auto run, unsigned i0) {        // entries i0 .. i0 + run kAssignThreads - 1
+      constexpr int U = decltype(run)::value;
+      unsigned i[U];
+      int r[U], page[U];
 #pragma unroll
-      for (int u = 0; u < kAssignRun; ++u) {
-        i[u] = i0 + u * kAssignThreads;
+      for (int u = 0; u < U; ++u) {
+        i[u] = i0 + u * kAssignThreads + tid;
         i[u] = i[u] < all.a ? i[u] : all.a - 1;     // past the end, the last one again: the same entry and page
       }
-      last_at<kAssignRun>(first, n, i, r);
+      last_at<U>(first, n, i, r);
 #pragma unroll
-      for (int u = 0; u < kAssignRun; ++u) {
-        const unsigned from = sum_to_most(used, i[u]);
-        page[u] = from < top ? a.free_pages[top - 1 - from] : -1;
+      for (int u = 0; u < U; ++u) {
+        const unsigned from = sum_to_most(used, i[u]), at = top - 1 - from;
+        page[u] = from >= top ? -1 : at >= moved_from ? moved[pad(at - moved_from)] : a.free_pages[at];
       }
 #pragma unroll
-      for (int u = 0; u < kAssignRun; ++u) a.table[(s0 + r[u]) * a.table_row + have[r[u]] + (i[u] - first[r[u]])] = page[u];
+      for (int u = 0; u < U; ++u) a.table[(s0 + r[u]) * a.table_row + have[r[u]] + (i[u] - first[r[u]])] = page[u];
+    };
+    for (unsigned i0 = 0; i0 < all.a;) {
+      if (all.a - i0 > kAssignThreads) {
+        deal(std::integral_constant<int, kAssignRun>{}, i0);
+        i0 += kAssignThreads * kAssignRun;
+      } else {
+        deal(std::integral_constant<int, 1>{}, i0);
+        i0 += kAssignThreads;
+      }
     }
     used = sum_to_most(used, all.a);
     tokens = sum_to_most(tokens, all.b);

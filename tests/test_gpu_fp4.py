@@ -646,6 +646,31 @@ def test_assign(torch, case):  # noqa: F811
         check_assign(torch, table, kv, new, stack, [free, 4], page, int(new.sum()) + pad, d)
 
 
+@pytest.mark.parametrize("S,top,page,holes,fit", [(40, 9000, 4, 0.0, 1.0), (40, 9000, 4, 0.3, 1.0), (3, 30000, 1, 0.1, 0.6),
+                                                  (1500, 40, 2, 0.2, 1.0), (1500, 40, 2, 0.0, 0.3), (2, 8192, 1, 0.0, 1.0)])
+def test_assign_gives_back_what_others_take(torch, S, top, page, holes, fit):  # noqa: F811
+    """Most requests end, tables with entries that are no pages, stacks that do not hold all that comes back, and new
+    tokens that take pages given back just now and ones that were free before."""
+    rng = np.random.default_rng(S + page)
+    kv = rng.integers(top // 2, top + 1, S)
+    done = (rng.random(S) < 0.7).astype(int)
+    done[0] = 1
+    held = -(-kv // page)
+    new = np.where(rng.random(S) < 0.8, rng.integers(0, int(1.5 * top) + 1, S), 0)
+    free = 50
+    pages = int(held.sum()) + free
+    order = rng.permutation(pages)
+    table = np.full((S, -(-3 * top // page)), -1)
+    at = 0
+    for s in range(S):
+        table[s, :held[s]] = order[at:at + held[s]]
+        at += held[s]
+    table[rng.random(table.shape) < holes] = -1
+    capacity = max(free, int(pages * fit))
+    stack = stack_of(pages, order[at:], capacity)
+    check_assign(torch, table, kv, new, stack, [free, 1], page, int(new.sum()), done)
+
+
 def test_assign_at_its_edges(torch):  # noqa: F811
     """Negative lengths, holes in the table of an ended request, tokens past the table, too few rows for the tokens, a
     stack that overflows, counts outside of it, no requests, no tokens, no pages."""
