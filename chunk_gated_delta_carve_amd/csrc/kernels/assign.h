@@ -13,7 +13,7 @@
 // kernel over all CUs. Bound by latency (a step of 64 requests: lengths, page, entry and
 // token wait for each other, 4.3 us) and by the scattered loads that one CU can make:
 // 333 requests of which 57 end with 7,700 pages, 8,800 given out and 141,000 tokens 14.3
-// and 6.3 us. Pages given back pass LDS, so that they are stored as they lie and taken
+// and 4.2 us. Pages given back pass LDS, so that they are stored as they lie and taken
 // again from there (18.7 us before that).
 #pragma once
 #include <type_traits>
@@ -102,22 +102,21 @@ __device__ __forceinline__ unsigned pages_of(const AssignArgs& a, unsigned token
 
 __device__ __forceinline__ unsigned at_least_0(int x) { return x > 0 ? x : 0; }
 
-// Position and slot of token t of request s, whose tokens end before c1 at length kv;
-// t >= c1 for a token behind the last request.
-__device__ __forceinline__ void put_token(const AssignArgs& a, int t, int s, int c1, int kv) {
-  int pos = 0;
-  int64_t slot = -1;
-  if (t < c1) {
-    pos = kv - c1 + t;
-    if (pos < 0) pos = 0;                           // lengths that stopped at 2^31 - 1
-    const int i = pos >> a.page_shift;
-    if (a.slots && i < a.width) {
-      const int page = a.table[s * a.table_row + i];
-      if (page >= 0) slot = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-    }
-  }
+// Position of token t of a request whose tokens end before c1 at length kv.
+__device__ __forceinline__ int position(int t, int c1, int kv) {
+  const int pos = kv - c1 + t;
+  return pos > 0 ? pos : 0;                         // lengths that stopped at 2^31 - 1
+}
+// Its page, -1 if there is none. No branch: the loads of several tokens go out together.
+__device__ __forceinline__ int page_of(const AssignArgs& a, bool real, int s, int pos) {
+  const int i = pos >> a.page_shift;
+  const bool in = real && a.slots && i < a.width;
+  const int page = *(in ? a.table + (s * a.table_row + i) : a.cu);
+  return in ? page : -1;
+}
+__device__ __forceinline__ void put_token(const AssignArgs& a, int t, int pos, int page) {
   if (a.positions) a.positions[t] = pos;
-  if (a.slots) a.slots[t] = slot;
+  if (a.slots) a.slots[t] = page < 0 ? -1 : ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
 // Where few requests have many pages each, a thread takes this many of them: their loads
@@ -238,9 +237,9 @@ __global__ __launch_bounds__(kAssignThreads) void paged_assign_kernel(AssignArgs
   if (tid == 0) offset[a.S] = tokens;
   __syncthreads();
   for (int t = tid; t < a.N; t += kAssignThreads) {
-    if ((unsigned)t >= tokens) { put_token(a, t, 0, 0, 0); continue; }
-    const int r = last_at(offset, a.S, t);
-    put_token(a, t, r, offset[r + 1], first[r]);
+    const bool real = (unsigned)t < tokens;
+    const int r = real ? last_at(offset, a.S, t) : 0, pos = real ? position(t, offset[r + 1], first[r]) : 0;
+    put_token(a, t, pos, page_of(a, real, r, pos));
   }
 }
 
@@ -253,14 +252,27 @@ __global__ __launch_bounds__(256) void paged_assign_tokens_kernel(AssignArgs a) 
     __syncthreads();
   }
   const int tokens = here ? offset[a.S] : a.cu[a.S];
+  // four tokens of a thread at a time, their loads side by side
+  constexpr int U = 4;
+  unsigned t[U];
+  int s[U], pos[U], page[U];
+  bool real[U];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t t = (int64_t)blockIdx.x * 1024 + u * 256 + threadIdx.x;
-    if (t >= a.N) return;
-    if (t >= tokens) { put_token(a, (int)t, 0, 0, 0); continue; }
-    const int s = here ? last_at(offset, a.S, (unsigned)t) : last_at(a.cu, a.S, (unsigned)t);
-    put_token(a, (int)t, s, here ? offset[s + 1] : a.cu[s + 1], a.kv_out[s]);
+  for (int u = 0; u < U; ++u) t[u] = blockIdx.x * (256 * U) + u * 256 + threadIdx.x;
+  if (here) last_at<U>(offset, a.S, t, s);
+  else last_at<U>(a.cu, a.S, t, s);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    real[u] = t[u] < (unsigned)tokens;              // (then there is a request)
+    const int after = real[u] ? s[u] + 1 : 0, c1 = here ? offset[after] : a.cu[after];
+    const int kv = *(real[u] ? a.kv_out + s[u] : a.cu);
+    pos[u] = real[u] ? position(t[u], c1, kv) : 0;
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) page[u] = page_of(a, real[u], s[u], pos[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (t[u] < (unsigned)a.N) put_token(a, t[u], pos[u], page[u]);
 }
 
 }  // namespace carve
