@@ -121,7 +121,7 @@ hipError_t join_rows(const carve::PagedArgs& a, hipStream_t s) {
   const int rows = (int)(most < BM ? most : BM);
   const int64_t items = a.Hk * (up((int64_t)a.N * a.G, BM) > a.S ? up((int64_t)a.N * a.G, BM) : a.S);
   if (a.shares >= kWideJoin * items)
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(a.shares, rows), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(up(a.shares, carve::kJoinNotes), rows), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 1>), dim3(a.shares, up(rows, 4)), dim3(256), 0, s, a);
   return hipGetLastError();

@@ -1388,21 +1388,39 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
   }
 }
 
-// The rows of the item, if any, that starts in workgroup blockIdx.x's stretch of the
-// row kernel and goes on behind it: what that workgroup noted down. A wave per row
-// (d = 64, fp32, 768 workgroups: 5.2 us, 9.5 with WAVES = 4), or a workgroup per row
-// where few items leave many shares to each (d = 128, 128 shares: 6.1 us, 12 in a
-// wave).
+// The rows of the items, one to a workgroup of the row kernel at most, that start in its
+// stretch and go on behind it: what that workgroup noted down. A wave per row (d = 64,
+// fp32, 768 workgroups: 5.2 us, 9.5 with WAVES = 4), or a workgroup per row where few items
+// leave many shares to each (d = 128, 128 shares: 6.1 us, 12 in a wave). Then few of the
+// notes hold anything, and a workgroup looks at kJoinNotes of them: leaving at once costs
+// a workgroup its start all the same (768 notes of 8 rows, 8 items: 6.3 us, 4.5 so).
+constexpr int kJoinNotes = 8;
+
+__device__ __forceinline__ int64_t noted_row(const PagedArgs& a, const int* cut, int r) {
+  const int row = cut[1] + r, i = a.by_g.div(row);
+  return (int64_t)(cut[0] + i) * a.Hq + cut[3] * a.G + (row - i * a.G);
+}
+
 template <typename E, int D, int WAVES>
 __global__ __launch_bounds__(256) void paged_rows_combine_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
-  const int64_t w = blockIdx.x;
-  const int* cut = a.cuts + w * kCutInts;
-  const int r = WAVES > 1 ? blockIdx.y : blockIdx.y * 4 + wave_id();
-  if (r >= cut[2]) return;
-  const int row = cut[1] + r, i = a.by_g.div(row);
-  const int64_t at = (int64_t)(cut[0] + i) * a.Hq + cut[3] * a.G + (row - i * a.G);
-  join_shares<E, D, WAVES>(a, at, (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r, 2 * LY::BM, cut[4]);
+  auto join = [&](int64_t w, int r) {
+    const int* cut = a.cuts + w * kCutInts;
+    join_shares<E, D, WAVES>(a, noted_row(a, cut, r), (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r,
+                             2 * LY::BM, cut[4]);
+  };
+  if constexpr (WAVES > 1) {
+    const int first = blockIdx.x * kJoinNotes, mine = first + lane_id();
+    const bool look = lane_id() < kJoinNotes && mine < a.shares;
+    unsigned todo = (unsigned)__ballot(look && (int)blockIdx.y < a.cuts[(look ? mine : 0) * (int64_t)kCutInts + 2]);
+    for (; todo; todo &= todo - 1) {
+      join(first + __builtin_ctz(todo), blockIdx.y);
+      if (todo & (todo - 1)) __syncthreads();       // the next one's sums take the same LDS
+    }
+  } else {
+    const int r = blockIdx.y * 4 + wave_id();
+    if (r < a.cuts[blockIdx.x * (int64_t)kCutInts + 2]) join(blockIdx.x, r);
+  }
 }
 
 }  // namespace carve
