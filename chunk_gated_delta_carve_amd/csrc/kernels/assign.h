@@ -11,9 +11,9 @@
 //
 // Few tokens (a decode step) are done by the same workgroup; many by a second
 // kernel over all CUs. Bound by latency (a step of 64 requests: lengths, page, entry and
-// token wait for each other, 4.3 us) and by the scattered loads that one CU can make:
+// token wait for each other, 3.8 us) and by the scattered loads that one CU can make:
 // 333 requests of which 57 end with 7,700 pages, 8,800 given out and 141,000 tokens 14.3
-// and 4.2 us. Pages given back pass LDS, so that they are stored as they lie and taken
+// and 4.4 us. Pages given back pass LDS, so that they are stored as they lie and taken
 // again from there (18.7 us before that).
 #pragma once
 #include <type_traits>

@@ -58,6 +58,14 @@ struct Fp4Entries {
 // of 16 bytes (8 at d = 64) and one scale, opened to bf16 in registers: the keys as
 // operands, the values on their way through the wave's LDS. fp32 queries and weights
 // enter the products as three bf16 parts, which hold their 24 bits; the codes are exact.
+// (The products that take 4-bit operands as they are drop what lies 2^13 below the largest
+// of eight terms, so a sum would not hold 32 bits.)
+//
+// Bound by memory where there is much (64 sequences of 200 to 8192 keys, 4 heads of 128,
+// 147 MB: 33 us, 4.4 TB/s), by an item's chain of trips otherwise: lengths, page, entries,
+// some 5 us (4 sequences of 50k to 65k keys of 2 heads, 64 MB: 18 us where the copy's rate
+// would give 13). Loading two blocks ahead costs d = 64 its fourth workgroup of a CU (256
+// sequences of 1000 keys, 12 heads, 54 us became 59) and gains d = 128 nothing.
 template <typename E, int D>
 struct RowsFp4 {
   static constexpr int BM = 16, KT = 32, BN = 4 * KT;                            // as RowsLayout
@@ -92,8 +100,8 @@ __device__ __forceinline__ f32x4 mma_bits(u32x4 a, u32x4 b, f32x4 c) {
 // An item costs a workgroup about as much before and after its blocks as three of them
 // (finding it, three dependent loads, joining the waves), so that much is added to its
 // blocks where the work is dealt out: short sequences, several to a workgroup, would
-// otherwise make the slowest ones. 64 sequences of 200 to 8192 keys, 4 heads of 128:
-// 37.5 us, without 44.
+// otherwise make the slowest ones. 64 sequences of 200 to 8192 keys, 4 heads of 128: 33.3
+// us, without 36.5; 12 heads of 64: 56 and 66.
 constexpr int kStart = 3;
 
 // WIDE: pages of 16 tokens and more, so that 16 aligned keys lie in one. A lane looks
@@ -397,7 +405,11 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
 // Many rows (bf16): the kernels of paged_attn.h over blocks that are opened to bf16 on
 // their way from registers to LDS. A thread has 16 channels of a key, 8 bytes and a
 // scale: 64 keys of 128 channels are one such piece for each of 512 threads, keys and
-// values alike, 16 conversions and four 16-byte stores a step.
+// values alike, 16 conversions and four 16-byte stores a step. What bounds those kernels
+// bounds these (products, then what stands beside them); a quarter of the loads makes up
+// for the conversions: 4096 tokens over 16384 keys, 16 on 4 heads of 128, 477 us (1.0
+// PFLOP/s) where the bf16 cache takes 498; 8 prompts, window 1024, 12 on 4 heads of 64, 82
+// and 88.
 template <int D, int NW, bool WIDE>
 struct Fp4Tiles : TileRows<D, NW, Fp4Args> {
   using R = TileRows<D, NW, Fp4Args>;
