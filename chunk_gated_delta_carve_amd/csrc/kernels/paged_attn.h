@@ -1393,7 +1393,7 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
 // fp32, 768 workgroups: 5.2 us, 9.5 with WAVES = 4), or a workgroup per row where few items
 // leave many shares to each (d = 128, 128 shares: 6.1 us, 12 in a wave). Then few of the
 // notes hold anything, and a workgroup looks at kJoinNotes of them: leaving at once costs
-// a workgroup its start all the same (768 notes of 8 rows, 8 items: 6.3 us, 4.5 so).
+// a workgroup its start all the same (768 notes of 8 rows, 8 items: 6.3 us, 4.3 so).
 constexpr int kJoinNotes = 8;
 
 __device__ __forceinline__ int64_t noted_row(const PagedArgs& a, const int* cut, int r) {
