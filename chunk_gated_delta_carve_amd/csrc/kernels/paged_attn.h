@@ -37,6 +37,30 @@ namespace carve {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Maximum over the four groups of 16 lanes: the lanes of one column of a 16 x 16 tile.
+__device__ __forceinline__ float max_groups(float x) {
+  auto u = __float_as_uint(x);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  u = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+// Maximum over all 64 lanes, in every lane.
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, dpp_mov<0x128>(x));   // rotations in 16 lanes, as sum_row16
+  x = fmaxf(x, dpp_mov<0x124>(x));
+  x = fmaxf(x, dpp_mov<0x122>(x));
+  return max_groups(fmaxf(x, dpp_mov<0x121>(x)));
+}
+// The kernel's arguments, read once more: for code that is seldom or late reached, so
+// that it does not hold scalar registers all through what comes before it.
+template <typename A>
+__device__ __forceinline__ const A& args_again() {
+  auto p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const A*)p;
+}
+
 // Division of n < 2^31 by a number that the host knows: floor(n mul / 2^(32 + shift)),
 // mul = ceil(2^(32 + shift) / d) with 2^shift < d <= 2^(shift + 1), is exact there.
 struct Divisor {

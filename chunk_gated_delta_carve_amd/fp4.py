@@ -7,9 +7,9 @@ bf16 cache's bytes), and `paged_read_fp4` gives the values back. `paged_fp4_cach
 marshalling only: every step runs in the HIP library.
 
 A cache is four uint8 tensors, k_cache and v_cache [pages, page_size, Hk, d / 2] and k_scale and v_scale [pages,
-page_size, Hk, d / 32]. Every 32 channels of a head share one scale 2^(byte - 127) (255: NaN); a code is a sign and
-0, 0.5, 1, 1.5, 2, 3, 4 or 6, two to a byte with the even channel in the low half. Page, token and head strides are
-free.
+page_size, Hk, d / 32]. Every 32 channels of a head share one scale 2^(byte - 127) (2 to 252; 255: NaN); a code is a
+sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6, two to a byte with the even channel in the low half. Page, token and head
+strides are free.
 """
 from __future__ import annotations
 

@@ -386,7 +386,8 @@ int carve_paged_attention(const carve_paged_config* cfg, const void* q, const vo
  * A head's d channels are d / 32 blocks of 32. A block is 32 codes of 4 bits (a sign,
  * two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte
  * with the even channel in the low half, and one byte e, its scale 2^(e - 127); 255
- * makes every value of the block NaN. Such a value is exact in bf16.
+ * makes every value of the block NaN. With 2 <= e <= 252, all that is ever stored, a value
+ * is a normal number or 0 and exact in bf16; what other bytes give is not defined.
  *   codes   uint8 [pages, page_size, Hk, d / 2]
  *   scales  uint8 [pages, page_size, Hk, d / 32]
  * for keys and for values; a head's bytes are contiguous, page, token and head strides
@@ -404,9 +405,9 @@ typedef struct {
 /* carve_paged_append into such a cache. A block takes the smallest scale 2^e with
  * max |x| <= 7 2^e, -125 <= e <= 125; a value becomes the nearest code, the even one of
  * two, at most 6: it is off by at most 2^e (by more only where |x| > 7 2^125), and by at
- * most 2^e / 4 where |x| <= 2^(e+1). A block with an infinity or NaN is stored as NaN (codes 0). The keys are normed and
- * rotated on the way where that is asked for, rounded to `dtype` as by
- * carve_qk_norm_rope_fwd, and that is what is stored in 4 bits. The same refusals hold;
+ * most 2^e / 4 where |x| <= 2^(e+1). A block with an infinity or NaN is stored as NaN
+ * (codes 0). The keys are normed and rotated on the way where that is asked for, rounded to
+ * `dtype` as by carve_qk_norm_rope_fwd, and that is what is stored in 4 bits. The same refusals hold;
  * codes and scales of keys and values may share one allocation. */
 int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k, const void* v, const void* q,
                            const void* q_weight, const void* k_weight, const float* cos, const float* sin,

@@ -767,6 +767,38 @@ def test_prompts_then_single_tokens(torch, dtype, Hq, Hk, d):  # noqa: F811
     assert int(count[1]) == 0 and int(count[0]) == pages - sum(-(-int(x) // page) for x in lens.cpu()) and len(set(held)) == S
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 128)])
+def test_room_in_a_cache_that_is_not_in_4_bits(torch, dtype, d):  # noqa: F811
+    """paged_assign's results as paged_append, paged_attention and qk_norm_rope_fwd take them."""
+    from chunk_gated_delta_carve_amd import paged_append, paged_assign, paged_attention, qk_norm_rope_fwd, rope_tables
+    S, Hq, Hk, page, pages, width = 3, 4, 2, 16, 40, 12
+    cos, sin = rope_tables(256, d)
+    kc, vc = (torch.zeros(pages, page, Hk, d, dtype=dt(torch, dtype), device="cuda") for _ in range(2))
+    tab = torch.full((S, width), -1, dtype=torch.int32, device="cuda")
+    lens, free, count = ints(torch, [0] * S), ints(torch, np.arange(pages)), ints(torch, [pages, 0])
+    history = [([], []) for _ in range(S)]
+    for turn, (n, over) in enumerate([([40, 7, 65], None), ([1, 1, 1], None), ([1, 20, 1], [0, 1, 0]), ([1, 1, 1], None)]):
+        N = sum(n)
+        q, k, v = (rand(torch, 400 + 3 * turn + i, (N, h, d), dtype) for i, h in enumerate((Hq, Hk, Hk)))
+        cu, lens, pos, slots, count = paged_assign(tab, lens, ints(torch, n), free, count, page, N,
+                                                   done=None if over is None else ints(torch, over), kv_lens_out=lens)
+        qr = paged_append(k, v, kc, vc, tab, lens, cu, cos, sin, q=q)
+        q2, k2 = qk_norm_rope_fwd(q, k, cos, sin, pos, norm=False)
+        assert torch.equal(qr, q2)
+        assert torch.equal(kc.flatten(0, 1)[slots], k2) and torch.equal(vc.flatten(0, 1)[slots], v)
+        out = paged_attention(qr, kc, vc, tab, lens, cu)
+        offs = cu.cpu().numpy()
+        for s in range(S):
+            if over is not None and over[s]:
+                history[s] = ([], [])
+            history[s][0].extend(f64(k2)[offs[s]:offs[s + 1]])
+            history[s][1].extend(f64(v)[offs[s]:offs[s + 1]])
+            kf, vf = (np.array(x)[None] for x in history[s])
+            rows = slice(int(offs[s]), int(offs[s + 1]))
+            ref = att.paged_attention(f64(qr[rows]), kf, vf, np.zeros((1, 1), int), [kf.shape[1]], [0, n[s]], d ** -0.5, 0)
+            close(f"turn {turn} request {s}", out[rows], ref[0], attention_bounds(dtype, d, d ** -0.5, *ref)[0])
+
+
 def test_captured_decode_steps(torch):  # noqa: F811
     """A whole decode step (room, append, attention) captured once: every replay has the bits of an eager run of the same
     step on a copy of the state, with eager work in between. Two graphs share one workspace."""
