@@ -119,17 +119,22 @@ extern "C" int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k
   if (w.per_token > 65535) return CARVE_EUNSUPPORTED;
   // several tokens to a wave where there are more waves than the GPU holds at once, eight pieces to a lane at most
   const bool run = (int64_t)c.N * w.per_token > kFewWaves;
+  const bool turn = c.rot > 0 || norm;
   const hipError_t e = by_type(c.dtype, c.d, [&](auto t, auto d) {
     return by_pieces(w.per_lane, [&](auto u) {
-      constexpr int U = decltype(u)::value, TOK = U <= 2 ? 4 : 2;
-      const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-      if (run)
-        hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, U, TOK>),
-                           dim3((unsigned)up(c.N, 4 * TOK), w.per_token), dim3(256), 0, s, f);
-      else
-        hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), decltype(d)::value, U, 1>),
-                           dim3((unsigned)up(c.N, 4), w.per_token), dim3(256), 0, s, f);
-      return hipGetLastError();
+      constexpr int U = decltype(u)::value, D = decltype(d)::value;
+      auto launch = [&](auto tok, auto turned) {
+        constexpr int TOK = decltype(tok)::value;
+        hipLaunchKernelGGL((carve::paged_append_fp4_kernel<decltype(t), D, U, TOK, decltype(turned)::value>),
+                           dim3((unsigned)up(c.N, 4 * TOK), w.per_token), dim3(256), 0,
+                           reinterpret_cast<hipStream_t>(stream), f);
+        return hipGetLastError();
+      };
+      auto tokens = [&](auto turned) {
+        return run ? launch(std::integral_constant<int, U <= 2 ? 4 : 2>{}, turned)
+                   : launch(std::integral_constant<int, 1>{}, turned);
+      };
+      return turn ? tokens(std::true_type{}) : tokens(std::false_type{});
     });
   });
   return e == hipSuccess ? CARVE_OK : hip_failed(e);

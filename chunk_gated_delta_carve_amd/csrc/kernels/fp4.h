@@ -102,41 +102,61 @@ struct Fp4AppendArgs {
   Fp4Strides k, v;                     // of the scales
 };
 
-// As token_place, every lane for a token of its own.
-__device__ __forceinline__ TokenPlace lane_place(const AppendArgs& a, int n) {
-  TokenPlace x{kNoToken, -1, 0};
-  if (n >= a.N || a.S == 0) return x;
-  int s = n, i = 0, cnt = 1;
-  if (a.cu) {
-    s = last_at(a.cu, a.S, (unsigned)n);
-    const int c0 = a.cu[s], c1 = a.cu[s + 1];
-    if (n < c0 || n >= c1) return x;                // behind the last sequence
-    i = n - c0;
-    cnt = c1 - c0;
-  } else if (s >= a.S) {
+// Where the TOK tokens from n0 on go, lane l for token l % TOK. What tells their sequences
+// is loaded ahead of the wave's rows, since loads come back in the order they went out: up
+// to 64 sequences a lane has one of them, beyond a lane looks its token's up.
+template <int TOK>
+struct TokenSeeker {
+  int s, c0, c1, kv;
+  __device__ __forceinline__ TokenSeeker(const AppendArgs& a, int n0) {
+    const int n = n0 + lane_id() % TOK;
+    s = a.cu ? lane_id() : n;
+    if (a.cu && a.S > 64) s = last_at(a.cu, a.S, (unsigned)n);
+    s = s < a.S ? s : a.S - 1;
+    c0 = a.cu ? a.cu[s] : s;
+    c1 = a.cu ? a.cu[s + 1] : s + 1;
+    kv = a.kv_lens[s];
+  }
+  __device__ __forceinline__ TokenPlace places(const AppendArgs& a, int n0) const {
+    const int n = n0 + lane_id() % TOK;
+    int in = s, b = c0, e = c1, len = kv;
+    if (a.cu && a.S <= 64) {
+#pragma unroll
+      for (int k = 0; k < TOK; ++k) {
+        const int over = __popcll(__ballot(lane_id() < a.S && c1 <= n0 + k)), t = over < a.S ? over : a.S - 1;
+        const int tb = __builtin_amdgcn_readlane(c0, t), te = __builtin_amdgcn_readlane(c1, t);
+        const int tl = __builtin_amdgcn_readlane(kv, t);
+        const bool mine = lane_id() % TOK == k;
+        in = mine ? t : in; b = mine ? tb : b; e = mine ? te : e; len = mine ? tl : len;
+      }
+    }
+    TokenPlace x{kNoToken, -1, 0};
+    if (n >= a.N || n < b || n >= e) return x;      // behind the last sequence
+    x.pos = (int64_t)len - e + n;
+    const int64_t slot = x.pos >> a.page_shift;
+    if (x.pos >= 0 && slot < a.width) x.page = a.table[in * a.table_row + slot];
+    if (x.page >= a.pages) x.page = -1;
+    x.off = x.pos & ((1 << a.page_shift) - 1);
     return x;
   }
-  x.pos = (int64_t)a.kv_lens[s] - cnt + i;
-  const int64_t slot = x.pos >> a.page_shift;
-  if (x.pos >= 0 && slot < a.width) x.page = a.table[s * a.table_row + slot];
-  if (x.page >= a.pages) x.page = -1;
-  x.off = x.pos & ((1 << a.page_shift) - 1);
-  return x;
-}
+};
 
 // A wave has 64 U pieces of each of TOK neighbouring tokens (q's, k's and v's heads): all
-// of the rows are under way while lanes look for the tokens' places, three loads that wait
-// for each other. A block's lanes (4, or 8 in fp32) find its largest value by lane
-// exchanges; each stores its own codes, the first the scale. Bound by its addresses at
-// first: 22,044 tokens of 8 heads of 128 in bf16 (57 MB read and written) took 28 us with a
-// 64-bit product for every stride and piece, and take 18 with a token's part as scalars
-// and a head's found once for all tokens; 64 single tokens, three trips to memory, 3.6.
-template <typename E, int D, int U, int TOK>
+// of the rows are under way while lanes look for the tokens' places. A block's lanes (4, or
+// 8 in fp32) find its largest value by lane exchanges; each stores its own codes, the first
+// the scale. Bound by instructions, then by the trips to memory that wait for each other
+// (lengths; rows and page; the stores): 22,044 tokens of 8 heads of 128 in bf16 (57 MB read
+// and written) took 28 us with a 64-bit product for every stride and piece, 18 with a
+// token's part as scalars and a head's found once for all tokens, and take 15 (3.8 TB/s)
+// with sequences found in one trip and without what norm and rotation need (TURN) where
+// there is neither (16.3 with it); 64 single tokens 3.5.
+template <typename E, int D, int U, int TOK, bool TURN>
 __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) {
   const AppendArgs& a = f.a;
   constexpr int V = Piece<E>::V, LPR = D / V;
   const int n0 = (blockIdx.x * 4 + wave_id()) * TOK;
   if (n0 >= a.N) return;
+  const TokenSeeker<TOK> seek(a, n0);
   const Turn<E, D> t(a.rot, a.interleaved);
   const int heads = a.Hq + 2 * a.Hk;
   u32x4 raw[TOK][U];
@@ -159,9 +179,9 @@ __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) 
     code_at[u] = (uint64_t)hk * (unsigned)(isk ? a.kc_head : a.vc_head) + t.c * (V / 2);
     scale_at[u] = (uint64_t)hk * (unsigned)(isk ? f.k.head : f.v.head) + t.c / (kFp4Block / V);
   }
-  const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
-  const TokenPlace mine = lane_place(a, n0 + lane_id() % TOK);
-  const bool turns = a.rot > 0 || a.norm;
+  u32x4 wq{}, wk{};
+  if constexpr (TURN) { wq = weight_piece<E, D>(a.wq, t.c); wk = weight_piece<E, D>(a.wk, t.c); }
+  const TokenPlace mine = seek.places(a, n0);
 #pragma unroll
   for (int k = 0; k < TOK; ++k) {
     const int64_t n = n0 + k;
@@ -177,15 +197,17 @@ __global__ __launch_bounds__(256) void paged_append_fp4_kernel(Fp4AppendArgs f) 
     uint8_t *kc = token(a.kc, a.kc_page, a.kc_tok), *vc = token(a.vc, a.vc_page, a.vc_tok);
     uint8_t *ks = token(f.ks, f.k.page, f.k.tok), *vs = token(f.vs, f.v.page, f.v.tok);
     float cs[V], sn[V];
-    t.angles(a.cos, a.sin, a.rot, a.table_len, pos, false, cs, sn);
+    if constexpr (TURN) t.angles(a.cos, a.sin, a.rot, a.table_len, pos, false, cs, sn);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = hh[u];
       const bool isq = h < a.Hq, isk = h < a.Hq + a.Hk;
       u32x4 y = raw[k][u];
-      if (turns && __ballot(isk)) {
-        const u32x4 z = norm_rope_piece<E, D>(y, t, isq ? wq : wk, cs, sn, a.norm, a.eps);
-        y = isk ? z : y;
+      if constexpr (TURN) {
+        if (__ballot(isk)) {
+          const u32x4 z = norm_rope_piece<E, D>(y, t, isq ? wq : wk, cs, sn, a.norm, a.eps);
+          y = isk ? z : y;
+        }
       }
       if (isq) *reinterpret_cast<u32x4*>(static_cast<E*>(a.qo) + n * a.qo_row + h * D + t.c * V) = y;
       if (page < 0 || !__ballot(!isq)) continue;

@@ -203,6 +203,31 @@ def test_append_and_read_many_tokens(torch, dtype, Hk, d, N):  # noqa: F811
         assert (off <= top * (2 / 7)).all()
 
 
+@pytest.mark.parametrize("S,N,behind", [(64, 4500, 5), (65, 4500, 0), (300, 6000, 3), (1, 4200, 9), (63, 4301, 1)])
+def test_append_of_many_tokens_of_many_sequences(torch, S, N, behind):  # noqa: F811
+    """Waves whose tokens belong to several sequences, empty ones among them: as many as a wave has lanes, and more."""
+    from chunk_gated_delta_carve_amd import paged_append_fp4, paged_read_fp4
+    page, Hk, d = 8, 1, 64
+    rng = np.random.default_rng(S)
+    share = rng.random(S) ** 4 * (rng.random(S) < 0.6)
+    share[S // 2] = 0.2
+    n = np.floor(share / share.sum() * N).astype(int)
+    n[np.argmax(n)] += N - n.sum()
+    kv = [int(x + rng.integers(0, 30)) for x in n]
+    cu, lens, table, pages = ragged(torch, 16, S, list(n), kv, page)
+    parts = cache4(torch, "heads", pages, page, Hk, d, 99)
+    before = [u8(t).copy() for t in parts]
+    k, v = (rand(torch, 105 + i, (N + behind, Hk, d), "bf16", 1.5) for i in range(2))
+    paged_append_fp4(k, v, *parts, ints(torch, table), ints(torch, lens), ints(torch, cu))
+    at = [(s, int(lens[s]) - n[s] + i) for s in range(S) for i in range(n[s])]
+    page_no, off = np.array([table[s, p // page] for s, p in at]), np.array([p % page for _, p in at])
+    for (codes, scale), x, (c0, s0) in zip((parts[:2], parts[2:]), (k, v), (before[:2], before[2:])):
+        c0[page_no, off], s0[page_no, off] = orc.encode(f64(x[:N]))
+        assert np.array_equal(u8(codes), c0) and np.array_equal(u8(scale), s0)
+    got = paged_read_fp4(*parts, tensor(torch, page_no * page + off))
+    assert all(np.array_equal(f64(a), orc.decode(*orc.encode(f64(x[:N])))) for a, x in zip(got, (k, v)))
+
+
 @pytest.mark.parametrize("dtype,Hq,Hk,d,N", [("bf16", 4, 2, 64, 9001), ("f32", 12, 4, 64, 2501), ("bf16", 16, 16, 128, 3001)])
 def test_append_in_one_call_or_two(torch, dtype, Hq, Hk, d, N):  # noqa: F811
     """Norm and rotation on the way of many tokens, some of them behind the last sequence."""
