@@ -196,11 +196,24 @@ namespace {
 // 64 of 1000 18.1 and 24.5, of 2000 29 and 36, of 200 to 8192 87 and 61.
 constexpr int kWhole = 8;
 
+// Rows (tokens x grouped heads) per sequence on average up to which the row kernel is taken:
+// a 16-row tile of it opens every block anew, but deals single tokens and chunks evenly
+// and leaves no tile half empty. Row and tile kernels a call, heads of 128, 16 on 16, 8 times
+// 40 tokens over 3000 to 6000 keys 52 and 171 us, 100 times 80 over 200 to 400 keys 103 and 133,
+// 160 tokens 186 and 136; 16 on 4, 2 times 40 over 6000 to 12000 keys 31 and 33, 80 tokens 47
+// and 40, 63 single tokens and a chunk of 256 over 200 to 8192 keys 76 and 353, of 2048 324 and
+// 362. Heads of 64, 12 on 12, 28 times 40 tokens over 750 to 1500 keys 26 and 45, 100 times 40
+// over 200 to 400 keys 34 and 33, 80 tokens 57 and 35; 8 times 80 over 3000 to 6000 keys 47 and
+// 48, 160 tokens 79 and 71.
+struct Rows16 { int few_keys, many_keys; };
+constexpr Rows16 kRows128{128, 128}, kRows64{48, 80};
+
 Plan plan_of(const carve_paged_config* c) {
   const bool f32 = c->dtype == CARVE_F32;
   const int wide = f32 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<carve::bf16, 128>::PER_CU;
   const int slim = f32 ? carve::RowsFp4<float, 64>::PER_CU : carve::RowsFp4<carve::bf16, 64>::PER_CU;
-  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, kWhole, 32, 16, 2048});
+  const Rows16 rows = c->d == 128 ? kRows128 : kRows64;
+  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, kWhole, rows.few_keys, rows.many_keys, 2048});
 }
 
 template <typename E, int D>
