@@ -209,11 +209,9 @@ struct Rows16 { int few_keys, many_keys; };
 constexpr Rows16 kRows128{128, 128}, kRows64{48, 80};
 
 Plan plan_of(const carve_paged_config* c) {
-  const bool f32 = c->dtype == CARVE_F32;
-  const int wide = f32 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<carve::bf16, 128>::PER_CU;
-  const int slim = f32 ? carve::RowsFp4<float, 64>::PER_CU : carve::RowsFp4<carve::bf16, 64>::PER_CU;
+  const int per_cu = c->d == 128 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<float, 64>::PER_CU;   // of bf16 too
   const Rows16 rows = c->d == 128 ? kRows128 : kRows64;
-  return plan_attention(c, {c->d == 128 ? wide : slim, carve::kStart, kWhole, rows.few_keys, rows.many_keys, 2048});
+  return plan_attention(c, {per_cu, carve::kStart, kWhole, rows.few_keys, rows.many_keys, 2048});
 }
 
 template <typename E, int D>

@@ -69,7 +69,9 @@ struct Fp4Entries {
 template <typename E, int D>
 struct RowsFp4 {
   static constexpr int BM = 16, KT = 32, BN = 4 * KT;                            // as RowsLayout
-  static constexpr int PER_CU = (D == 128 ? 3 : 4) - (sizeof(E) == 4);
+  // workgroups of a CU; one fewer in fp32 would spare a register of d = 128, and took 92 us for
+  // 77 (50 sequences of 38 to 75 tokens over 385 to 770 keys, 16 heads on 4 of 128), at d = 64 48 for 41
+  static constexpr int PER_CU = D == 128 ? 3 : 4;
   static constexpr int NI = D / 32;                                              // products per block of 16 keys
   static constexpr int NQ = sizeof(E) == 2 ? 1 : 3, NP = sizeof(E) == 2 ? 2 : 3; // parts of q and of the weights
   static constexpr int VLD = 2 * D + 32, OLD = D + 4;
