@@ -211,7 +211,10 @@ constexpr Rows16 kRows128{128, 128}, kRows64{48, 80};
 Plan plan_of(const carve_paged_config* c) {
   const int per_cu = c->d == 128 ? carve::RowsFp4<float, 128>::PER_CU : carve::RowsFp4<float, 64>::PER_CU;   // of bf16 too
   const Rows16 rows = c->d == 128 ? kRows128 : kRows64;
-  return plan_attention(c, {per_cu, carve::kStart, kWhole, rows.few_keys, rows.many_keys, 2048});
+  const Plan p = plan_attention(c, {per_cu, carve::kStart, kWhole, rows.few_keys, rows.many_keys, 2048});
+  if (p.most <= kMaxInt) return p;
+  // more blocks than the row kernel counts: in bf16 the tile kernels take any number
+  return plan_attention(c, {per_cu, carve::kStart, kWhole, 0, 0, 2048});
 }
 
 template <typename E, int D>

@@ -220,6 +220,16 @@ def assign(L, ptr=(), **kw):
     return L.carve_paged_assign(ctypes.byref(_lib.CarveAssignConfig(**base)), *ptrs(ASSIGN, dict(ptr)), None)
 
 
+def test_more_blocks_than_the_row_kernel_counts(L):  # noqa: F811
+    """Few rows a sequence under a table of 2^23 keys each: the tile kernels take them, fp32 is refused."""
+    need = ctypes.c_int64()
+    for dtype, code in ((_lib.CARVE_BF16, _lib.CARVE_OK), (_lib.CARVE_F32, _lib.CARVE_EUNSUPPORTED)):
+        c = fp4_cfg(N=8192, S=256, Hq=128, Hk=32, d=128, width=1 << 19, pages=1 << 19, dtype=dtype)
+        assert L.carve_paged_workspace_fp4(ctypes.byref(c), ctypes.byref(need)) == code
+    c = fp4_cfg(N=8192, S=256, Hq=128, Hk=32, d=128, width=1 << 12, pages=1 << 12)
+    assert L.carve_paged_workspace_fp4(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_OK and need.value > 0
+
+
 def test_assign_refused(L):  # noqa: F811
     at = {n: FAKE + i * 64 * MB for i, n in enumerate(ASSIGN)}
     assert L.carve_paged_assign(None, *ptrs(ASSIGN, {}), None) == _lib.CARVE_EINVAL

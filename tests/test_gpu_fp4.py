@@ -366,6 +366,31 @@ def test_ragged_contexts_dealt_to_workgroups(torch, case):  # noqa: F811
     check_attention(torch, out, lse, q, kf, vf, table, lens, cu, d ** -0.5, window, dtype)
 
 
+CHUNKS = [
+    # dtype, Hq, Hk, d, page, n, kv, window: several 16-row tiles to a sequence, and batches of single tokens with a chunk
+    ("bf16", 8, 2, 128, 16, [32, 1, 17, 9], [3000, 2, 17, 800], 0), ("bf16", 4, 4, 128, 64, [100, 128], [100, 2222], 150),
+    ("bf16", 16, 2, 128, 8, [15, 16], [2500, 90], 0), ("bf16", 4, 4, 64, 16, [48, 30, 33], [48, 1900, 333], 0),
+    ("bf16", 4, 4, 64, 16, [79], [5000], 1111), ("bf16", 3, 1, 64, 32, [1] * 30 + [200], [700, 1, 33] * 10 + [900], 0),
+    ("bf16", 4, 1, 128, 16, [300] + [1] * 20, [300] + [2100] * 20, 0), ("f32", 4, 2, 128, 16, [70, 2], [1300, 2], 0),
+    ("f32", 3, 3, 64, 4, [99, 1, 17], [99, 400, 1700], 64),
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=[str(i) for i in range(len(CHUNKS))])
+def test_chunks_of_few_rows(torch, case):  # noqa: F811
+    from chunk_gated_delta_carve_amd import paged_attention_fp4
+    dtype, Hq, Hk, d, page, n, kv, window = case
+    say("case", case)
+    cu, lens, table, pages = ragged(torch, 37, len(n), n, kv, page)
+    parts = cache4(torch, "heads", pages, page, Hk, d, 137)
+    q = rand(torch, 138, (sum(n), Hq, d), dtype)
+    args = ints(torch, table), ints(torch, lens), ints(torch, cu)
+    out, lse = paged_attention_fp4(q, *parts, *args, window=window, return_lse=True)
+    kf, vf = (tensor(torch, x) for x in values(parts))
+    check_attention(torch, out, lse, q, kf, vf, table, lens, cu, d ** -0.5, window, dtype)
+    assert torch.equal(out, paged_attention_fp4(q, *parts, *args, window=window))
+
+
 @pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("bf16", 64, 64), ("f32", 64, 16)])
 def test_long_stretches(torch, dtype, d, page):  # noqa: F811
     """More blocks to a workgroup than a lane's pages last for: each sequence has the bits of its first keys alone only
