@@ -376,8 +376,15 @@ CHUNKS = [
 ]
 
 
+CHUNKS += [  # and of many rows, in pages of few tokens and of many
+    ("bf16", 16, 16, 128, 2, [700, 1400], [900, 1400], 0), ("bf16", 16, 16, 128, 16, [1400, 3, 800], [1500, 3000, 800], 300),
+    ("bf16", 4, 2, 128, 4, [200, 255], [1333, 255], 0), ("bf16", 4, 2, 64, 2, [300, 77], [500, 77], 0),
+    ("bf16", 12, 4, 64, 1, [222], [300], 100), ("bf16", 2, 2, 64, 128, [600, 129, 1], [600, 2500, 64], 0),
+]
+
+
 @pytest.mark.parametrize("case", CHUNKS, ids=[str(i) for i in range(len(CHUNKS))])
-def test_chunks_of_few_rows(torch, case):  # noqa: F811
+def test_chunks(torch, case):  # noqa: F811
     from chunk_gated_delta_carve_amd import paged_attention_fp4
     dtype, Hq, Hk, d, page, n, kv, window = case
     say("case", case)
