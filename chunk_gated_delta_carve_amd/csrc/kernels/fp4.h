@@ -102,6 +102,10 @@ struct Fp4AppendArgs {
   Fp4Strides k, v;                     // of the scales
 };
 
+// Where a new token goes: its position and its entry in the cache, page -1 where it has none.
+struct TokenPlace { int64_t pos, page, off; };
+constexpr int64_t kNoToken = INT64_MIN;             // position of a token behind the last sequence
+
 // Where the TOK tokens from n0 on go, lane l for token l % TOK. What tells their sequences
 // is loaded ahead of the wave's rows, since loads come back in the order they went out: up
 // to 64 sequences a lane has one of them, beyond a lane looks its token's up.

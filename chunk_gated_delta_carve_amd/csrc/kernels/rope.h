@@ -336,26 +336,6 @@ struct AppendArgs {
   float eps;
 };
 
-// Where a new token goes: its position and its entry in the cache, page -1 where it
-// has none.
-struct TokenPlace { int64_t pos, page, off; };
-constexpr int64_t kNoToken = INT64_MIN;             // position of a token behind the last sequence
-__device__ __forceinline__ TokenPlace token_place(const AppendArgs& a, int n) {
-  int s = n, i = 0, cnt = 1;
-  if (a.cu) {
-    s = find_sequence(a.cu, a.S, n);
-    if (s < a.S) { i = n - a.cu[s]; cnt = a.cu[s + 1] - a.cu[s]; }
-  }
-  TokenPlace x{kNoToken, -1, 0};
-  if (s >= a.S || i < 0) return x;
-  x.pos = (int64_t)a.kv_lens[s] - cnt + i;
-  const int64_t slot = x.pos >> a.page_shift;
-  if (x.pos >= 0 && slot < a.width) x.page = a.table[s * a.table_row + slot];
-  if (x.page >= a.pages) x.page = -1;
-  x.off = x.pos & ((1 << a.page_shift) - 1);
-  return x;
-}
-
 // One wave per token and 64 U pieces of its rows (q's, k's and v's heads): the
 // sequence, position and page are found once per wave. A token whose position
 // is negative, lies past the block table or falls on a page number outside the
@@ -365,12 +345,22 @@ __global__ __launch_bounds__(256) void paged_append_kernel(AppendArgs a) {
   constexpr int V = Piece<E>::V, LPR = D / V;
   const int n = blockIdx.x * 4 + wave_id();
   if (n >= a.N) return;
-  const TokenPlace at = token_place(a, n);
-  if (at.pos == kNoToken) return;                   // behind the last sequence
+  int s = n, i = 0, cnt = 1;
+  if (a.cu) {
+    s = find_sequence(a.cu, a.S, n);
+    if (s < a.S) { i = n - a.cu[s]; cnt = a.cu[s + 1] - a.cu[s]; }
+  }
+  if (s >= a.S || i < 0) return;                    // behind the last sequence
+  const int64_t pos = (int64_t)a.kv_lens[s] - cnt + i;
+  const int64_t slot = pos >> a.page_shift;
+  int page = -1;
+  if (pos >= 0 && slot < a.width) page = a.table[s * a.table_row + slot];
+  const bool stored = page >= 0 && page < a.pages;
+  const int64_t off = pos & ((1 << a.page_shift) - 1);
   const Turn<E, D> t(a.rot, a.interleaved);
   const int heads = a.Hq + 2 * a.Hk;
   float cs[V], sn[V];
-  t.angles(a.cos, a.sin, a.rot, a.table_len, at.pos, false, cs, sn);
+  t.angles(a.cos, a.sin, a.rot, a.table_len, pos, false, cs, sn);
   const u32x4 wq = weight_piece<E, D>(a.wq, t.c), wk = weight_piece<E, D>(a.wk, t.c);
   u32x4 raw[U];
   int hh[U];
@@ -389,10 +379,10 @@ __global__ __launch_bounds__(256) void paged_append_kernel(AppendArgs a) {
     const u32x4 y = norm_rope_piece<E, D>(raw[u], t, h < a.Hq ? wq : wk, cs, sn, a.norm, a.eps);
     if (h < a.Hq) {
       *reinterpret_cast<u32x4*>(static_cast<E*>(a.qo) + n * a.qo_row + h * D + t.c * V) = y;
-    } else if (h < heads && at.page >= 0) {
+    } else if (h < heads && stored) {
       const bool isk = h < a.Hq + a.Hk;
-      E* dst = isk ? static_cast<E*>(a.kc) + at.page * a.kc_page + at.off * a.kc_tok + (h - a.Hq) * a.kc_head
-                   : static_cast<E*>(a.vc) + at.page * a.vc_page + at.off * a.vc_tok + (h - a.Hq - a.Hk) * a.vc_head;
+      E* dst = isk ? static_cast<E*>(a.kc) + page * a.kc_page + off * a.kc_tok + (h - a.Hq) * a.kc_head
+                   : static_cast<E*>(a.vc) + page * a.vc_page + off * a.vc_tok + (h - a.Hq - a.Hk) * a.vc_head;
       *reinterpret_cast<u32x4*>(dst + t.c * V) = isk ? y : raw[u];
     }
   }
