@@ -108,7 +108,7 @@ hipError_t dispatch_attention(const carve::PagedArgs& a, const Plan& plan, hipSt
                   : launch_tiles<carve::PlainTiles, D, false>(a, plan, s);
   hipLaunchKernelGGL((carve::paged_rows_kernel<E, D>), dim3(a.shares), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess || a.shares == 1 ? e : join_rows<E, D>(a, s);
+  return e != hipSuccess || !a.cuts ? e : join_rows<E, D>(a, s);
 }
 
 }  // namespace

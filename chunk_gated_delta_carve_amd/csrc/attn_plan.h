@@ -24,7 +24,7 @@ constexpr int kWideJoin = 32;          // shares per item from which a workgroup
 struct Choice {
   int per_cu;                // row kernel: workgroups that a CU holds
   int more;                  // and blocks that an item counts for beside its own
-  int whole;                 // and blocks up to which items are dealt undivided, twice that where they fill the CUs
+  int whole;                 // and blocks up to which items are dealt undivided, twice that where they fill the CUs; 0: never
   int rows_short, rows_long, long_keys;
 };
 struct Plan {
@@ -60,7 +60,7 @@ inline Plan plan_attention(const carve_paged_config* c, const Choice& ch) {
   } else {
     // a workgroup per block of keys at most; no item has more blocks than this counts
     const int64_t items = p.tiles * c->Hk, nb = up(keys, BN) + 1, want = (int64_t)kCUs * ch.per_cu;
-    p.whole = nb - 1 <= (items >= kCUs ? 2 : 1) * ch.whole;
+    p.whole = ch.whole > 0 && nb - 1 <= (items >= kCUs ? 2 : 1) * ch.whole;     // (a table without pages has no blocks)
     p.most = items * (p.whole ? 1 : nb + ch.more);
     p.shares = (int)(p.most < want ? p.most : want);
     p.rows = p.shares > 1 && !p.whole ? 2 * (int64_t)p.shares * BM : 0;

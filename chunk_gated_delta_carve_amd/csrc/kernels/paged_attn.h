@@ -507,7 +507,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
   int* cut = a.cuts + blockIdx.x * kCutInts;
-  if (threadIdx.x == 0 && a.shares > 1) cut[2] = 0;
+  if (threadIdx.x == 0 && a.cuts) cut[2] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);
   const int end_block = plan.start(blockIdx.x + 1);

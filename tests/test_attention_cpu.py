@@ -458,3 +458,20 @@ def test_append_refuses_caches_that_start_alike(L):
     for apart, code in ((0, _lib.CARVE_EINVAL), (112, _lib.CARVE_EINVAL), (-112, _lib.CARVE_EINVAL),
                         (MB, _lib.CARVE_OK)):
         assert append(L, c, k_cache=FAKE + 64 * MB, v_cache=FAKE + 64 * MB + apart) == code, apart
+
+
+@pytest.mark.parametrize("dtype", [_lib.CARVE_BF16, _lib.CARVE_F32])
+@pytest.mark.parametrize("d,n,S", [(64, 1, 4), (128, 1, 7), (64, 3, 4), (128, 5, 2)])
+def test_workspace_over_a_table_without_pages(L, d, n, S, dtype):
+    """A block table of width 0: the row kernel deals one block of an item (16 rows of a key/value head) to a workgroup,
+    each of which has room for two partial results of 16 rows and a note of eight numbers."""
+    need = ctypes.c_int64()
+    step = n == 1
+    c = paged_cfg(N=S * n, S=S, d=d, width=0, flags=_lib.CARVE_PAGED_STEP if step else 0, dtype=dtype)
+    assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_OK
+    G, Hk = 2, 2
+    items = (S if step else -(-S * n * G // 16) + S - 1) * Hk
+    assert need.value == (items * 32 * (d + 2) + items * 8) * 4 > 0
+    c.width = c.table_row = 1                    # one page: an item may begin inside a block, two of them
+    assert L.carve_paged_workspace(ctypes.byref(c), ctypes.byref(need)) == _lib.CARVE_OK
+    assert need.value == 2 * (items * 32 * (d + 2) + items * 8) * 4

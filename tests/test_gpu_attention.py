@@ -1071,3 +1071,24 @@ def test_captured_chunk_follows_the_lengths(torch, dtype, n, Hq, Hk, d, window):
         for i, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)), (turn, kv, i)
         assert torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("dtype,d,Hk,n", [
+    # row kernel, step and ragged; tile kernels of four and of eight waves
+    ("bf16", 64, 2, [1] * 4), ("bf16", 128, 1, [1] * 70), ("f32", 64, 3, [1]), ("f32", 128, 2, [1] * 5),
+    ("bf16", 64, 2, [3, 1, 0, 2]), ("f32", 64, 2, [40, 1]), ("bf16", 64, 2, [150, 60]), ("bf16", 128, 2, [150, 60]),
+    ("bf16", 128, 66, [150, 200])])
+def test_a_table_without_pages(torch, dtype, d, Hk, n):
+    """Width 0, the smallest table there is: nothing is stored, and no row sees a key."""
+    from chunk_gated_delta_carve_amd import paged_append, paged_attention
+    S, N, step = len(n), sum(n), all(x == 1 for x in n)
+    table = torch.empty(S, 0, dtype=torch.int32, device="cuda")
+    lens, cu = ints(torch, [x + 9 for x in n]), None if step else ints(torch, np.concatenate([[0], np.cumsum(n)]))
+    kc, vc = cache(torch, "plain", 2, 16, Hk, d, dtype, 310)
+    q, k, v = (rand(torch, 312 + i, (N, h, d), dtype) for i, h in enumerate((2 * Hk, Hk, Hk)))
+    was = kc.clone(), vc.clone()
+    assert torch.equal(paged_append(k, v, kc, vc, table, lens, cu, q=q), q)
+    assert torch.equal(kc, was[0]) and torch.equal(vc, was[1])
+    out = torch.full_like(q, 3.0)
+    o, lse = paged_attention(q, kc, vc, table, lens, cu, out=out, return_lse=True)
+    assert o is out and not out.any() and torch.isneginf(lse).all()

@@ -957,3 +957,23 @@ def test_refusals(torch):  # noqa: F811
         with pytest.raises(err):
             call()
             say("not refused:", i)
+
+
+@pytest.mark.parametrize("dtype,d,Hk,n", [
+    ("bf16", 64, 2, [1] * 4), ("bf16", 128, 1, [1] * 70), ("f32", 64, 3, [1]), ("f32", 128, 2, [1] * 5),
+    ("bf16", 64, 2, [3, 1, 0, 2]), ("f32", 64, 2, [40, 1]), ("bf16", 64, 2, [150, 60]), ("bf16", 128, 2, [150, 60]),
+    ("bf16", 128, 66, [150, 200])])
+def test_a_table_without_pages(torch, dtype, d, Hk, n):  # noqa: F811
+    """Width 0, in the row kernel and in the tile kernels of four and of eight waves: nothing is stored, no key is seen."""
+    from chunk_gated_delta_carve_amd import paged_append_fp4, paged_attention_fp4
+    S, N, step = len(n), sum(n), all(x == 1 for x in n)
+    table = torch.empty(S, 0, dtype=torch.int32, device="cuda")
+    lens, cu = ints(torch, [x + 9 for x in n]), None if step else ints(torch, np.concatenate([[0], np.cumsum(n)]))
+    parts = cache4(torch, "plain", 2, 16, Hk, d, 310)
+    q, k, v = (rand(torch, 312 + i, (N, h, d), dtype) for i, h in enumerate((2 * Hk, Hk, Hk)))
+    was = [t.clone() for t in parts]
+    assert torch.equal(paged_append_fp4(k, v, *parts, table, lens, cu, q=q), q)
+    assert all(torch.equal(a, b) for a, b in zip(parts, was))
+    out = torch.full_like(q, 3.0)
+    o, lse = paged_attention_fp4(q, *parts, table, lens, cu, out=out, return_lse=True)
+    assert o is out and not out.any() and torch.isneginf(lse).all()
