@@ -431,13 +431,18 @@ __device__ __forceinline__ RowsWork rows_work(const PagedArgs& a, int s, int BM,
   return w;
 }
 
-// n / d for n >= 0, d > 0, neither near 2^31: the quotient of floats is off by one at most
-// where it is below 2^20, and larger ones are left to the exact division.
-__device__ __forceinline__ int quotient(int n, int d) {
-  int q = (int)((float)n * __builtin_amdgcn_rcpf((float)d));
-  if (q > 0xfffff) return n / d;
-  const int r = n - q * d;
+// n / d from a number that is off by one at most. q d may pass 2^31: unsigned.
+__host__ __device__ constexpr int settled_quotient(int q, int n, int d) {
+  const int r = (int)((unsigned)n - (unsigned)q * (unsigned)d);
   return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+static_assert(settled_quotient(768, 0x7fffffff, 2796203) == 767 && settled_quotient(766, 0x7fffffff, 2796203) == 767 &&
+              settled_quotient(2, 0x7fffffff, 0x7fffffff) == 1 && settled_quotient(1, 0, 0x7fffffff) == 0);
+// n / d for n >= 0, d > 0: the quotient of floats is off by one at most where it is below
+// 2^20, and larger ones are left to the exact division.
+__device__ __forceinline__ int quotient(int n, int d) {
+  const float q = (float)n * __builtin_amdgcn_rcpf((float)d);
+  return q >= 0x1p20f ? n / d : settled_quotient((int)q, n, d);
 }
 
 // Prefix sums of the sequences' blocks, a lane per run of sequences; with one
