@@ -418,7 +418,10 @@ int carve_paged_append_fp4(const carve_fp4_config* cfg, const void* k, const voi
  * paged.k_row and paged.v_row apart) from entry slots[n] % page_size of page
  * slots[n] / page_size. A slot outside [0, pages page_size) gives zeros. Either of k
  * and v may be NULL with its codes and scales. Of paged N, Hk, d, page_size, pages,
- * dtype, k_row, v_row and the caches' strides are looked at; N at most 2^26 - 4. */
+ * dtype, k_row, v_row and the caches' strides say what is read; the other fields are
+ * checked as by the calls above, so 0 in them is right, and CARVE_PAGED_STEP with
+ * another S than N is refused. N at most 2^26 - 4, k and v together at most 2^38 - 2^14
+ * bytes (CARVE_EUNSUPPORTED beyond). */
 int carve_paged_read_fp4(const carve_fp4_config* cfg, const uint8_t* k_codes, const uint8_t* k_scales,
                          const uint8_t* v_codes, const uint8_t* v_scales, const int64_t* slots, void* k, void* v,
                          void* stream);

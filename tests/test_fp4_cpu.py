@@ -267,3 +267,14 @@ def test_sizes_past_32_bits_in_python():
         with pytest.raises(ValueError):
             paged_fp4_workspace_bytes(**{**base, n: 2 ** 31})
     assert paged_fp4_workspace_bytes(**base, window=2 ** 40) == paged_fp4_workspace_bytes(**base)
+
+
+def test_what_a_read_is_limited_to(L):  # noqa: F811
+    """The whole configuration has to hold, and the outputs have at most 2^24 - 1 workgroups of 2^14 bytes."""
+    c = fp4_cfg(N=20, S=3, flags=_lib.CARVE_PAGED_STEP, k_row=256, v_row=256)
+    assert read(L, c) == _lib.CARVE_EINVAL
+    far = dict(zip(READ, (FAKE + i * (1 << 42) for i in range(len(READ)))))
+    for d, dtype, Hk, N in ((128, _lib.CARVE_F32, 64, 1 << 22), (128, _lib.CARVE_BF16, 256, 1 << 21)):
+        c = fp4_cfg(N=N, S=0, Hq=0, Hk=Hk, d=d, dtype=dtype, width=0, flags=0, rot=0)
+        assert 2 * N * Hk * d * (4 if dtype == _lib.CARVE_F32 else 2) > 2 ** 38 - 2 ** 14
+        assert read(L, c, **far) == _lib.CARVE_EUNSUPPORTED
