@@ -29,8 +29,8 @@ _U8 = torch.uint8
 def _pack(*values):
     try:
         return _lib.pack_fp4(*values)
-    except struct.error as e:
-        raise ValueError(f"a size past 32 bits: {e}") from None
+    except struct.error as e:            # a size past its bits, or a scale or eps that is no float
+        raise ValueError(f"a value that the configuration does not hold: {e}") from None
 
 
 def paged_fp4_cache(pages, page_size, heads, d, device="cuda"):

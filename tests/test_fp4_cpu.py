@@ -278,3 +278,21 @@ def test_what_a_read_is_limited_to(L):  # noqa: F811
         c = fp4_cfg(N=N, S=0, Hq=0, Hk=Hk, d=d, dtype=dtype, width=0, flags=0, rot=0)
         assert 2 * N * Hk * d * (4 if dtype == _lib.CARVE_F32 else 2) > 2 ** 38 - 2 ** 14
         assert read(L, c, **far) == _lib.CARVE_EUNSUPPORTED
+
+
+def test_values_that_do_not_fit_the_configuration():
+    """Sizes past 32 bits and what is no float are refused, the latter not as a size; a float past fp32's range goes through as infinity, which
+    the library refuses by its own range, as in the calls over the other caches."""
+    from chunk_gated_delta_carve_amd.fp4 import _pack
+    ok = [1] * 13 + [1e-6, 0.125] + [0] * 17
+    c = _lib.CarveFp4Config.from_buffer_copy(_pack(*ok))
+    assert c.paged.scale == 0.125 and c.paged.N == 1
+    for at, name in ((13, "eps"), (14, "scale")):
+        c = _lib.CarveFp4Config.from_buffer_copy(_pack(*ok[:at], 1e300, *ok[at + 1:]))
+        assert getattr(c.paged, name) == getattr(_lib.CarvePagedConfig(**{name: 1e300}), name) == float("inf")
+        for bad in ("x", 10 ** 400):
+            with pytest.raises(ValueError, match="not a float") as e:
+                _pack(*ok[:at], bad, *ok[at + 1:])
+            assert "size" not in str(e.value)
+    with pytest.raises(ValueError):
+        _pack(1 << 31, *ok[1:])
