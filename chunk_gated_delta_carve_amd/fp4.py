@@ -214,7 +214,9 @@ def paged_assign(block_table, kv_lens, new_lens, free_pages, free_count, page_si
     the last token), slots as paged_read_fp4 does (page * page_size + offset; -1 behind the last token and where no page
     is). Requests are served in their order; one that finds the stack empty has -1 in its table, which is counted in
     free_count_out[1], and those tokens are neither stored nor seen. kv_lens_out may be kv_lens, free_count_out
-    free_count. A page that several requests hold must not be in the table of one that has ended."""
+    free_count. A page that several requests hold must not be in the table of one that has ended. Entries past
+    ceil(kv_lens / page_size) are taken for empty: where a length is set back (drafted tokens that were rejected), the
+    pages past it have to be put on the stack first, or they are lost."""
     dev = block_table.device
     if dev.type != "cuda":
         raise ValueError("paged_assign runs on the GPU only; move the inputs to a cuda device")

@@ -452,7 +452,9 @@ int carve_paged_attention_fp4(const carve_fp4_config* cfg, const void* q, const 
  * written (entries past the table's width are not, and take nothing). Where the stack is
  * empty the entry is -1 and free_count_out[1] counts one more; such tokens have no slot
  * and neither are they stored or seen. A page that several requests hold is the caller's
- * to keep out of ended ones.
+ * to keep out of ended ones. Table entries past ceil(old_s / page_size) are taken for
+ * empty and written over: a caller that sets a length back (tokens that were drafted and
+ * rejected) first puts the pages past it on the stack itself, or they are lost.
  *   positions [N]  of token cu[s] + i: old_s + i; 0 behind cu[S]
  *   slots [N]      page page_size + position mod page_size, or -1 without a page and
  *                  behind cu[S]

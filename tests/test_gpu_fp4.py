@@ -977,3 +977,18 @@ def test_a_table_without_pages(torch, dtype, d, Hk, n):  # noqa: F811
     out = torch.full_like(q, 3.0)
     o, lse = paged_attention_fp4(q, *parts, table, lens, cu, out=out, return_lse=True)
     assert o is out and not out.any() and torch.isneginf(lse).all()
+
+
+def test_assign_after_a_length_was_set_back(torch):  # noqa: F811
+    """A request of 40 tokens in pages 3, 4 and 5, set back to 10: what its table holds past them is written over, and is
+    kept where the caller gave it back."""
+    for stack, count, page in (([0, 1, 2, -7, -7, -7], 3, 2), ([0, 1, 2, 5, 4, -7], 5, 4)):
+        tab, free = ints(torch, [[3, 4, 5, -1]]), ints(torch, stack)
+        check_assign(torch, [[3, 4, 5, -1]], [10], [20], stack, [count, 0], 16, 20, None)
+        from chunk_gated_delta_carve_amd import paged_assign
+        cu, lens, pos, slots, left = paged_assign(tab, ints(torch, [10]), ints(torch, [20]), free, ints(torch, [count, 0]),
+                                                  16, 20)
+        assert tab[0].tolist() == [3, page, 5, -1] and lens.tolist() == [30] and left.tolist() == [count - 1, 0]
+        assert slots.tolist() == [3 * 16 + i for i in range(10, 16)] + [page * 16 + i for i in range(14)]
+        kept = set(free[:count - 1].tolist()) | set(tab[0, :2].tolist())
+        assert (kept == {0, 1, 2, 3, 4, 5}) == (count == 5)
