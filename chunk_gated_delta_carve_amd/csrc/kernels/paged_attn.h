@@ -467,8 +467,11 @@ struct RowsPlan {
     return RowsWork{at(own.n0), at(own.cnt), at(own.pos0), at(own.items), at(own.nb)};
   }
 };
-// 2 heads, one token over 40000 keys 10.4 + 4.3 us with the join, 10.7 + 8.0 with a block each;
-// fp32, 5 sequences of up to 37 tokens, 11.9 + 4.2 and 13.0 + 6.3.
+// Few blocks, with the join: one token over 40000 keys of 2 heads 14 us, with a block each 18;
+// fp32, 5 sequences of up to 37 tokens over up to 2047 keys of 4 heads of 64, 16.1 and 19.3. Where
+// the items are many it costs, since they have few parts to join either way: 16 sequences of 2000
+// keys of 4 heads of 128 15.5 and 14.7, 8 of 3000 keys of 12 heads of 64 16.5 and 15.9, fp32 5
+// single tokens over 1500 keys of 4 heads of 64 12.4 and 11.1. The rule does not look at the items.
 constexpr int kFewBlocks = 3, kRowsCUs = 256;
 template <int MORE = 0>
 __device__ __forceinline__ RowsPlan rows_plan(const PagedArgs& a, int BM, int BN) {
