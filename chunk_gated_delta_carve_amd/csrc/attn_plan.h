@@ -59,7 +59,8 @@ inline Plan plan_attention(const carve_paged_config* c, const Choice& ch) {
     p.rows = p.splits > 1 ? (int64_t)p.splits * c->N * c->Hq : 0;
   } else {
     // a workgroup per block of keys at most; no item has more blocks than this counts
-    const int64_t items = p.tiles * c->Hk, nb = up(keys, BN) + 1, want = (int64_t)kCUs * ch.per_cu;
+    const int64_t items = p.tiles * c->Hk, nb = up(keys, BN) + 1;
+    const int64_t want = std::min(kCUs * ch.per_cu, carve::kMostNotes);
     p.whole = ch.whole > 0 && nb - 1 <= (items >= kCUs ? 2 : 1) * ch.whole;     // (a table without pages has no blocks)
     p.most = items * (p.whole ? 1 : nb + ch.more);
     p.shares = (int)(p.most < want ? p.most : want);
@@ -121,7 +122,7 @@ hipError_t join_rows(const carve::PagedArgs& a, hipStream_t s) {
   const int rows = (int)(most < BM ? most : BM);
   const int64_t items = a.Hk * (up((int64_t)a.N * a.G, BM) > a.S ? up((int64_t)a.N * a.G, BM) : a.S);
   if (a.shares >= kWideJoin * items)
-    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(up(a.shares, carve::kJoinNotes), rows), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 4>), dim3(a.tiles * a.Hk, rows), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((carve::paged_rows_combine_kernel<E, D, 1>), dim3(a.shares, up(rows, 4)), dim3(256), 0, s, a);
   return hipGetLastError();

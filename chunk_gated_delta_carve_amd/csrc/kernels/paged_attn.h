@@ -220,12 +220,21 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int s, int j) {   // 
 
 // What is noted down about an item (rows of one key/value head) whose keys several
 // workgroups share: first token of the sequence, first row, rows (0: no such item),
-// head, and the number of workgroups that hold parts of it. The row kernel's
-// workgroups note the item that starts in their stretch and goes on behind it, the
-// tile kernels' first share of every tile notes that.
+// head, and the number of workgroups that hold parts of it. The tile kernels' first
+// share of every tile notes that. The row kernel's workgroups note the item that starts
+// in their stretch and goes on behind it, the rows of all notes next to each other, since
+// the join looks through them, and the rest behind.
 constexpr int kCutInts = 8;                         // of workspace
 __device__ __forceinline__ void note_cut(int* cut, const AttnTile& x, int h, int count) {
   cut[0] = x.n0; cut[1] = x.row0; cut[2] = x.rows; cut[3] = h; cut[4] = count;
+}
+struct Note { int n0, row0, h, count; };
+__device__ __forceinline__ Note* note_of(const PagedArgs& a, int w) {
+  return reinterpret_cast<Note*>(a.cuts + a.shares) + w;
+}
+__device__ __forceinline__ void note_item(const PagedArgs& a, const AttnTile& x, int h, int count) {
+  a.cuts[blockIdx.x] = x.rows;
+  *note_of(a, blockIdx.x) = {x.n0, x.row0, h, count};
 }
 
 __device__ __forceinline__ float log_sum(const PagedArgs& a, float m, float l) {
@@ -514,8 +523,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   __shared__ int bad[16];
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan(a, LY::BM, LY::BN);
-  int* cut = a.cuts + blockIdx.x * kCutInts;
-  if (threadIdx.x == 0 && a.cuts) cut[2] = 0;
+  if (threadIdx.x == 0 && a.cuts) a.cuts[blockIdx.x] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);
   const int end_block = plan.start(blockIdx.x + 1);
@@ -538,7 +546,7 @@ __global__ __launch_bounds__(256, (RowsLayout<E, D>::PER_CU)) void paged_rows_ke
   const int64_t k0_ = (int64_t)(x.lo / LY::BN + blk) * LY::BN, k1_ = k0_ + (int64_t)take * LY::BN;
   const int k0 = k0_ > x.lo ? (int)k0_ : x.lo, k1 = k1_ < x.hi ? (int)k1_ : x.hi;
   const RowOut<E, D> ro{a, h, take == w.nb, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
-  if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_cut(cut, x, h, plan.share(last_block) - blockIdx.x + 1);
+  if (threadIdx.x == 0 && blk == 0 && take < w.nb) note_item(a, x, h, plan.share(last_block) - blockIdx.x + 1);
 
   // this lane's row and its queries, in the pieces the keys come in
   const int row = x.row0 + (c < x.rows ? c : x.rows - 1);
@@ -1433,34 +1441,67 @@ __global__ __launch_bounds__(256) void paged_tile_combine_kernel(PagedArgs a) {
 // stretch and go on behind it: what that workgroup noted down. A wave per row (d = 64,
 // fp32, 768 workgroups: 5.2 us, 9.5 with WAVES = 4), or a workgroup per row where few items
 // leave many shares to each (d = 128, 128 shares: 6.1 us, 12 in a wave). Then few of the
-// notes hold anything, and a workgroup looks at kJoinNotes of them: leaving at once costs
-// a workgroup its start all the same (768 notes of 8 rows, 8 items: 6.3 us, 4.3 so).
-constexpr int kJoinNotes = 8;
+// notes hold anything, and workgroup b looks at all of them for the b-th that does: one for
+// every note costs each its start (768 notes of 8 rows, 8 items: 6.3 us, 4.4 so), and one for
+// eight neighbouring notes joins those of short items in turn (seven contexts of 500 keys and
+// one of 65536, 16 on 2 heads of 128 in bf16: 10.9 us, 9.6 with one for every note, 6.6 so).
+constexpr int kMostNotes = 1024;
 
-__device__ __forceinline__ int64_t noted_row(const PagedArgs& a, const int* cut, int r) {
-  const int row = cut[1] + r, i = a.by_g.div(row);
-  return (int64_t)(cut[0] + i) * a.Hq + cut[3] * a.G + (row - i * a.G);
+// x of the lane N below in the row of 16, 0 where there is none.
+template <int N>
+__device__ __forceinline__ int dpp_up(int x) { return __builtin_amdgcn_update_dpp(0, x, 0x110 + N, 0xf, 0xf, false); }
+
+__device__ __forceinline__ int64_t noted_row(const PagedArgs& a, const Note& x, int r) {
+  const int row = x.row0 + r, i = a.by_g.div(row);
+  return (int64_t)(x.n0 + i) * a.Hq + x.h * a.G + (row - i * a.G);
 }
 
 template <typename E, int D, int WAVES>
 __global__ __launch_bounds__(256) void paged_rows_combine_kernel(PagedArgs a) {
   using LY = RowsLayout<E, D>;
-  auto join = [&](int64_t w, int r) {
-    const int* cut = a.cuts + w * kCutInts;
-    join_shares<E, D, WAVES>(a, noted_row(a, cut, r), (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r,
-                             2 * LY::BM, cut[4]);
+  auto join = [&](const Note& x, int64_t w, int r) {
+    join_shares<E, D, WAVES>(a, noted_row(a, x, r), (2 * w + 1) * LY::BM + r, 2 * (w + 1) * LY::BM + r, 2 * LY::BM,
+                             x.count);
   };
   if constexpr (WAVES > 1) {
-    const int first = blockIdx.x * kJoinNotes, mine = first + lane_id();
-    const bool look = lane_id() < kJoinNotes && mine < a.shares;
-    unsigned todo = (unsigned)__ballot(look && (int)blockIdx.y < a.cuts[(look ? mine : 0) * (int64_t)kCutInts + 2]);
-    for (; todo; todo &= todo - 1) {
-      join(first + __builtin_ctz(todo), blockIdx.y);
-      if (todo & (todo - 1)) __syncthreads();       // the next one's sums take the same LDS
+    __shared__ unsigned long long noted[kMostNotes / 64];
+    constexpr int U = kMostNotes / 64 / WAVES;
+    const int r = blockIdx.y;
+    int rows[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = (u * WAVES + wave_id()) * 64 + lane_id();
+      rows[u] = a.cuts[w < a.shares ? w : 0];
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = u * WAVES + wave_id();
+      const unsigned long long here = __ballot(r < rows[u] && i * 64 + lane_id() < a.shares);
+      if (lane_id() == 0) noted[i] = here;
+    }
+    __syncthreads();
+    // 16 words, one to each lane of a row: the word and the place in it of note blockIdx.x
+    static_assert(kMostNotes == 16 * 64);
+    const unsigned long long word = noted[lane_id() % 16];
+    const int own = __popcll(word);
+    int upto = own;
+    upto += dpp_up<1>(upto);
+    upto += dpp_up<2>(upto);
+    upto += dpp_up<4>(upto);
+    upto += dpp_up<8>(upto);
+    const int i = __popcll(__ballot(lane_id() < 16 && upto <= (int)blockIdx.x));
+    if (i == 16) return;                            // (as many workgroups as items, and an item is noted once at most)
+    unsigned long long here = (unsigned)__builtin_amdgcn_readlane((int)word, i) |
+                              (unsigned long long)(unsigned)__builtin_amdgcn_readlane((int)(word >> 32), i) << 32;
+    for (int skip = blockIdx.x - __builtin_amdgcn_readlane(upto - own, i); skip > 0; --skip) here &= here - 1;
+    const int w = i * 64 + __builtin_ctzll(here);
+    join(*note_of(a, w), w, r);
   } else {
     const int r = blockIdx.y * 4 + wave_id();
-    if (r < a.cuts[blockIdx.x * (int64_t)kCutInts + 2]) join(blockIdx.x, r);
+    const int rows = a.cuts[blockIdx.x];
+    Note x = *note_of(a, blockIdx.x);
+    asm volatile("" : "+s"(x.n0), "+s"(x.row0), "+s"(x.h), "+s"(x.count));     // loaded beside the rows, not behind the branch
+    if (r < rows) join(x, blockIdx.x, r);
   }
 }
 

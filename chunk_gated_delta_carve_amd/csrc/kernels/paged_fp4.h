@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   __shared__ int bad[16];
   const int lane = lane_id(), wave = wave_id(), c = lane & 15, g = lane >> 4;
   const RowsPlan plan = rows_plan<kStart>(a, LY::BM, LY::BN);
-  if (threadIdx.x == 0 && a.po) a.cuts[blockIdx.x * kCutInts + 2] = 0;
+  if (threadIdx.x == 0 && a.po) a.cuts[blockIdx.x] = 0;
   if ((int)blockIdx.x >= plan.shares) return;
   int at_block = plan.start(blockIdx.x);            // in blocks of the plan, kStart more per item than it has
   const int end_block = plan.start(blockIdx.x + 1);
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256, (RowsFp4<E, D>::PER_CU)) void paged_rows_fp4_k
   const Fp4Args& z = args_again<Fp4Args>();
   const RowOut<E, D> ro{z, h, whole, (int64_t)(2 * blockIdx.x + (blk > 0 ? 0 : 1)) * LY::BM, 1};
   if (threadIdx.x == 0 && blk == 0 && !whole)
-    note_cut(z.cuts + blockIdx.x * kCutInts, x, h, plan.share(last_block) - blockIdx.x + 1);
+    note_item(z, x, h, plan.share(last_block) - blockIdx.x + 1);
   l = sum_halves(sum_row_pairs(l));
   if (threadIdx.x < 16) bad[threadIdx.x] = 0;
   if (g == 0) { ms[wave][c] = m; ls[wave][c] = l; }

@@ -1092,3 +1092,22 @@ def test_a_table_without_pages(torch, dtype, d, Hk, n):
     out = torch.full_like(q, 3.0)
     o, lse = paged_attention(q, kc, vc, table, lens, cu, out=out, return_lse=True)
     assert o is out and not out.any() and torch.isneginf(lse).all()
+
+
+SIDE_BY_SIDE = [[300] * 7 + [20000], [20000] + [300] * 7, [5000] * 8, [9000, 200, 200, 200, 9000, 200, 200, 11000],
+                [40000, 150]]
+
+
+@pytest.mark.parametrize("kv", SIDE_BY_SIDE, ids=[str(i) for i in range(len(SIDE_BY_SIDE))])
+@pytest.mark.parametrize("dtype,Hq,Hk,d", [("bf16", 16, 2, 128), ("f32", 4, 2, 64)])
+def test_short_and_long_contexts_joined_in_one_call(torch, dtype, Hq, Hk, d, kv):
+    """Few items with many shares, whose notes lie next to each other, evenly apart, or both."""
+    from chunk_gated_delta_carve_amd import paged_attention
+    S = len(kv)
+    cu, lens, table, pages = ragged(torch, 41, S, [1] * S, kv, 64)
+    kc, vc = cache(torch, "plain", pages, 64, Hk, d, dtype, 320)
+    q = rand(torch, 322, (S, Hq, d), dtype)
+    args = q, kc, vc, ints(torch, table), ints(torch, lens)
+    out, lse = paged_attention(*args, return_lse=True)
+    check_attention(torch, out, lse, q, kc, vc, table, lens, cu, d ** -0.5, 0, dtype)
+    assert torch.equal(out, paged_attention(*args))

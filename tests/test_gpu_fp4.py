@@ -992,3 +992,21 @@ def test_assign_after_a_length_was_set_back(torch):  # noqa: F811
         assert slots.tolist() == [3 * 16 + i for i in range(10, 16)] + [page * 16 + i for i in range(14)]
         kept = set(free[:count - 1].tolist()) | set(tab[0, :2].tolist())
         assert (kept == {0, 1, 2, 3, 4, 5}) == (count == 5)
+
+
+from test_gpu_attention import SIDE_BY_SIDE  # noqa: E402
+
+
+@pytest.mark.parametrize("kv", SIDE_BY_SIDE, ids=[str(i) for i in range(len(SIDE_BY_SIDE))])
+@pytest.mark.parametrize("dtype,Hq,Hk,d", [("bf16", 16, 2, 128), ("f32", 4, 2, 64)])
+def test_short_and_long_contexts_joined_in_one_call(torch, dtype, Hq, Hk, d, kv):  # noqa: F811
+    from chunk_gated_delta_carve_amd import paged_attention_fp4
+    S = len(kv)
+    cu, lens, table, pages = ragged(torch, 41, S, [1] * S, kv, 64)
+    parts = cache4(torch, "heads", pages, 64, Hk, d, 320)
+    q = rand(torch, 322, (S, Hq, d), dtype)
+    args = q, *parts, ints(torch, table), ints(torch, lens)
+    out, lse = paged_attention_fp4(*args, return_lse=True)
+    kf, vf = (tensor(torch, x) for x in values(parts))
+    check_attention(torch, out, lse, q, kf, vf, table, lens, cu, d ** -0.5, 0, dtype)
+    assert torch.equal(out, paged_attention_fp4(*args))
