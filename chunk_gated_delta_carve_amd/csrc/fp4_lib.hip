@@ -192,8 +192,9 @@ namespace {
 // there are items for every CU): splitting it needs a second launch to join the parts.
 // Undivided and divided, kernel time of all launches, bf16: 4 heads of 128, 16 sequences
 // of 1000 keys 13.6 and 12.5 us (and 3 us of the host's for a launch, which a captured graph
-// does not pay: there the second is better), 2000 keys 21.6 and 15.0; 64 of 500 10.6 and 15.9, of 2000 23.2 and 24.6, of 4000 42 and 36; 12 heads of 64,
-// 64 of 1000 18.1 and 24.5, of 2000 29 and 36, of 200 to 8192 87 and 61.
+// does not pay: there the second is better), 2000 keys 21.6 and 15.0; 64 of 500 10.6 and
+// 15.9, of 2000 23.2 and 24.6, of 4000 42 and 36; 12 heads of 64, 64 of 1000 18.1 and 24.5, of
+// 2000 29 and 36, of 200 to 8192 87 and 61.
 // The keys are those that the table holds: under a wide one short contexts are divided too.
 constexpr int kWhole = 8;
 
